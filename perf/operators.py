@@ -139,7 +139,7 @@ def prepare(case, seed):
 # ---- plain forms ---------------------------------------------------------------------------
 def _quantize(x, amax):
     """Codes of x with the scale amax / 448, shaped to broadcast against x."""
-    s = amax / E4M3_MAX
+    s = amax / torch.full_like(amax, E4M3_MAX)  # by a tensor: a plain number would be a product with 1/448
     t = torch.where(s > 0, x / s, torch.zeros_like(x))
     return t.clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn), s
 
@@ -282,7 +282,7 @@ def _nearest_e4m3(t):
 
 
 def _codes64(x, amax):
-    s = amax / E4M3_MAX
+    s = amax / torch.full_like(amax, E4M3_MAX)
     held = s.float().double()  # the scale as it is stored
     # the quotient is an fp32 one by definition: quotients of bf16 values often lie on a border between two codes
     t = torch.where(held > 0, x / held, torch.zeros_like(x)).float().double()

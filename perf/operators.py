@@ -208,12 +208,12 @@ def _plain(state):
     g, u = gu[:, :d], gu[:, d:]
     sigma = 1.0 / (1.0 + torch.exp(-g))
     if op == "swiglu":
-        q, s = _quantize_rows((g * sigma * u).to(torch.bfloat16))
+        q, s = _quantize_rows(g * sigma * u)
         return {"q": q, "scales": s}
     dy = state["dy"].float()
-    dgu = torch.cat([dy * u * (sigma * (1.0 + g * (1.0 - sigma))), dy * (g * sigma)], 1).to(torch.bfloat16)
+    dgu = torch.cat([dy * u * (sigma * (1.0 + g * (1.0 - sigma))), dy * (g * sigma)], 1)
     q, s = _quantize_rows(dgu)
-    return {"dgu": dgu, "q": q, "scales": s}
+    return {"dgu": dgu.to(torch.bfloat16), "q": q, "scales": s}
 
 
 # ---- the framework's calls -----------------------------------------------------------------
@@ -332,10 +332,10 @@ def exact(case, seed):
     g, u = gu.chunk(2, 1)
     silu = g * torch.sigmoid(g)
     if op == "swiglu":
-        q, s = _codes64_of_rows((silu * u).to(torch.bfloat16).double())
+        q, s = _codes64_of_rows(silu * u)
         return {"q": q, "scales": s}
     dy = state["dy"].double()
     slope = torch.sigmoid(g) + silu * torch.sigmoid(-g)
     dgu = torch.cat([dy * u * slope, dy * silu], 1)
-    q, s = _codes64_of_rows(dgu.to(torch.bfloat16).double())
+    q, s = _codes64_of_rows(dgu)
     return {"dgu": dgu, "q": q, "scales": s}

@@ -2,7 +2,7 @@
 
 Every function here checks torch dtypes, shapes, contiguity and devices, then
 passes raw device pointers and the current HIP stream to the C ABI declared in
-include/fp8bs.h.  No arithmetic of the method happens in Python; if the library
+include/fp8bs.h and include/fp8bs_g128.h.  No arithmetic of the method happens in Python; if the library
 is missing the call raises ``Fp8bsError`` - there is no fallback path.
 """
 
@@ -65,6 +65,20 @@ def load_library() -> ctypes.CDLL:
         lib.fp8bs_quantize_e8m0.restype = ctypes.c_int
         lib.fp8bs_gemm_e8m0_nt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
         lib.fp8bs_gemm_e8m0_nt.restype = ctypes.c_int
+        lib.fp8bs_quantize_tg128.argtypes = [vp, i64, i64, vp, vp, vp]
+        lib.fp8bs_quantize_tg128.restype = ctypes.c_int
+        lib.fp8bs_quantize_b128.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, vp]
+        lib.fp8bs_quantize_b128.restype = ctypes.c_int
+        lib.fp8bs_gemm_tg128_nt.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
+        lib.fp8bs_gemm_tg128_nt.restype = ctypes.c_int
+        lib.fp8bs_grouped_gemm_tg128_nt.argtypes = [vp, vp, vp, vp, vp, i32, vp, i64, i64, i64, vp]
+        lib.fp8bs_grouped_gemm_tg128_nt.restype = ctypes.c_int
+        lib.fp8bs_grouped_wgrad.argtypes = [vp, vp, vp, i32, vp, i32, i64, i64, i64, vp]
+        lib.fp8bs_grouped_wgrad.restype = ctypes.c_int
+        lib.fp8bs_swiglu_quantize_tg128.argtypes = [vp, i64, i64, vp, vp, vp, vp]
+        lib.fp8bs_swiglu_quantize_tg128.restype = ctypes.c_int
+        lib.fp8bs_swiglu_backward_quantize_tg128.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
+        lib.fp8bs_swiglu_backward_quantize_tg128.restype = ctypes.c_int
         lib.fp8bs_status_str.argtypes = [ctypes.c_int]
         lib.fp8bs_status_str.restype = ctypes.c_char_p
         _lib = lib
@@ -150,6 +164,36 @@ def grouped_gemm_nt_raw(a_ptr, sa_ptr, bt_ptr, sbt_ptr, off_ptr, G, c_ptr, M_tot
 
 def grouped_gemm_raw(a_ptr, sa_ptr, b_ptr, sb_ptr, off_ptr, G, c_ptr, M_total, N, K, stream=None) -> int:
     return load_library().fp8bs_grouped_gemm(a_ptr, sa_ptr, b_ptr, sb_ptr, off_ptr, G, c_ptr, M_total, N, K, stream)
+
+
+def quantize_tg128_raw(x_ptr, rows, cols, q_ptr, s_ptr, stream=None) -> int:
+    return load_library().fp8bs_quantize_tg128(x_ptr, rows, cols, q_ptr, s_ptr, stream)
+
+
+def quantize_b128_raw(x_ptr, G, rows, cols, q_ptr, s_ptr, qt_ptr, st_ptr, stream=None) -> int:
+    return load_library().fp8bs_quantize_b128(x_ptr, G, rows, cols, q_ptr, s_ptr, qt_ptr, st_ptr, stream)
+
+
+def gemm_tg128_nt_raw(a_ptr, sa_ptr, bt_ptr, sbt_ptr, c_ptr, M, N, K, stream=None) -> int:
+    return load_library().fp8bs_gemm_tg128_nt(a_ptr, sa_ptr, bt_ptr, sbt_ptr, c_ptr, M, N, K, stream)
+
+
+def grouped_gemm_tg128_nt_raw(a_ptr, sa_ptr, bt_ptr, sbt_ptr, off_ptr, G, c_ptr, M_total, N, K, stream=None) -> int:
+    return load_library().fp8bs_grouped_gemm_tg128_nt(a_ptr, sa_ptr, bt_ptr, sbt_ptr, off_ptr, G, c_ptr, M_total, N,
+                                                      K, stream)
+
+
+def grouped_wgrad_raw(dy_ptr, x_ptr, off_ptr, G, dw_ptr, accumulate, M_total, N, K, stream=None) -> int:
+    return load_library().fp8bs_grouped_wgrad(dy_ptr, x_ptr, off_ptr, G, dw_ptr, accumulate, M_total, N, K, stream)
+
+
+def swiglu_quantize_tg128_raw(gu_ptr, rows, d, q_ptr, s_ptr, y_ptr, stream=None) -> int:
+    return load_library().fp8bs_swiglu_quantize_tg128(gu_ptr, rows, d, q_ptr, s_ptr, y_ptr, stream)
+
+
+def swiglu_backward_quantize_tg128_raw(gu_ptr, dy_ptr, rows, d, dgu_ptr, q_ptr, s_ptr, y_ptr, stream=None) -> int:
+    return load_library().fp8bs_swiglu_backward_quantize_tg128(gu_ptr, dy_ptr, rows, d, dgu_ptr, q_ptr, s_ptr, y_ptr,
+                                                               stream)
 
 
 # ---- tensor entry points -----------------------------------------------------------------
@@ -395,3 +439,180 @@ def gemm_e8m0_nt(a: torch.Tensor, ea: torch.Tensor, bt: torch.Tensor, ebt: torch
     _same_device(a, ea, bt, ebt, out)
     _check(gemm_e8m0_nt_raw(_ptr(a), _ptr(ea), _ptr(bt), _ptr(ebt), _ptr(out), M, N, K, _stream_ptr(a)))
     return out
+
+
+# ---- scales of 128 values (include/fp8bs_g128.h) -------------------------------------------
+GROUP = 128
+
+
+def _blocks128(n: int) -> int:
+    return (n + GROUP - 1) // GROUP
+
+
+def _call_on(t: torch.Tensor, raw, *args) -> None:
+    """One library call on the current stream of t's device, whichever device is current."""
+    index = t.device.index
+    if index == torch.cuda.current_device():
+        _check(raw(*args, _stream_ptr(t)))
+    else:
+        with torch.cuda.device(index):
+            _check(raw(*args, _stream_ptr(t)))
+
+
+def _output(t: torch.Tensor | None, name: str, shape, dtypes, device) -> torch.Tensor:
+    """The caller's output, checked, or a new one of the first of `dtypes`."""
+    if t is None:
+        return torch.empty(shape, dtype=dtypes[0] if isinstance(dtypes, tuple) else dtypes, device=device)
+    _need(t, name, dtypes, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _need_shape(t: torch.Tensor, name: str, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def quantize_tg128(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """bf16 [R, C] -> (E4M3 codes uint8 [R, C], fp32 scales [R, ceil(C/128)], one per row and 128 columns)."""
+    _need(x, "x", torch.bfloat16, 2)
+    R, C = x.shape
+    q = _output(q, "q", (R, C), E4M3_DTYPES, x.device)
+    scales = _output(scales, "scales", (R, _blocks128(C)), torch.float32, x.device)
+    _same_device(x, q, scales)
+    _call_on(x, quantize_tg128_raw, _ptr(x), R, C, _ptr(q), _ptr(scales))
+    return q, scales
+
+
+def quantize_b128(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                  transposed: bool = False, qt: torch.Tensor | None = None, scales_t: torch.Tensor | None = None):
+    """bf16 weight [R, C] or weights [G, R, C] -> (E4M3 codes uint8 of the same shape, fp32 scales
+    [(G,) ceil(R/128), ceil(C/128)], one per 128x128 block).
+
+    With ``transposed`` (or when ``qt`` and ``scales_t`` are given) also the transposed codes [(G,) C, R]
+    and scales [(G,) ceil(C/128), ceil(R/128)], as third and fourth elements."""
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+        raise ValueError("x must be a tensor of 2 or 3 dimensions")
+    _need(x, "x", torch.bfloat16, x.dim())
+    lead = tuple(x.shape[:-2])
+    R, C = x.shape[-2:]
+    G = lead[0] if lead else 1
+    if (qt is None) != (scales_t is None):
+        raise ValueError("qt and scales_t go together")
+    transposed = transposed or qt is not None
+    q = _output(q, "q", tuple(x.shape), E4M3_DTYPES, x.device)
+    scales = _output(scales, "scales", lead + (_blocks128(R), _blocks128(C)), torch.float32, x.device)
+    if transposed:
+        qt = _output(qt, "qt", lead + (C, R), E4M3_DTYPES, x.device)
+        scales_t = _output(scales_t, "scales_t", lead + (_blocks128(C), _blocks128(R)), torch.float32, x.device)
+        _same_device(x, q, scales, qt, scales_t)
+    else:
+        _same_device(x, q, scales)
+    _call_on(x, quantize_b128_raw, _ptr(x), G, R, C, _ptr(q), _ptr(scales), _ptr(qt), _ptr(scales_t))
+    return (q, scales, qt, scales_t) if transposed else (q, scales)
+
+
+def gemm_tg128_nt(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, sbt: torch.Tensor,
+                  out: torch.Tensor | None = None):
+    """E4M3 a [M, K], sa [M, ceil(K/128)], K-major weight bt [N, K], sbt [ceil(N/128), ceil(K/128)] -> bf16 [M, N]."""
+    _need(a, "a", E4M3_DTYPES, 2)
+    _need(bt, "bt", E4M3_DTYPES, 2)
+    _need(sa, "sa", torch.float32, 2)
+    _need(sbt, "sbt", torch.float32, 2)
+    M, K = a.shape
+    N = bt.shape[0]
+    _need_shape(bt, "bt", (N, K))
+    _need_shape(sa, "sa", (M, _blocks128(K)))
+    _need_shape(sbt, "sbt", (_blocks128(N), _blocks128(K)))
+    out = _output(out, "out", (M, N), torch.bfloat16, a.device)
+    _same_device(a, sa, bt, sbt, out)
+    _call_on(a, gemm_tg128_nt_raw, _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(out), M, N, K)
+    return out
+
+
+def grouped_gemm_tg128_nt(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, sbt: torch.Tensor,
+                          offsets: torch.Tensor, out: torch.Tensor | None = None):
+    """a [M_total, K], sa [M_total, ceil(K/128)], weights bt [G, N, K], sbt [G, ceil(N/128), ceil(K/128)],
+    offsets int32 [G+1] on the device (any ascending row numbers) -> bf16 [M_total, N].
+
+    Rows outside every range keep what ``out`` holds (a new ``out`` is not initialised)."""
+    _need(a, "a", E4M3_DTYPES, 2)
+    _need(bt, "bt", E4M3_DTYPES, 3)
+    _need(sa, "sa", torch.float32, 2)
+    _need(sbt, "sbt", torch.float32, 3)
+    _need(offsets, "offsets", torch.int32, 1)
+    M, K = a.shape
+    G, N = bt.shape[:2]
+    _need_shape(bt, "bt", (G, N, K))
+    _need_shape(offsets, "offsets", (G + 1,))
+    _need_shape(sa, "sa", (M, _blocks128(K)))
+    _need_shape(sbt, "sbt", (G, _blocks128(N), _blocks128(K)))
+    out = _output(out, "out", (M, N), torch.bfloat16, a.device)
+    _same_device(a, sa, bt, sbt, offsets, out)
+    _call_on(a, grouped_gemm_tg128_nt_raw, _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(offsets), G, _ptr(out), M, N,
+             K)
+    return out
+
+
+def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                  accumulate: bool = False):
+    """bf16 dy [M_total, N], x [M_total, K], offsets int32 [G+1] on the device -> fp32 [G, N, K], the sums of
+    dy[m, n] * x[m, k] over each range's rows; with ``accumulate`` they are added to ``out``."""
+    _need(dy, "dy", torch.bfloat16, 2)
+    _need(x, "x", torch.bfloat16, 2)
+    _need(offsets, "offsets", torch.int32, 1)
+    M, N = dy.shape
+    K = x.shape[1]
+    G = offsets.shape[0] - 1
+    _need_shape(x, "x", (M, K))
+    if G < 1:
+        raise ValueError("offsets needs at least two entries")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    out = _output(out, "out", (G, N, K), torch.float32, dy.device)
+    _same_device(dy, x, offsets, out)
+    _call_on(dy, grouped_wgrad_raw, _ptr(dy), _ptr(x), _ptr(offsets), G, _ptr(out), 1 if accumulate else 0, M, N, K)
+    return out
+
+
+def swiglu_quantize_tg128(gu: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                          y: torch.Tensor | None = None, want_y: bool = False):
+    """bf16 [R, 2d] = [gate | up] -> silu(gate) * up, quantized as by quantize_tg128 from its fp32 values:
+    (q uint8 [R, d], scales fp32 [R, ceil(d/128)]), plus the bf16 values [R, d] as a third element when
+    ``want_y`` is true or ``y`` is given."""
+    _need(gu, "gu", torch.bfloat16, 2)
+    R, d2 = gu.shape
+    if d2 % 2:
+        raise ValueError("gu needs an even number of columns")
+    d = d2 // 2
+    q = _output(q, "q", (R, d), E4M3_DTYPES, gu.device)
+    scales = _output(scales, "scales", (R, _blocks128(d)), torch.float32, gu.device)
+    if y is not None or want_y:
+        y = _output(y, "y", (R, d), torch.bfloat16, gu.device)
+        _same_device(gu, y)
+    _same_device(gu, q, scales)
+    _call_on(gu, swiglu_quantize_tg128_raw, _ptr(gu), R, d, _ptr(q), _ptr(scales), _ptr(y))
+    return (q, scales) if y is None else (q, scales, y)
+
+
+def swiglu_backward_quantize_tg128(gu: torch.Tensor, dy: torch.Tensor, dgu: torch.Tensor | None = None,
+                                   q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                                   y: torch.Tensor | None = None, want_y: bool = False):
+    """The gradient of silu(gate) * up for bf16 gu [R, 2d] and dy [R, d]: (dgu bf16 [R, 2d], its codes uint8
+    [R, 2d] and scales fp32 [R, ceil(2d/128)] as by quantize_tg128 from the fp32 values), plus the forward
+    value bf16 [R, d] as a fourth element when ``want_y`` is true or ``y`` is given."""
+    _need(gu, "gu", torch.bfloat16, 2)
+    _need(dy, "dy", torch.bfloat16, 2)
+    R, d = dy.shape
+    _need_shape(gu, "gu", (R, 2 * d))
+    dgu = _output(dgu, "dgu", (R, 2 * d), torch.bfloat16, gu.device)
+    q = _output(q, "q", (R, 2 * d), E4M3_DTYPES, gu.device)
+    scales = _output(scales, "scales", (R, _blocks128(2 * d)), torch.float32, gu.device)
+    if y is not None or want_y:
+        y = _output(y, "y", (R, d), torch.bfloat16, gu.device)
+        _same_device(gu, y)
+    _same_device(gu, dy, dgu, q, scales)
+    _call_on(gu, swiglu_backward_quantize_tg128_raw, _ptr(gu), _ptr(dy), R, d, _ptr(dgu), _ptr(q), _ptr(scales),
+             _ptr(y))
+    return (dgu, q, scales) if y is None else (dgu, q, scales, y)

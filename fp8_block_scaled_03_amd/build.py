@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8bs.so")
 
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "rmsnorm.hip", "gemm_e8m0.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "rmsnorm.hip", "gemm_e8m0.hip", "api_g128.cpp",
+           "quantize_g128.hip", "gemm_g128.hip", "wgrad.hip", "swiglu.hip"]
 # measurement and test support (single instructions for the tests and the
 # bench), linked into a library of its own
 PROBE_SOURCES = ["probe.hip"]

@@ -49,7 +49,7 @@ const char* fp8bs_status_str(fp8bs_status s) {
   switch (s) {
     case FP8BS_OK: return "FP8BS_OK";
     case FP8BS_EINVAL: return "FP8BS_EINVAL: invalid argument (null pointer, negative size or bad group count)";
-    case FP8BS_ESHAPE: return "FP8BS_ESHAPE: a dimension is not a multiple of 32 or is too large";
+    case FP8BS_ESHAPE: return "FP8BS_ESHAPE: a dimension is not a multiple of 32 (16 in the 128-value forms) or is too large";
     case FP8BS_EALIGN: return "FP8BS_EALIGN: matrix pointers must be 16-byte aligned, scales 4-byte aligned";
     case FP8BS_EHIP: return "FP8BS_EHIP: the HIP runtime reported an error";
     case FP8BS_ENOSYS: return "FP8BS_ENOSYS: not available on this device";

@@ -1,0 +1,77 @@
+// The E4M3 quantizer's steps for groups of 128 columns that 16 neighbouring lanes
+// hold (eight values each): the group's maximum and the codes.
+#pragma once
+#include "common.hpp"
+
+namespace fp8bs {
+
+// Largest value of the 16 lanes of a DPP row, in every one of them (values with
+// a clear sign bit, compared as integers).  Lane exchanges inside a row of 16
+// go through the VALU: no LDS traffic.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  auto take = [](uint32_t a, uint32_t b) __attribute__((always_inline)) { return a > b ? a : b; };
+  v = take(v, __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true));   // lane ^ 1
+  v = take(v, __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true));   // lane ^ 2
+  v = take(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));  // the other quad of eight
+  v = take(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true));  // the other eight
+  return v;
+}
+
+// Largest |x| of eight bf16 values, as fp32 bits.
+__device__ __forceinline__ uint32_t amax_bf16x8(uint4 w) {
+  typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+  auto mag = [](uint32_t x) __attribute__((always_inline)) { return __builtin_bit_cast(v2us, x & 0x7FFF7FFFu); };
+  const v2us m = __builtin_elementwise_max(__builtin_elementwise_max(mag(w.x), mag(w.y)),
+                                           __builtin_elementwise_max(mag(w.z), mag(w.w)));
+  return (uint32_t)(m[0] > m[1] ? m[0] : m[1]) << 16;
+}
+
+struct Scale {
+  float s, r;  // scale, and its reciprocal where the reciprocal path is valid (else 0)
+};
+
+__device__ __forceinline__ Scale scale_of(uint32_t amax_bits) {
+  const float amax = __builtin_bit_cast(float, amax_bits);
+  const float s = amax / 448.0f;
+  return {s, amax >= QUANT_RECIP_MIN_AMAX ? 1.0f / s : 0.0f};
+}
+
+// Eight values -> eight codes.  With the reciprocal path |x / s| is at most
+// 448 (1 + 2^-22), which rounds to 448, so nothing is clamped; a subnormal scale
+// can be off by more, and the division path clamps.
+template <bool RECIP>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], Scale k) {
+  uint32_t p[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[4 * h + i];
+      t[i] = RECIP || k.r != 0.0f ? quant_quotient_recip(x, k.s, k.r) : sat448(quant_quotient_div(x, k.s));
+    }
+    p[h] = pack_e4m3x4(t[0], t[1], t[2], t[3]);
+  }
+  return make_uint2(p[0], p[1]);
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16_lo(ws[i]);
+    v[2 * i + 1] = bf16_hi(ws[i]);
+  }
+}
+
+// fp32 -> bf16, nearest even, two at a time in one instruction.
+__device__ __forceinline__ uint32_t bf16_round_pair(float lo, float hi) {
+  typedef float v2f __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{lo, hi}, v2bf));
+}
+__device__ __forceinline__ uint4 bf16_round8(const float (&v)[8]) {
+  return make_uint4(bf16_round_pair(v[0], v[1]), bf16_round_pair(v[2], v[3]), bf16_round_pair(v[4], v[5]),
+                    bf16_round_pair(v[6], v[7]));
+}
+
+}  // namespace fp8bs

@@ -1,0 +1,207 @@
+// bf16 -> E4M3 quantizers with one scale per row and 128 columns, and per
+// 128x128 block (with the transposed codes on request).
+//
+// Per group: amax = max |x|, s = amax / 448 in fp32, q = E4M3(x / s); the
+// quotient is formed from the scale's reciprocal and one correction (see
+// quantize.hip), the same bits as a division.  Both kernels are bound by HBM
+// traffic: two bytes read, one written (two with the transpose) per value.
+//
+// Sixteen lanes hold a group's 128 columns of one row, eight (16 bytes) each, so
+// a wave's load covers four rows of 256 bytes and a group's maximum is found
+// by DPP exchanges inside a row of lanes.
+#include "launch_g128.hpp"
+#include "quant_g128.hpp"
+
+#include <type_traits>
+
+namespace fp8bs {
+
+// One wave per region of 4U rows x 128 columns; all U loads of a lane are in
+// flight before any arithmetic.
+template <int U>
+__global__ void __launch_bounds__(256) quantize_tg128_kernel(const uint16_t* __restrict__ x, int64_t rows,
+                                                             int64_t cols, uint8_t* __restrict__ q,
+                                                             float* __restrict__ scales, int64_t n_regions) {
+  const int lane = threadIdx.x & 63;
+  const int piece = lane & 15, rsub = lane >> 4;
+  const int64_t nb = (cols + 127) >> 7;
+  const int64_t waves_total = (int64_t)gridDim.x * 4;
+  for (int64_t reg = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); reg < n_regions; reg += waves_total) {
+    const int64_t rb = reg / nb, cb = reg - rb * nb;
+    const int64_t col = cb * 128 + piece * 8;
+    uint4 w[U];
+    bool ok[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t row = rb * (4 * U) + 4 * k + rsub;
+      ok[k] = row < rows && col < cols;
+      w[k] = ok[k] ? *reinterpret_cast<const uint4*>(x + row * cols + col) : make_uint4(0, 0, 0, 0);
+    }
+    Scale sc[U];
+    bool all_recip = true;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      sc[k] = scale_of(row16_max(amax_bf16x8(w[k])));
+      all_recip = all_recip && (sc[k].r != 0.0f || !ok[k]);
+    }
+    auto store = [&](auto RECIP_) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int64_t row = rb * (4 * U) + 4 * k + rsub;
+        float v[8];
+        unpack8(w[k], v);
+        const uint2 p = codes8<decltype(RECIP_)::value>(v, sc[k]);
+        if (ok[k]) {
+          store_codes8(q + row * cols + col, p.x, p.y);
+          if (piece == 0) scales[row * nb + cb] = sc[k].s;
+        }
+      }
+    };
+    // every group of the wave on the reciprocal path (the common case): no
+    // per-element branches
+    if (__all(all_recip)) store(std::true_type{});
+    else store(std::false_type{});
+  }
+}
+
+// Four bytes of four rows, transposed: dword c of the result holds byte c of
+// r0, r1, r2, r3.
+__device__ __forceinline__ void transpose4x4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_t (&o)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(r1, r0, 0x05010400u);  // r0.0 r1.0 r0.1 r1.1
+  const uint32_t b = __builtin_amdgcn_perm(r1, r0, 0x07030602u);  // r0.2 r1.2 r0.3 r1.3
+  const uint32_t c = __builtin_amdgcn_perm(r3, r2, 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(r3, r2, 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// One 256-thread workgroup per 128x128 block.  Lane (piece, rsub) of wave w holds
+// rows 32w + 8 rsub .. +7 of columns 8 piece .. +7, an 8x8 square that it transposes
+// by byte permutes; the transposed codes go through LDS so that whole
+// 128-byte rows of qt are written.
+constexpr int TPAD = 128 + 16;  // LDS row of 128 codes, 16-byte aligned, rows 4 banks apart
+
+template <bool TRANSPOSED>
+__global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __restrict__ x, int64_t rows,
+                                                            int64_t cols, uint8_t* __restrict__ q,
+                                                            float* __restrict__ scales, uint8_t* __restrict__ qt,
+                                                            float* __restrict__ scales_t, uint32_t rb_count,
+                                                            uint32_t cb_count) {
+  __shared__ uint32_t wave_max[4];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[TRANSPOSED ? 128 * TPAD : 16];
+  const int lane = threadIdx.x & 63;
+  const int w = threadIdx.x >> 6;
+  const int piece = lane & 15, rsub = lane >> 4;
+  const uint32_t cb = blockIdx.x % cb_count, rest = blockIdx.x / cb_count;
+  const uint32_t rb = rest % rb_count;
+  const int64_t gi = rest / rb_count;
+  x += gi * rows * cols;
+  q += gi * rows * cols;
+  const int64_t col = (int64_t)cb * 128 + piece * 8;
+  const int r0 = 32 * w + 8 * rsub;
+  uint4 v[8];
+  bool ok[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t row = (int64_t)rb * 128 + r0 + k;
+    ok[k] = row < rows && col < cols;
+    v[k] = ok[k] ? *reinterpret_cast<const uint4*>(x + row * cols + col) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t mk = amax_bf16x8(v[k]);
+    m = m > mk ? m : mk;
+  }
+  m = row16_max(m);
+#pragma unroll
+  for (int d = 16; d <= 32; d <<= 1) {
+    const uint32_t o = __shfl_xor(m, d, 64);
+    m = m > o ? m : o;
+  }
+  if (lane == 0) wave_max[w] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = m > wave_max[i] ? m : wave_max[i];
+  const Scale sc = scale_of(m);
+  uint2 p[8];
+  if (sc.r != 0.0f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float f[8];
+      unpack8(v[k], f);
+      p[k] = codes8<true>(f, sc);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float f[8];
+      unpack8(v[k], f);
+      p[k] = codes8<false>(f, sc);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t row = (int64_t)rb * 128 + r0 + k;
+    if (ok[k]) store_codes8(q + row * cols + col, p[k].x, p[k].y);
+  }
+  if (threadIdx.x == 0) {
+    scales[(gi * rb_count + rb) * cb_count + cb] = sc.s;
+    if constexpr (TRANSPOSED) scales_t[(gi * cb_count + cb) * rb_count + rb] = sc.s;
+  }
+  if constexpr (TRANSPOSED) {
+    qt += gi * rows * cols;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // columns 4h .. 4h + 3 of the lane's eight
+      uint32_t lo[4], hi[4];
+      auto word = [&](int k) __attribute__((always_inline)) { return h == 0 ? p[k].x : p[k].y; };
+      transpose4x4(word(0), word(1), word(2), word(3), lo);
+      transpose4x4(word(4), word(5), word(6), word(7), hi);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint2*>(tile + (piece * 8 + 4 * h + c) * TPAD + r0) = make_uint2(lo[c], hi[c]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 32 columns of the block per pass, eight lanes of 16 bytes each
+      const int c = i * 32 + (threadIdx.x >> 3), r = (threadIdx.x & 7) * 16;
+      const int64_t qc = (int64_t)cb * 128 + c, qr = (int64_t)rb * 128 + r;
+      if (qc < cols && qr < rows)
+        *reinterpret_cast<uint4*>(qt + qc * rows + qr) = *reinterpret_cast<const uint4*>(tile + c * TPAD + r);
+    }
+  }
+}
+
+hipError_t launch_quantize_tg128(const void* x, int64_t rows, int64_t cols, void* q, float* scales,
+                                 hipStream_t stream) {
+  const int64_t nb = (cols + 127) / 128;
+  auto go = [&](auto U_) {
+    constexpr int U = decltype(U_)::value;
+    const int64_t n_regions = ((rows + 4 * U - 1) / (4 * U)) * nb;
+    int64_t grid = (n_regions + 3) / 4;
+    if (grid > 65536) grid = 65536;
+    hipLaunchKernelGGL((quantize_tg128_kernel<U>), dim3((unsigned)grid), dim3(256), 0, stream, (const uint16_t*)x,
+                       rows, cols, (uint8_t*)q, scales, n_regions);
+  };
+  // a region of 32 rows per wave when that fills the chip, else of four
+  if ((rows + 31) / 32 * nb >= 4096) go(std::integral_constant<int, 8>{});
+  else go(std::integral_constant<int, 1>{});
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_b128(const void* x, int64_t G, int64_t rows, int64_t cols, void* q, float* scales,
+                                void* qt, float* scales_t, hipStream_t stream) {
+  const int64_t rb = (rows + 127) / 128, cb = (cols + 127) / 128;
+  const dim3 grid((unsigned)(G * rb * cb));
+  if (qt)
+    hipLaunchKernelGGL(quantize_b128_kernel<true>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
+                       (uint8_t*)q, scales, (uint8_t*)qt, scales_t, (uint32_t)rb, (uint32_t)cb);
+  else
+    hipLaunchKernelGGL(quantize_b128_kernel<false>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
+                       (uint8_t*)q, scales, (uint8_t*)nullptr, (float*)nullptr, (uint32_t)rb, (uint32_t)cb);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

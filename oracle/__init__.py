@@ -36,6 +36,7 @@ from .exact import gemm_exact
 from .rmsnorm import residual_add, rmsnorm_ref, rmsnorm_tolerance_ok, RMS_REL_TOL, RMS_ABS_TOL
 from .e8m0 import (e8m0_exponent, quantize_blocks_e8m0, dequantize_e8m0, gemm_ref_e8m0_nt, gemm_e8m0_bound_nt,
                    emulate_gemm_e8m0_nt, code_exponents, step_bound)
+from .g128 import (quantize_g128, dequantize_g128, gemm_g128_bound, swiglu, swiglu_grad, e4m3_half_step)
 
 __all__ = [
     "Minifloat", "E4M3FN", "FP16", "BF16",
@@ -49,4 +50,5 @@ __all__ = [
     "residual_add", "rmsnorm_ref", "rmsnorm_tolerance_ok", "RMS_REL_TOL", "RMS_ABS_TOL",
     "e8m0_exponent", "quantize_blocks_e8m0", "dequantize_e8m0", "gemm_ref_e8m0_nt", "gemm_e8m0_bound_nt",
     "emulate_gemm_e8m0_nt", "code_exponents", "step_bound",
+    "quantize_g128", "dequantize_g128", "gemm_g128_bound", "swiglu", "swiglu_grad", "e4m3_half_step",
 ]

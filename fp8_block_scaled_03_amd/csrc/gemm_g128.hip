@@ -23,6 +23,8 @@
 #include "launch_g128.hpp"
 #include "ragged.hpp"
 
+#include <type_traits>
+
 namespace fp8bs {
 
 typedef int v8i_t __attribute__((ext_vector_type(8)));
@@ -244,6 +246,315 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   }
 }
 
+// ---- the large tile: 256 x 256 per workgroup, eight waves of 128 x 64 (2 row bands by
+// 4 column bands), MFMAs fed without a pause.
+//
+// In a wave every MFMA of row sub-tile i is preceded by the four promotion fmas of
+// the product that the same column sub-tile had for row sub-tile i - 1, so the
+// fmas run under the matrix pipe and no product is waited for (a register-only
+// loop in this order reaches 4.84 PFLOP/s, the MFMAs alone 4.92).  Fragments of
+// row sub-tile i + 1 are read from LDS one sub-tile ahead; the weight fragments of
+// the next step replace the current ones as the last row sub-tile's MFMAs issue.
+//
+// A step's data arrive in three parts with two barriers per step:
+//   middle (before row sub-tile 3): rows of sub-tiles 0-3 of A's slot and the
+//     weight's slot have been read by every wave; the loads of step ks + 2 into them
+//     are issued;
+//   end (before row sub-tile 7): the rest of A's slot has been read, its loads
+//     for ks + 2 are issued; the next step's first fragments may be read.
+// Each load has about one and a half steps to land.  The waits count a wave's own
+// loads (they return in order); the barrier makes them everybody's.
+constexpr int XBM = 256, XBN = 256, XTHREADS = 512;
+constexpr int X_A = 0, X_B = 2 * XBM * GK, X_S = X_B + 2 * XBN * GK;  // LDS: A slots, weight slots, scales
+constexpr int X_SLOT = XBM * GK;
+constexpr int X_SBUF = XBM * SCH * 4;  // scales of 256 rows x 8 K-blocks
+constexpr int X_LDS = X_S + 2 * X_SBUF;
+
+template <bool GROUPED>
+__global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
+    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
+    const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
+    int64_t N, int64_t K, uint32_t tiles_n) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  typedef __attribute__((address_space(3))) unsigned char lds_u8;
+  typedef __attribute__((address_space(3))) const v4i lds_v4i;
+  typedef __attribute__((address_space(3))) const float lds_f32;
+  typedef __attribute__((address_space(3))) v4i lds_v4i_w;
+  lds_u8* const lds = (lds_u8*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+  const int lane = threadIdx.x & 63;
+  const int w = wave_id_uniform();
+  const int wm = w >> 2, wn = w & 3;  // the waves of one SIMD (w, w + 4) are in different row bands
+  const int g = lane >> 4, lo = lane & 15;
+
+  TileAt t;
+  if constexpr (GROUPED) {
+    if (!find_tile<XBM>(offsets, G, M, tiles_n, blockIdx.x, t)) return;
+    bt += (int64_t)t.group * N * K;
+    sbt += (int64_t)t.group * ((N + 127) >> 7) * ((K + 127) >> 7);
+  } else {
+    dense_tile<XBM>(M, tiles_n, blockIdx.x, gridDim.x, t);
+  }
+  const int64_t row0 = t.row0, col0 = (int64_t)t.tn * XBN;
+  const int m_valid = (int)(t.row_end - row0 < XBM ? t.row_end - row0 : XBM);
+  const int n_valid = (int)(N - col0 < XBN ? N - col0 : XBN);
+  const int KB = (int)((K + 127) >> 7);
+
+  // ---- direct loads of 8 rows each; lane l loads row l >> 3, 16-byte piece
+  // (l & 7) ^ (row & 7).  Rows past the range read its last row.
+  const int piece = (lane & 7) ^ (lane >> 3);
+  auto row_off = [&](int row, int valid) __attribute__((always_inline)) -> uint32_t {
+    const int r = row + (lane >> 3);
+    return (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + piece * 16;
+  };
+  const int a_first = (w >> 2) * 128 + (w & 3) * 16;  // rows of sub-tiles 0-3; those of 4-7 lie 64 further
+  uint32_t a_off[4], b_off[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a_off[i] = row_off(a_first + (i >> 1) * 64 + (i & 1) * 8, m_valid);
+    b_off[i] = row_off((w * 4 + i) * 8, n_valid);
+  }
+  const uint8_t* const a0 = uniform_ptr(a + row0 * K);
+  const uint8_t* const b0 = uniform_ptr(bt + col0 * K);
+  const uint8_t* const sa0 = uniform_ptr(reinterpret_cast<const uint8_t*>(sa + row0 * KB));
+  // In the partial last K-block the pieces past K read the last whole piece (the
+  // LDS bytes are cleared afterwards).
+  const int over = (KB - 1) * GK + piece * 16 + 16 - (int)K;
+  const uint32_t tail_back = over > 0 ? over : 0;
+  const bool partial = (K & 127) != 0;
+
+  auto issue_a = [&](int ks, int i) __attribute__((always_inline)) {  // i 0, 1: sub-tiles 0-3; 2, 3: 4-7
+    const uint32_t dst = lds0 + X_A + (ks & 1) * X_SLOT + (a_first + (i >> 1) * 64 + (i & 1) * 8) * GK;
+    dma16_at(a0 + (int64_t)ks * GK, a_off[i] - (ks == KB - 1 ? tail_back : 0u), dst);
+  };
+  auto issue_b = [&](int ks, int i) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + X_B + (ks & 1) * X_SLOT + (w * 32 + i * 8) * GK;
+    dma16_at(b0 + (int64_t)ks * GK, b_off[i] - (ks == KB - 1 ? tail_back : 0u), dst);
+  };
+  // Scales of eight rows x eight K-blocks, one per lane: part q (0..3) of this
+  // wave's 32 rows of chunk `chunk`, to [row][K-block].
+  auto issue_s = [&](int chunk, int q) __attribute__((always_inline)) {
+    const int first = w * 32 + q * 8;
+    const int r = first + (lane >> 3), kb = chunk * SCH + (lane & 7);
+    const uint32_t off = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                     lds0 + X_S + (chunk & 1) * X_SBUF + first * SCH * 4),
+                 "v"(off * 4), "s"(sa0)
+                 : "memory");
+  };
+  // Zeros behind K in the last K-block's slots, once its data are there for every wave.
+  auto clear_tail = [&]() __attribute__((always_inline)) {
+    const int first = (int)(K & 127) >> 4;  // first piece past K
+    const int r = threadIdx.x & 255;
+    lds_u8* const base = lds + (threadIdx.x < 256 ? X_A : X_B) + ((KB - 1) & 1) * X_SLOT + r * GK;
+    for (int p = first; p < 8; ++p) *(lds_v4i_w*)(base + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
+  };
+
+  const int64_t nb = (col0 + wn * 64) >> 7;
+  // read through the scalar cache (the weight's scales are not written meanwhile)
+  typedef __attribute__((address_space(4))) const float const_f32;
+  const const_f32* const sb_row = (const const_f32*)uniform64(
+      reinterpret_cast<int64_t>(sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB));
+
+  // The loads of step ks + 2, one at a time: after the middle barrier the scales
+  // (even steps), sub-tiles 0-3 of A and the weight, after the end barrier
+  // sub-tiles 4-7 of A.
+  auto issue_mid = [&](int ks, int n) __attribute__((always_inline)) {
+    if (n == 0) {
+      if ((ks & 1) == 0) issue_s((ks >> 3) + 1, (ks & 7) >> 1);
+    } else if (n < 3) {
+      issue_a(ks + 2, n - 1);
+    } else {
+      issue_b(ks + 2, n - 3);
+    }
+  };
+  auto issue_end = [&](int ks, int n) __attribute__((always_inline)) { issue_a(ks + 2, 2 + n); };
+
+  // The waits and barriers of one step, between which `work` runs its parts: 0
+  // before the middle, 1 to the end, 2 after it; part 1 issues the seven loads of
+  // issue_mid and part 2 the two of issue_end if `loads`.  P is ks & 1 while steps
+  // ks + 2 are loaded (waits leave the younger loads in flight); with P = -1 (the
+  // last steps) every load has been waited for.
+  auto step = [&](int ks, auto P_, auto&& work) __attribute__((always_inline)) {
+    constexpr int P = decltype(P_)::value;
+    const bool loads = P >= 0 || ks + 2 < KB;
+    if constexpr (P >= 0) __builtin_assume((ks & 1) == P);
+    work(std::integral_constant<int, 0>{}, loads);
+    if constexpr (P >= 0) wait_vmcnt<(P == 1 ? 9 : 8)>();
+    else wait_vmcnt<0>();
+    lds_barrier();
+    work(std::integral_constant<int, 1>{}, loads);
+    if constexpr (P >= 0) wait_vmcnt<(P == 0 ? 9 : 8)>();
+    else wait_vmcnt<0>();
+    lds_barrier();
+    if (P < 0 && partial && ks + 2 == KB) {
+      clear_tail();
+      lds_barrier();
+    }
+    work(std::integral_constant<int, 2>{}, loads);
+  };
+  auto run = [&](auto&& work) __attribute__((always_inline)) {
+    int ks = 0;
+#pragma unroll 1
+    for (; ks + 3 < KB; ks += 2) {
+      step(ks, std::integral_constant<int, 0>{},
+           [&](auto part, bool loads) __attribute__((always_inline)) { work(ks, part, loads); });
+      step(ks + 1, std::integral_constant<int, 1>{},
+           [&](auto part, bool loads) __attribute__((always_inline)) { work(ks + 1, part, loads); });
+    }
+#pragma unroll 1
+    for (; ks < KB; ++ks)
+      step(ks, std::integral_constant<int, -1>{},
+           [&](auto part, bool loads) __attribute__((always_inline)) { work(ks, part, loads); });
+  };
+
+  v4f acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const bool wave_live = wm * 128 < m_valid && wn * 64 < n_valid;
+  if (KB > 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) issue_s(0, q);
+    // as in the loop: (sub-tiles 0-3 and the weight), then sub-tiles 4-7
+    auto issue_first = [&](int ks) __attribute__((always_inline)) {
+      issue_a(ks, 0);
+      issue_a(ks, 1);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) issue_b(ks, n);
+    };
+    issue_first(0);
+    issue_a(0, 2);
+    issue_a(0, 3);
+    if (KB > 1) issue_first(1);
+    if (KB > 2) wait_vmcnt<8>();
+    else wait_vmcnt<0>();
+    lds_barrier();
+    if (KB > 1) {
+      issue_a(1, 2);
+      issue_a(1, 3);
+    }
+    if (partial && KB == 1) {
+      clear_tail();
+      lds_barrier();
+    }
+
+    if (wave_live) {
+      const int sw0 = 16 * (g ^ (lo & 7)), sw1 = 16 * ((4 + g) ^ (lo & 7));
+      const lds_u8* const ra0 = lds + X_A + (wm * 128 + lo) * GK + sw0;
+      const lds_u8* const ra1 = lds + X_A + (wm * 128 + lo) * GK + sw1;
+      const lds_u8* const rb0 = lds + X_B + (wn * 64 + lo) * GK + sw0;
+      const lds_u8* const rb1 = lds + X_B + (wn * 64 + lo) * GK + sw1;
+      const lds_u8* const rs = lds + X_S + (wm * 128 + lo) * SCH * 4;
+      auto read = [&](const lds_u8* p0, const lds_u8* p1, int off) __attribute__((always_inline)) -> v8i_t {
+        const v4i x = *(lds_v4i*)(p0 + off), y = *(lds_v4i*)(p1 + off);
+        return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      };
+      v8i_t bf[4], af[2];
+      v4f p[4];
+      float sc[8];
+      float sb = sb_row[0];
+      // the first step's fragments; products of "row sub-tile 7 of the step before" are zeros
+      af[0] = read(ra0, ra1, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf[j] = read(rb0, rb1, j * 2048);
+        p[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] = 0.0f;
+
+      run([&](int ks, auto part_, bool loads) __attribute__((always_inline)) {
+        constexpr int part = decltype(part_)::value;
+        const int slot = (ks & 1) * X_SLOT;
+        constexpr int first = part == 0 ? 0 : part == 1 ? 3 : 7, last = part == 0 ? 3 : part == 1 ? 7 : 8;
+#pragma unroll
+        for (int i = first; i < last; ++i) {
+          if (i < 7) af[(i + 1) & 1] = read(ra0, ra1, slot + (i + 1) * 2048);
+          else af[0] = read(ra0, ra1, (X_SLOT - slot));  // after the last step: in bounds, never used
+          float s_raw[8];
+          if (i == 0) {
+            const lds_u8* const q = rs + ((ks >> 3) & 1) * X_SBUF + (ks & 7) * 4;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) s_raw[x] = *(lds_f32*)(q + x * 16 * SCH * 4);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            promote(acc[(i + 7) & 7][j], p[j], sc[(i + 7) & 7]);
+            asm volatile("" : "+v"(acc[(i + 7) & 7][j]));  // here, not where it is next needed
+            __builtin_amdgcn_sched_barrier(0);
+            p[j] = mfma_block(bf[j], af[i & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i == 7) bf[j] = read(rb0, rb1, (X_SLOT - slot) + j * 2048);
+            // one load per two MFMAs: a burst would hold up the wave's issue
+            if (j & 1) {
+              const int n = (i - first) * 2 + (j >> 1);
+              if (part == 1 && n < 7 && loads) issue_mid(ks, n);
+              if (part == 2 && loads) issue_end(ks, n);
+            }
+          }
+          if (i == 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) sc[x] = s_raw[x] * sb;
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (i == 3) sb = sb_row[ks + 1 < KB ? ks + 1 : ks];
+        }
+      });
+#pragma unroll
+      for (int j = 0; j < 4; ++j) promote(acc[7][j], p[j], sc[7]);
+    } else {
+      run([&](int ks, auto part_, bool loads) __attribute__((always_inline)) {
+        constexpr int part = decltype(part_)::value;
+        if (part == 1 && loads)
+#pragma unroll
+          for (int n = 0; n < 7; ++n) issue_mid(ks, n);
+        if (part == 2 && loads) {
+          issue_end(ks, 0);
+          issue_end(ks, 1);
+        }
+      });
+    }
+    wait_vmcnt<0>();
+  }
+
+  // ---- epilogue: lane holds row 16i + lo, columns 16j + 4g .. +3 of its wave
+  if (!wave_live) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = wm * 128 + 16 * i + lo;
+    if (r < m_valid) {
+      uint16_t* const cr = c + (row0 + r) * N + col0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = wn * 64 + 16 * j + 4 * g;
+        if (col < n_valid)
+          *reinterpret_cast<uint2*>(cr + col) =
+              make_uint2(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]));
+      }
+    }
+  }
+}
+
+static hipError_t launch_big(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
+                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  const int64_t tiles_n = (N + XBN - 1) / XBN;
+  const int64_t tiles_m = offsets ? (M + XBM - 1) / XBM + (G < M ? G : M) : (M + XBM - 1) / XBM;
+  if (tiles_m * tiles_n > (int64_t)0xFFFFFFFF / XTHREADS) return hipErrorNotSupported;
+  const dim3 grid((unsigned)(tiles_m * tiles_n));
+  if (offsets)
+    hipLaunchKernelGGL(gemm_g128_big_kernel<true>, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa,
+                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+  else
+    hipLaunchKernelGGL(gemm_g128_big_kernel<false>, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa,
+                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+  return hipGetLastError();
+}
+
 template <int MI, int NJ, int WM, int WN>
 constexpr int tile_lds() {
   return 2 * (16 * MI * WM + 16 * NJ * WN) * GK + 2 * SCH * 16 * MI * WM * 4;
@@ -280,7 +591,11 @@ static hipError_t launch_tile(const void* a, const float* sa, const void* bt, co
 }
 
 hipError_t set_gemm_g128_attributes() {
-  hipError_t e = set_tile_attributes<8, 4, 2, 4>();
+  hipError_t e = hipFuncSetAttribute((const void*)gemm_g128_big_kernel<false>,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, X_LDS);
+  if (e == hipSuccess)
+    e = hipFuncSetAttribute((const void*)gemm_g128_big_kernel<true>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                            X_LDS);
   if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 2>();
   if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2>();
   return e;
@@ -290,7 +605,7 @@ hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, cons
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t avg = (M + G - 1) / G;  // rows per range
   auto tiles = [&](int64_t b) { return G * ((avg + b - 1) / b) * ((N + b - 1) / b); };
-  if (tiles(256) >= 256) return launch_tile<8, 4, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (tiles(256) >= 256) return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (tiles(128) >= 256) return launch_tile<4, 4, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   return launch_tile<2, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
 }

@@ -267,7 +267,10 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 constexpr int XBM = 256, XBN = 256, XTHREADS = 512;
 constexpr int X_A = 0, X_B = 2 * XBM * GK, X_S = X_B + 2 * XBN * GK;  // LDS: A slots, weight slots, scales
 constexpr int X_SLOT = XBM * GK;
-constexpr int X_SBUF = XBM * SCH * 4;  // scales of 256 rows x 8 K-blocks
+// Scales of 256 rows x 8 K-blocks: eight rows as [K-block][row], 256 bytes, two such
+// pieces per row sub-tile at 0 and 288 of its 768 bytes: the 16 rows that a
+// read takes for one K-block lie on 16 banks.
+constexpr int X_SSUB = 768, X_SBUF = XBM / 16 * X_SSUB;
 constexpr int X_LDS = X_S + 2 * X_SBUF;
 
 template <bool GROUPED>
@@ -333,13 +336,12 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     dma16_at(b0 + (int64_t)ks * GK, b_off[i] - (ks == KB - 1 ? tail_back : 0u), dst);
   };
   // Scales of eight rows x eight K-blocks, one per lane: part q (0..3) of this
-  // wave's 32 rows of chunk `chunk`, to [row][K-block].
+  // wave's 32 rows of chunk `chunk`.
   auto issue_s = [&](int chunk, int q) __attribute__((always_inline)) {
-    const int first = w * 32 + q * 8;
-    const int r = first + (lane >> 3), kb = chunk * SCH + (lane & 7);
+    const int r = w * 32 + q * 8 + (lane & 7), kb = chunk * SCH + (lane >> 3);
     const uint32_t off = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
-                     lds0 + X_S + (chunk & 1) * X_SBUF + first * SCH * 4),
+                     lds0 + X_S + (chunk & 1) * X_SBUF + (w * 2 + (q >> 1)) * X_SSUB + (q & 1) * 288),
                  "v"(off * 4), "s"(sa0)
                  : "memory");
   };
@@ -352,10 +354,14 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   };
 
   const int64_t nb = (col0 + wn * 64) >> 7;
-  // read through the scalar cache (the weight's scales are not written meanwhile)
-  typedef __attribute__((address_space(4))) const float const_f32;
-  const const_f32* const sb_row = (const const_f32*)uniform64(
-      reinterpret_cast<int64_t>(sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB));
+  // The weight's scales, one per wave and step: lane l holds step 64c + l's.  Waited
+  // for where they are loaded, so that nothing in the loop waits for them.
+  const float* const sb_row = sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB;
+  auto load_sb = [&](int ks) __attribute__((always_inline)) -> int {
+    int v = __builtin_bit_cast(int, sb_row[ks + lane < KB ? ks + lane : KB - 1]);
+    asm volatile("" : "+v"(v));
+    return v;
+  };
 
   // The loads of step ks + 2, one at a time: after the middle barrier the scales
   // (even steps), sub-tiles 0-3 of A and the weight, after the end barrier
@@ -448,7 +454,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
       const lds_u8* const ra1 = lds + X_A + (wm * 128 + lo) * GK + sw1;
       const lds_u8* const rb0 = lds + X_B + (wn * 64 + lo) * GK + sw0;
       const lds_u8* const rb1 = lds + X_B + (wn * 64 + lo) * GK + sw1;
-      const lds_u8* const rs = lds + X_S + (wm * 128 + lo) * SCH * 4;
+      const lds_u8* const rs = lds + X_S + wm * 8 * X_SSUB + (lo >> 3) * 288 + (lo & 7) * 4;
       auto read = [&](const lds_u8* p0, const lds_u8* p1, int off) __attribute__((always_inline)) -> v8i_t {
         const v4i x = *(lds_v4i*)(p0 + off), y = *(lds_v4i*)(p1 + off);
         return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
       v8i_t bf[4], af[2];
       v4f p[4];
       float sc[8];
-      float sb = sb_row[0];
+      int sb_lanes = load_sb(0);
       // the first step's fragments; products of "row sub-tile 7 of the step before" are zeros
       af[0] = read(ra0, ra1, 0);
 #pragma unroll
@@ -470,6 +476,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
       run([&](int ks, auto part_, bool loads) __attribute__((always_inline)) {
         constexpr int part = decltype(part_)::value;
         const int slot = (ks & 1) * X_SLOT;
+        if (part == 0 && (ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
         constexpr int first = part == 0 ? 0 : part == 1 ? 3 : 7, last = part == 0 ? 3 : part == 1 ? 7 : 8;
 #pragma unroll
         for (int i = first; i < last; ++i) {
@@ -477,9 +484,9 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
           else af[0] = read(ra0, ra1, (X_SLOT - slot));  // after the last step: in bounds, never used
           float s_raw[8];
           if (i == 0) {
-            const lds_u8* const q = rs + ((ks >> 3) & 1) * X_SBUF + (ks & 7) * 4;
+            const lds_u8* const q = rs + ((ks >> 3) & 1) * X_SBUF + (ks & 7) * 32;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) s_raw[x] = *(lds_f32*)(q + x * 16 * SCH * 4);
+            for (int x = 0; x < 8; ++x) s_raw[x] = *(lds_f32*)(q + x * X_SSUB);
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -498,11 +505,11 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
             }
           }
           if (i == 0) {
+            const float sb = __builtin_bit_cast(float, __builtin_amdgcn_readlane(sb_lanes, ks & 63));
 #pragma unroll
             for (int x = 0; x < 8; ++x) sc[x] = s_raw[x] * sb;
             __builtin_amdgcn_sched_barrier(0);
           }
-          if (i == 3) sb = sb_row[ks + 1 < KB ? ks + 1 : ks];
         }
       });
 #pragma unroll

@@ -33,9 +33,6 @@ typedef float v2f_t __attribute__((ext_vector_type(2)));
 constexpr int GK = 128;        // K-block = K step = bytes of one staged row
 constexpr int SCH = 8;         // K-blocks per staged chunk of A's scales
 
-// 16 zero bytes that stand for K past the end of a row
-__device__ const uint4 g128_zeros = {0, 0, 0, 0};
-
 // P of one K-block for a 16x16 output sub-tile (w: weight rows, x: A rows).
 __device__ __forceinline__ v4f mfma_block(v8i_t w, v8i_t x) {
   const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -55,33 +52,51 @@ __device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint
                : "memory");
 }
 
-// A tile of BM = 16*MI*WM rows by BN = 16*NJ*WN columns per workgroup of
-// WM x WN waves; wave (wm, wn) owns MI x NJ sub-tiles of 16x16.  A and Bt are
-// streamed as bytes into a ring of two 128-deep steps in LDS with direct loads,
-// a step ahead; row r of a stage holds its 128 bytes with 16-byte piece p at
-// position p ^ (r & 7), which spreads a fragment read over all banks.  A's
-// scales of eight K-blocks at a time are loaded to registers, then placed in LDS
-// in the order in which a lane needs them (its MI sub-tile rows side by side).
-// A weight scale is one value per wave and step: lane l holds the one of step
-// 64c + l.
-template <int MI, int NJ, int WM, int WN, bool GROUPED>
+// ---- small and middle tiles: BM = 16*MI*WM rows by BN = 16*NJ*WN columns per
+// workgroup of WM x WN waves; wave (wm, wn) owns MI x NJ sub-tiles of 16x16.
+//
+// A and Bt are streamed as bytes with direct loads into a ring of S steps in
+// LDS, S - 1 steps ahead: few workgroups (a decode step's tiles) then still keep
+// enough bytes in flight.  Row r of a stage holds its 128 bytes with 16-byte
+// piece p at position p ^ (r & 7), which spreads a fragment read over all
+// banks.  A's scales come eight K-blocks at a time, one or
+// two such chunks ahead; a weight scale is one value per wave and step, held by lane l for step 64c + l.
+// Waits until at most min(ahead, MOST) steps of P loads are in flight.
+template <int MOST, int P>
+__device__ __forceinline__ void wait_steps(int ahead) {
+  if constexpr (MOST == 0) {
+    wait_vmcnt<0>();
+  } else {
+    if (ahead >= MOST) wait_vmcnt<MOST * P>();
+    else wait_steps<MOST - 1, P>(ahead);
+  }
+}
+
+template <int MI, int NJ, int WM, int WN, int S, bool GROUPED>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
     const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
     int64_t N, int64_t K, uint32_t tiles_n) {
-  constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN, WAVES = WM * WN, THREADS = 64 * WAVES;
+  constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN, WAVES = WM * WN;
   constexpr int STAGE = (BM + BN) * GK;
-  constexpr int A_PIECES = BM / 8 / WAVES, B_PIECES = BN / 8 / WAVES;  // 1 KB loads per wave and step
-  constexpr int S_ITEMS = (2 * BM + THREADS - 1) / THREADS;            // half chunks of one row per thread
-  static_assert(A_PIECES * 8 * WAVES == BM && B_PIECES * 8 * WAVES == BN, "tile is a whole number of loads");
+  constexpr int PIECES = (BM + BN) / 8 / WAVES;            // 1 KB loads per wave and step
+  constexpr int S_PIECES = BM / 8;                         // 256-byte scale loads per chunk
+  constexpr int S_STEPS = (S_PIECES + WAVES - 1) / WAVES;  // steps of a chunk that issue one per wave
+  constexpr int SSUB = 768, SBUF = BM / 16 * SSUB;         // as in the large tile
+  static_assert(PIECES * 8 * WAVES == BM + BN, "tile is a whole number of loads");
   static_assert(NJ * 16 <= 128 && 128 % (NJ * 16) == 0, "a wave's columns lie in one weight block");
+  static_assert(S_STEPS + S <= SCH, "a chunk of scales has landed before its first step");
+  static_assert(PIECES * (S - 2) < 64, "vmcnt range");
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  float* const s_lds = reinterpret_cast<float*>(smem + 2 * STAGE);     // [2][SCH][BM]
+  typedef __attribute__((address_space(3))) unsigned char lds_u8;
+  typedef __attribute__((address_space(3))) const v4i lds_v4i;
+  typedef __attribute__((address_space(3))) v4i lds_v4i_w;
+  typedef __attribute__((address_space(3))) const float lds_f32;
+  lds_u8* const lds = (lds_u8*)smem;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
   const int lane = threadIdx.x & 63;
   const int w = wave_id_uniform();
-  // the waves of one SIMD (w, w + 4) lie in different row bands, so a tile with
-  // few rows still uses every SIMD
   const int wm = w / WN, wn = w % WN;
   const int g = lane >> 4, lo = lane & 15;
 
@@ -99,82 +114,47 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   const int KB = (int)((K + 127) >> 7);
   const bool wave_live = wm * 16 * MI < m_valid && wn * 16 * NJ < n_valid;
 
-  // ---- direct loads: piece i of a wave is rows 8p .. 8p+7, p = w*PIECES + i;
-  // lane l loads row 8p + (l >> 3), 16-byte piece (l & 7) ^ (row & 7).  Rows past
-  // the range read its last row (never stored).
+  // ---- direct loads: piece p = w + i*WAVES is rows 8p .. 8p+7 of the stage (A's rows,
+  // then the weight's); lane l loads row l >> 3, 16-byte piece (l & 7) ^ (row & 7).
+  // Rows past the range read its last row (never stored); in the partial last
+  // K-block the pieces past K read the last whole piece (cleared afterwards).
   const int piece = (lane & 7) ^ (lane >> 3);
-  uint32_t a_off[A_PIECES], b_off[B_PIECES];
+  uint32_t off[PIECES];
+  const uint8_t* from[PIECES];
 #pragma unroll
-  for (int i = 0; i < A_PIECES; ++i) {
-    int r = 8 * (w * A_PIECES + i) + (lane >> 3);
-    r = r < m_valid ? r : m_valid - 1;
-    a_off[i] = (uint32_t)r * (uint32_t)K + piece * 16;
+  for (int i = 0; i < PIECES; ++i) {
+    const int p = w + i * WAVES;
+    const bool of_a = p < BM / 8;
+    const int valid = of_a ? m_valid : n_valid;
+    const int r = (of_a ? p : p - BM / 8) * 8 + (lane >> 3);
+    off[i] = (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + piece * 16;
+    from[i] = uniform_ptr(of_a ? a + row0 * K : bt + col0 * K);
   }
-#pragma unroll
-  for (int i = 0; i < B_PIECES; ++i) {
-    int r = 8 * (w * B_PIECES + i) + (lane >> 3);
-    r = r < n_valid ? r : n_valid - 1;
-    b_off[i] = (uint32_t)r * (uint32_t)K + piece * 16;
-  }
-  const uint8_t* const a0 = uniform_ptr(a + row0 * K);
-  const uint8_t* const b0 = uniform_ptr(bt + col0 * K);
-  typedef __attribute__((address_space(3))) unsigned char lds_u8;
-  const uint32_t ring = (uint32_t)(uintptr_t)((lds_u8*)smem);
+  const int over = (KB - 1) * GK + piece * 16 + 16 - (int)K;
+  const uint32_t tail_back = over > 0 ? over : 0;
+  const bool partial = (K & 127) != 0;
+  const uint8_t* const sa0 = uniform_ptr(reinterpret_cast<const uint8_t*>(sa + row0 * KB));
 
-  auto issue = [&](int ks) __attribute__((always_inline)) {
-    const uint32_t slot = ring + (ks & 1) * STAGE;
-    const uint8_t* const ak = a0 + (int64_t)ks * GK;
-    const uint8_t* const bk = b0 + (int64_t)ks * GK;
-    if ((int64_t)(ks + 1) * GK <= K) {
+  auto issue = [&](int ks, int slot) __attribute__((always_inline)) {
+    const uint32_t back = ks == KB - 1 ? tail_back : 0u;
 #pragma unroll
-      for (int i = 0; i < A_PIECES; ++i) dma16_at(ak, a_off[i], slot + (w * A_PIECES + i) * 1024);
-#pragma unroll
-      for (int i = 0; i < B_PIECES; ++i) dma16_at(bk, b_off[i], slot + BM * GK + (w * B_PIECES + i) * 1024);
-    } else {
-      // the partial last K-block: pieces past K are zeros
-      const bool in = (int64_t)ks * GK + piece * 16 < K;
-      const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&g128_zeros);
-#pragma unroll
-      for (int i = 0; i < A_PIECES; ++i) dma16(in ? ak + a_off[i] : zero, slot + (w * A_PIECES + i) * 1024);
-#pragma unroll
-      for (int i = 0; i < B_PIECES; ++i)
-        dma16(in ? bk + b_off[i] : zero, slot + BM * GK + (w * B_PIECES + i) * 1024);
-    }
+    for (int i = 0; i < PIECES; ++i)
+      dma16_at(from[i] + (int64_t)ks * GK, off[i] - back, lds0 + slot * STAGE + (w + i * WAVES) * 1024);
   };
-
-  // ---- A's scales: item = (row, half of the chunk), four K-blocks each
-  float s_reg[S_ITEMS][4];
-  auto load_scales = [&](int chunk) __attribute__((always_inline)) {
-#pragma unroll
-    for (int n = 0; n < S_ITEMS; ++n) {
-      const int item = n * THREADS + threadIdx.x;
-      int r = (item >> 1) < m_valid ? item >> 1 : m_valid - 1;
-      const float* const p = sa + (row0 + r) * KB;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int kb = chunk * SCH + (item & 1) * 4 + x;
-        s_reg[n][x] = p[kb < KB ? kb : KB - 1];
-      }
-    }
-  };
-  auto place_scales = [&](int chunk) __attribute__((always_inline)) {
-#pragma unroll
-    for (int n = 0; n < S_ITEMS; ++n) {
-      const int item = n * THREADS + threadIdx.x;
-      const int r = item >> 1;
-      if (S_ITEMS * THREADS == 2 * BM || r < BM) {
-        // row r = 16*MI*band + 16*i + lane -> [band][lane][i]
-        const int at = r / (16 * MI) * (16 * MI) + (r & 15) * MI + (r % (16 * MI)) / 16;
-        float* const p = s_lds + ((chunk & 1) * SCH + (item & 1) * 4) * BM + at;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) p[x * BM] = s_reg[n][x];
-      }
-    }
+  auto issue_s = [&](int chunk, int p) __attribute__((always_inline)) {
+    const int r = p * 8 + (lane & 7), kb = chunk * SCH + (lane >> 3);
+    const uint32_t o = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                     lds0 + S * STAGE + (chunk & 1) * SBUF + (p >> 1) * SSUB + (p & 1) * 288),
+                 "v"(o * 4), "s"(sa0)
+                 : "memory");
   };
   const int64_t nb = (col0 + wn * 16 * NJ) >> 7;
   const float* const sb_row = sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB;
-  auto load_sb = [&](int ks) __attribute__((always_inline)) {
-    return sb_row[ks + lane < KB ? ks + lane : KB - 1];
+  auto load_sb = [&](int ks) __attribute__((always_inline)) -> int {
+    int v = __builtin_bit_cast(int, sb_row[ks + lane < KB ? ks + lane : KB - 1]);
+    asm volatile("" : "+v"(v));
+    return v;
   };
 
   v4f acc[MI][NJ];
@@ -183,48 +163,64 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto frag = [&](const unsigned char* base, int r) __attribute__((always_inline)) -> v8i_t {
-    const v4i p0 = *reinterpret_cast<const v4i*>(base + r * GK + 16 * (g ^ (lo & 7)));
-    const v4i p1 = *reinterpret_cast<const v4i*>(base + r * GK + 16 * ((4 + g) ^ (lo & 7)));
-    return v8i_t{p0[0], p0[1], p0[2], p0[3], p1[0], p1[1], p1[2], p1[3]};
-  };
-
-  float sb_now = 0.0f, sb_next = 0.0f;
   if (KB > 0) {
-    load_scales(0);
-    sb_now = load_sb(0);
-    place_scales(0);
-    issue(0);
-  }
-  for (int ks = 0; ks < KB; ++ks) {
-    wait_vmcnt<0>();  // step ks has landed
-    if ((ks & 7) == 4 && ks + 4 < KB) place_scales((ks >> 3) + 1);
-    lds_barrier();    // ... for every wave; step ks-1's slot is free
-    if ((ks & 7) == 0) {
-      if ((ks & 63) == 0 && ks > 0) sb_now = sb_next;
-      if (ks + 8 < KB) load_scales((ks >> 3) + 1);
-      if ((ks & 63) == 56) sb_next = load_sb(ks + 8);
-    }
-    if (ks + 1 < KB) issue(ks + 1);
-    if (wave_live) {
-      const unsigned char* const slot = smem + (ks & 1) * STAGE;
-      const float* const sp = s_lds + (((ks >> 3) & 1) * SCH + (ks & 7)) * BM + wm * 16 * MI + lo * MI;
-      const float sb = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb_now), ks & 63));
-      float sc[MI];
+    int sb_lanes = load_sb(0);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) sc[i] = sp[i] * sb;
-      v8i_t bf[NJ];
+    for (int q = 0; q < S_STEPS; ++q)
+      if (q * WAVES + w < S_PIECES) issue_s(0, q * WAVES + w);
+    for (int ks = 0; ks < S - 1 && ks < KB; ++ks) issue(ks, ks);
+
+    const int sw0 = 16 * (g ^ (lo & 7)), sw1 = 16 * ((4 + g) ^ (lo & 7));
+    const lds_u8* const ra = lds + (wm * 16 * MI + lo) * GK;
+    const lds_u8* const rb = lds + (BM + wn * 16 * NJ + lo) * GK;
+    const lds_u8* const rs = lds + S * STAGE + wm * MI * SSUB + (lo >> 3) * 288 + (lo & 7) * 4;
+    auto frag = [&](const lds_u8* base) __attribute__((always_inline)) -> v8i_t {
+      const v4i x = *(lds_v4i*)(base + sw0), y = *(lds_v4i*)(base + sw1);
+      return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    };
+
+    int slot = 0;
+#pragma unroll 1
+    for (int ks = 0; ks < KB; ++ks) {
+      if ((ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
+      wait_steps<S - 2, PIECES>(KB - 1 - ks);  // step ks has landed (scale loads only make it stricter)
+      lds_barrier();                           // ... for every wave; step ks-1's slot is free
+      const int free = slot == 0 ? S - 1 : slot - 1;
+      if ((ks & 7) < S_STEPS && (ks >> 3) < (KB - 1) >> 3 && (ks & 7) * WAVES + w < S_PIECES)
+        issue_s((ks >> 3) + 1, (ks & 7) * WAVES + w);
+      if (ks + S - 1 < KB) issue(ks + S - 1, free);
+      if (partial && ks == KB - 1) {
+        for (int x = threadIdx.x; x < (BM + BN) * 8; x += 64 * WAVES) {
+          const int r = x >> 3, p = x & 7;
+          if (p >= (int)(K & 127) >> 4)
+            *(lds_v4i_w*)(lds + slot * STAGE + r * GK + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
+        }
+        lds_barrier();
+      }
+      if (wave_live) {
+        const float sb =
+            __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb_lanes), ks & 63));
+        const lds_u8* const q = rs + ((ks >> 3) & 1) * SBUF + (ks & 7) * 32;
+        float sc[MI];
+        v8i_t bf[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) bf[j] = frag(slot + BM * GK, wn * 16 * NJ + 16 * j + lo);
+        for (int j = 0; j < NJ; ++j) bf[j] = frag(rb + slot * STAGE + 16 * j * GK);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const v8i_t af = frag(slot, wm * 16 * MI + 16 * i + lo);
+        for (int i = 0; i < MI; ++i) sc[i] = *(lds_f32*)(q + i * SSUB);
         v4f p[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) p[j] = mfma_block(bf[j], af);
+        for (int i = 0; i < MI; ++i) {
+          const v8i_t af = frag(ra + slot * STAGE + 16 * i * GK);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) promote(acc[i][j], p[j], sc[i]);
+          for (int j = 0; j < NJ; ++j) {
+            if (i > 0) promote(acc[i - 1][j], p[j], sc[i - 1] * sb);
+            p[j] = mfma_block(bf[j], af);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) promote(acc[MI - 1][j], p[j], sc[MI - 1] * sb);
       }
+      slot = slot == S - 1 ? 0 : slot + 1;
     }
   }
 
@@ -562,21 +558,21 @@ static hipError_t launch_big(const void* a, const float* sa, const void* bt, con
   return hipGetLastError();
 }
 
-template <int MI, int NJ, int WM, int WN>
+template <int MI, int NJ, int WM, int WN, int S>
 constexpr int tile_lds() {
-  return 2 * (16 * MI * WM + 16 * NJ * WN) * GK + 2 * SCH * 16 * MI * WM * 4;
+  return S * (16 * MI * WM + 16 * NJ * WN) * GK + 2 * MI * WM * 768;
 }
 
-template <int MI, int NJ, int WM, int WN>
+template <int MI, int NJ, int WM, int WN, int S>
 static hipError_t set_tile_attributes() {
-  hipError_t e = hipFuncSetAttribute((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, false>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds<MI, NJ, WM, WN>());
+  hipError_t e = hipFuncSetAttribute((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false>,
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds<MI, NJ, WM, WN, S>());
   if (e != hipSuccess) return e;
-  return hipFuncSetAttribute((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, true>,
-                             hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds<MI, NJ, WM, WN>());
+  return hipFuncSetAttribute((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, true>,
+                             hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds<MI, NJ, WM, WN, S>());
 }
 
-template <int MI, int NJ, int WM, int WN>
+template <int MI, int NJ, int WM, int WN, int S>
 static hipError_t launch_tile(const void* a, const float* sa, const void* bt, const float* sbt,
                               const int32_t* offsets, int G, void* c, int64_t M, int64_t N, int64_t K,
                               hipStream_t stream) {
@@ -587,13 +583,163 @@ static hipError_t launch_tile(const void* a, const float* sa, const void* bt, co
   if (tiles_m * tiles_n > (int64_t)0xFFFFFFFF / THREADS) return hipErrorNotSupported;
   const dim3 grid((unsigned)(tiles_m * tiles_n));
   if (offsets)
-    hipLaunchKernelGGL((gemm_g128_tile_kernel<MI, NJ, WM, WN, true>), grid, dim3(THREADS),
-                       (tile_lds<MI, NJ, WM, WN>()), stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt, offsets,
-                       G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+    hipLaunchKernelGGL((gemm_g128_tile_kernel<MI, NJ, WM, WN, S, true>), grid, dim3(THREADS),
+                       (tile_lds<MI, NJ, WM, WN, S>()), stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt,
+                       offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
   else
-    hipLaunchKernelGGL((gemm_g128_tile_kernel<MI, NJ, WM, WN, false>), grid, dim3(THREADS),
-                       (tile_lds<MI, NJ, WM, WN>()), stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt, offsets,
-                       G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+    hipLaunchKernelGGL((gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false>), grid, dim3(THREADS),
+                       (tile_lds<MI, NJ, WM, WN, S>()), stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt,
+                       offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+  return hipGetLastError();
+}
+
+// ---- few rows of a narrow weight: it is streamed once, straight to registers, by
+// workgroups of four waves that own 16 columns of C and all K, so that the few
+// columns still occupy every CU.
+//
+// The waves share K: wave w forms the products of K-blocks KC*r + w*U .. +U-1 of
+// round r (KC = 4*U) and puts them into LDS beside their scale products; after
+// one barrier the same threads add the round's KC products to their
+// accumulators in ascending order.  So many K-blocks are in flight at once, yet
+// an element's sequence of operations is that of the tiles, whatever M is.  The
+// next round's loads are issued before the round's products are formed.
+template <int MT, int U>
+__global__ void __launch_bounds__(256) gemm_g128_rows_kernel(const uint8_t* __restrict__ a,
+                                                             const float* __restrict__ sa,
+                                                             const uint8_t* __restrict__ bt,
+                                                             const float* __restrict__ sbt,
+                                                             uint16_t* __restrict__ c, int64_t M, int64_t N,
+                                                             int64_t K) {
+  constexpr int KC = 4 * U;
+  constexpr int SL = (MT * U + 3) / 4;  // scale products per lane and round
+  __shared__ __attribute__((aligned(16))) float part[2][KC][MT * 256];
+  __shared__ float sprod[2][KC][16 * MT];
+  const int lane = threadIdx.x & 63;
+  const int w = wave_id_uniform();
+  const int g = lane >> 4, lo = lane & 15;
+  const int KB = (int)((K + 127) >> 7);
+  const bool partial = (K & 127) != 0;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int rounds = (KB + KC - 1) / KC;
+  const int last = (int)K - 16;  // K offset of the last whole piece
+  const uint8_t* const bp = bt + (n0 + lo) * K;
+  const float* const sbp = sbt + (n0 >> 7) * KB;
+  const uint8_t* ap[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) ap[i] = a + (16 * i + lo < M ? 16 * i + lo : M - 1) * K;
+
+  struct Set {
+    v4i b[U][2], a[U][MT][2];
+    float sa[SL], sb[SL];
+  };
+  // Loads past the last K-block repeat it and are not used; pieces past K read the
+  // last whole piece and are replaced by zeros.
+  auto load = [&](Set& s, int r) __attribute__((always_inline)) {
+    const int kb0 = r * KC + w * U;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = kb0 + u < KB ? kb0 + u : KB - 1;
+      int o0 = kb * GK + 16 * g, o1 = o0 + 64;
+      o0 = o0 < last ? o0 : last;
+      o1 = o1 < last ? o1 : last;
+      s.b[u][0] = *reinterpret_cast<const v4i*>(bp + o0);
+      s.b[u][1] = *reinterpret_cast<const v4i*>(bp + o1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        s.a[u][i][0] = *reinterpret_cast<const v4i*>(ap[i] + o0);
+        s.a[u][i][1] = *reinterpret_cast<const v4i*>(ap[i] + o1);
+      }
+    }
+    // scale product x of the lane: K-block u and row sub-tile i with u*MT + i = 4x + g
+#pragma unroll
+    for (int x = 0; x < SL; ++x) {
+      const int ui = 4 * x + g < MT * U ? 4 * x + g : MT * U - 1;
+      const int kb = kb0 + ui / MT < KB ? kb0 + ui / MT : KB - 1;
+      const int64_t row = 16 * (ui % MT) + lo;
+      s.sa[x] = sa[(row < M ? row : M - 1) * KB + kb];
+      s.sb[x] = sbp[kb];
+    }
+  };
+  auto products = [&](Set& s, int r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = r * KC + w * U + u;
+      if (partial && kb == KB - 1) {
+        const v4i z = {0, 0, 0, 0};
+        const bool in0 = kb * GK + 16 * g < K, in1 = kb * GK + 64 + 16 * g < K;
+        s.b[u][0] = in0 ? s.b[u][0] : z;
+        s.b[u][1] = in1 ? s.b[u][1] : z;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          s.a[u][i][0] = in0 ? s.a[u][i][0] : z;
+          s.a[u][i][1] = in1 ? s.a[u][i][1] : z;
+        }
+      }
+      auto join = [](v4i x, v4i y) __attribute__((always_inline)) {
+        return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      };
+      const v8i_t bf = join(s.b[u][0], s.b[u][1]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        *reinterpret_cast<v4f*>(&part[r & 1][w * U + u][i * 256 + lane * 4]) =
+            mfma_block(bf, join(s.a[u][i][0], s.a[u][i][1]));
+    }
+#pragma unroll
+    for (int x = 0; x < SL; ++x) {
+      const int ui = 4 * x + g;
+      if (MT * U % 4 == 0 || ui < MT * U) sprod[r & 1][w * U + ui / MT][16 * (ui % MT) + lo] = s.sa[x] * s.sb[x];
+    }
+  };
+
+  // thread t owns elements t*MT .. +MT-1 of the MT x 64 lanes x 4 results
+  const int e = threadIdx.x * MT;
+  const int row = (e >> 8) * 16 + ((e >> 2) & 15), col = ((e >> 6) & 3) * 4 + (e & 3);
+  float acc[MT];
+#pragma unroll
+  for (int x = 0; x < MT; ++x) acc[x] = 0.0f;
+  auto chain = [&](int r) __attribute__((always_inline)) {
+    const int n = KB - r * KC < KC ? KB - r * KC : KC;
+    auto add = [&](int k) __attribute__((always_inline)) {
+      const float s = sprod[r & 1][k][row];
+#pragma unroll
+      for (int x = 0; x < MT; ++x) acc[x] = __builtin_fmaf(part[r & 1][k][e + x], s, acc[x]);
+    };
+    if (n == KC) {
+#pragma unroll
+      for (int k = 0; k < KC; ++k) add(k);
+    } else {
+      for (int k = 0; k < n; ++k) add(k);
+    }
+  };
+
+  // A round writes the LDS half that the round before the last one was read from:
+  // every thread has passed the barrier between them.
+  Set s0, s1;
+  load(s0, 0);
+  for (int r = 0; r < rounds; r += 2) {
+    load(s1, r + 1);
+    products(s0, r);
+    __syncthreads();
+    chain(r);
+    if (r + 1 < rounds) {
+      load(s0, r + 2);
+      products(s1, r + 1);
+      __syncthreads();
+      chain(r + 1);
+    }
+  }
+  if (row < M) {
+    uint16_t* const cp = c + row * N + n0 + col;
+    if constexpr (MT == 1) *cp = (uint16_t)bf16_pair(acc[0], 0.0f);
+    else *reinterpret_cast<uint32_t*>(cp) = bf16_pair(acc[0], acc[1]);
+  }
+}
+
+template <int MT, int U>
+static hipError_t launch_rows(const void* a, const float* sa, const void* bt, const float* sbt, void* c, int64_t M,
+                              int64_t N, int64_t K, hipStream_t stream) {
+  hipLaunchKernelGGL((gemm_g128_rows_kernel<MT, U>), dim3((unsigned)(N / 16)), dim3(256), 0, stream,
+                     (const uint8_t*)a, sa, (const uint8_t*)bt, sbt, (uint16_t*)c, M, N, K);
   return hipGetLastError();
 }
 
@@ -603,18 +749,53 @@ hipError_t set_gemm_g128_attributes() {
   if (e == hipSuccess)
     e = hipFuncSetAttribute((const void*)gemm_g128_big_kernel<true>, hipFuncAttributeMaxDynamicSharedMemorySize,
                             X_LDS);
-  if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 2>();
-  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2>();
+  if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 2, 2>();
+  if (e == hipSuccess) e = set_tile_attributes<2, 4, 2, 2, 2>();
+  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2, 2>();
+  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2, 4>();
+  if (e == hipSuccess) e = set_tile_attributes<1, 2, 2, 2, 4>();
+  if (e == hipSuccess) e = set_tile_attributes<1, 1, 2, 2, 4>();
   return e;
 }
 
+// The kernel is the largest tile that still gives the 256 CUs enough workgroups:
+// a larger tile moves fewer bytes per flop, but tiles that do not fill the chip
+// leave CUs idle (M x N x K, us):
+//   512 x 8192 x 8192    64x128 48   128x128 (256 tiles) 54
+//   1024 x 8192 x 8192   128x128 77  256x256 (128 tiles) 83   64x128 99
+//   512 x 28672 x 8192   256x256 (224 tiles) 110  128x128 156
+//   256 x 8192 x 8192    64x64 35    64x128 (256 tiles) 39
+//   128 x 8192 x 8192    32x64 28    64x64 (256 tiles) 34
+//   64 x 4096 x 4096     32x32 12    32x64 (128 tiles) 13
+// For ranges the count goes by their average, and a tile is not chosen much taller
+// than that: its rows past a range's end are work for nothing (64 ranges of 8
+// rows, N = 4096, K = 2048: 32x64 93, 128x128 over 110; 16 ranges of 56, K = 7168:
+// 128x128 91, 64x128 98; 16 of 125, K = 2048: 256x256 37, 128x128 41).
+// Few rows of a narrow weight give too few tiles altogether (16 x 4096 x 4096: rows
+// 7.4, 32x32 11; 32 x 2048 x 7168: 14, 19), a wide weight enough (16 x 28672 x
+// 8192: rows 56, 32x64 48).  With one row tile the call is bound by the weight's
+// stream and a deeper ring pays (64 x 28672 x 8192: 64x64 with four steps 55,
+// with two 61; 1024 x 2064 x 1552, bound by compute and occupancy: 18 and 12).
 hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-  const int64_t avg = (M + G - 1) / G;  // rows per range
-  auto tiles = [&](int64_t b) { return G * ((avg + b - 1) / b) * ((N + b - 1) / b); };
-  if (tiles(256) >= 256) return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (tiles(128) >= 256) return launch_tile<4, 4, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  return launch_tile<2, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (!offsets && K > 0) {
+    if (M <= 16 && N <= 8192) return launch_rows<1, 2>(a, sa, bt, sbt, c, M, N, K, stream);
+    if (M <= 32 && N <= 4096) return launch_rows<2, 1>(a, sa, bt, sbt, c, M, N, K, stream);
+  }
+  const int64_t live = G < M ? G : M;           // ranges that can have rows
+  const int64_t avg = (M + live - 1) / live;    // rows of one
+  auto tiles = [&](int64_t bm, int64_t bn) { return live * ((avg + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  if (avg >= 112 && tiles(256, 256) >= 200) return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 40 && tiles(128, 128) > 256)
+    return launch_tile<4, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 20 && tiles(64, 128) > 256)
+    return launch_tile<2, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 20 && tiles(64, 64) > 256) {
+    if (avg <= 64) return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<2, 2, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  }
+  if (tiles(32, 64) >= 200) return launch_tile<1, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  return launch_tile<1, 1, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
 }
 
 }  // namespace fp8bs

@@ -22,5 +22,6 @@ __all__ = list(_BINDING_NAMES)
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)  # found without this function from now on
+        return value
     raise AttributeError(name)

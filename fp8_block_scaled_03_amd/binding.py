@@ -443,45 +443,56 @@ def gemm_e8m0_nt(a: torch.Tensor, ea: torch.Tensor, bt: torch.Tensor, ebt: torch
 
 # ---- scales of 128 values (include/fp8bs_g128.h) -------------------------------------------
 GROUP = 128
+_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
 
 
 def _blocks128(n: int) -> int:
     return (n + GROUP - 1) // GROUP
 
 
-def _call_on(t: torch.Tensor, raw, *args) -> None:
-    """One library call on the current stream of t's device, whichever device is current."""
-    index = t.device.index
+def _call_on(device: torch.device, name: str, *args) -> None:
+    """One library call on the current stream of ``device``, whichever device is current."""
+    fn = getattr(_lib or load_library(), name)
+    index = device.index
     if index == torch.cuda.current_device():
-        _check(raw(*args, _stream_ptr(t)))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            _check(raw(*args, _stream_ptr(t)))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _check(status)
 
 
-def _output(t: torch.Tensor | None, name: str, shape, dtypes, device) -> torch.Tensor:
-    """The caller's output, checked, or a new one of the first of `dtypes`."""
-    if t is None:
-        return torch.empty(shape, dtype=dtypes[0] if isinstance(dtypes, tuple) else dtypes, device=device)
-    _need(t, name, dtypes, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _need_like(t: torch.Tensor, name: str, dtypes, shape: tuple, device: torch.device) -> torch.Tensor:
+    """t, which must be contiguous and of the given type, shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not accepted ({dtypes})")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError("all tensors must be on the same device")
     return t
 
 
-def _need_shape(t: torch.Tensor, name: str, shape) -> None:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _output(t: torch.Tensor | None, name: str, dtypes, shape: tuple, device: torch.device) -> torch.Tensor:
+    """The caller's output, checked, or a new one of the first of ``dtypes``."""
+    if t is None:
+        return torch.empty(shape, dtype=dtypes[0], device=device)
+    return _need_like(t, name, dtypes, shape, device)
 
 
 def quantize_tg128(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.Tensor | None = None):
     """bf16 [R, C] -> (E4M3 codes uint8 [R, C], fp32 scales [R, ceil(C/128)], one per row and 128 columns)."""
-    _need(x, "x", torch.bfloat16, 2)
+    _need(x, "x", _BF16, 2)
     R, C = x.shape
-    q = _output(q, "q", (R, C), E4M3_DTYPES, x.device)
-    scales = _output(scales, "scales", (R, _blocks128(C)), torch.float32, x.device)
-    _same_device(x, q, scales)
-    _call_on(x, quantize_tg128_raw, _ptr(x), R, C, _ptr(q), _ptr(scales))
+    dev = x.device
+    q = _output(q, "q", E4M3_DTYPES, (R, C), dev)
+    scales = _output(scales, "scales", _F32, (R, _blocks128(C)), dev)
+    _call_on(dev, "fp8bs_quantize_tg128", _ptr(x), R, C, _ptr(q), _ptr(scales))
     return q, scales
 
 
@@ -494,22 +505,20 @@ def quantize_b128(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.
     and scales [(G,) ceil(C/128), ceil(R/128)], as third and fourth elements."""
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
         raise ValueError("x must be a tensor of 2 or 3 dimensions")
-    _need(x, "x", torch.bfloat16, x.dim())
+    _need(x, "x", _BF16, x.dim())
     lead = tuple(x.shape[:-2])
     R, C = x.shape[-2:]
     G = lead[0] if lead else 1
+    dev = x.device
     if (qt is None) != (scales_t is None):
         raise ValueError("qt and scales_t go together")
     transposed = transposed or qt is not None
-    q = _output(q, "q", tuple(x.shape), E4M3_DTYPES, x.device)
-    scales = _output(scales, "scales", lead + (_blocks128(R), _blocks128(C)), torch.float32, x.device)
+    q = _output(q, "q", E4M3_DTYPES, lead + (R, C), dev)
+    scales = _output(scales, "scales", _F32, lead + (_blocks128(R), _blocks128(C)), dev)
     if transposed:
-        qt = _output(qt, "qt", lead + (C, R), E4M3_DTYPES, x.device)
-        scales_t = _output(scales_t, "scales_t", lead + (_blocks128(C), _blocks128(R)), torch.float32, x.device)
-        _same_device(x, q, scales, qt, scales_t)
-    else:
-        _same_device(x, q, scales)
-    _call_on(x, quantize_b128_raw, _ptr(x), G, R, C, _ptr(q), _ptr(scales), _ptr(qt), _ptr(scales_t))
+        qt = _output(qt, "qt", E4M3_DTYPES, lead + (C, R), dev)
+        scales_t = _output(scales_t, "scales_t", _F32, lead + (_blocks128(C), _blocks128(R)), dev)
+    _call_on(dev, "fp8bs_quantize_b128", _ptr(x), G, R, C, _ptr(q), _ptr(scales), _ptr(qt), _ptr(scales_t))
     return (q, scales, qt, scales_t) if transposed else (q, scales)
 
 
@@ -518,16 +527,13 @@ def gemm_tg128_nt(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, sbt: torc
     """E4M3 a [M, K], sa [M, ceil(K/128)], K-major weight bt [N, K], sbt [ceil(N/128), ceil(K/128)] -> bf16 [M, N]."""
     _need(a, "a", E4M3_DTYPES, 2)
     _need(bt, "bt", E4M3_DTYPES, 2)
-    _need(sa, "sa", torch.float32, 2)
-    _need(sbt, "sbt", torch.float32, 2)
     M, K = a.shape
-    N = bt.shape[0]
-    _need_shape(bt, "bt", (N, K))
-    _need_shape(sa, "sa", (M, _blocks128(K)))
-    _need_shape(sbt, "sbt", (_blocks128(N), _blocks128(K)))
-    out = _output(out, "out", (M, N), torch.bfloat16, a.device)
-    _same_device(a, sa, bt, sbt, out)
-    _call_on(a, gemm_tg128_nt_raw, _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(out), M, N, K)
+    N, KB, dev = bt.shape[0], _blocks128(K), a.device
+    _need_like(bt, "bt", E4M3_DTYPES, (N, K), dev)
+    _need_like(sa, "sa", _F32, (M, KB), dev)
+    _need_like(sbt, "sbt", _F32, (_blocks128(N), KB), dev)
+    out = _output(out, "out", _BF16, (M, N), dev)
+    _call_on(dev, "fp8bs_gemm_tg128_nt", _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(out), M, N, K)
     return out
 
 
@@ -539,19 +545,16 @@ def grouped_gemm_tg128_nt(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, s
     Rows outside every range keep what ``out`` holds (a new ``out`` is not initialised)."""
     _need(a, "a", E4M3_DTYPES, 2)
     _need(bt, "bt", E4M3_DTYPES, 3)
-    _need(sa, "sa", torch.float32, 2)
-    _need(sbt, "sbt", torch.float32, 3)
-    _need(offsets, "offsets", torch.int32, 1)
     M, K = a.shape
     G, N = bt.shape[:2]
-    _need_shape(bt, "bt", (G, N, K))
-    _need_shape(offsets, "offsets", (G + 1,))
-    _need_shape(sa, "sa", (M, _blocks128(K)))
-    _need_shape(sbt, "sbt", (G, _blocks128(N), _blocks128(K)))
-    out = _output(out, "out", (M, N), torch.bfloat16, a.device)
-    _same_device(a, sa, bt, sbt, offsets, out)
-    _call_on(a, grouped_gemm_tg128_nt_raw, _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(offsets), G, _ptr(out), M, N,
-             K)
+    KB, dev = _blocks128(K), a.device
+    _need_like(bt, "bt", E4M3_DTYPES, (G, N, K), dev)
+    _need_like(offsets, "offsets", _I32, (G + 1,), dev)
+    _need_like(sa, "sa", _F32, (M, KB), dev)
+    _need_like(sbt, "sbt", _F32, (G, _blocks128(N), KB), dev)
+    out = _output(out, "out", _BF16, (M, N), dev)
+    _call_on(dev, "fp8bs_grouped_gemm_tg128_nt", _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(offsets), G, _ptr(out),
+             M, N, K)
     return out
 
 
@@ -559,20 +562,20 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
                   accumulate: bool = False):
     """bf16 dy [M_total, N], x [M_total, K], offsets int32 [G+1] on the device -> fp32 [G, N, K], the sums of
     dy[m, n] * x[m, k] over each range's rows; with ``accumulate`` they are added to ``out``."""
-    _need(dy, "dy", torch.bfloat16, 2)
-    _need(x, "x", torch.bfloat16, 2)
-    _need(offsets, "offsets", torch.int32, 1)
+    _need(dy, "dy", _BF16, 2)
+    _need(x, "x", _BF16, 2)
+    _need(offsets, "offsets", _I32, 1)
     M, N = dy.shape
-    K = x.shape[1]
-    G = offsets.shape[0] - 1
-    _need_shape(x, "x", (M, K))
+    K, G, dev = x.shape[1], offsets.shape[0] - 1, dy.device
     if G < 1:
         raise ValueError("offsets needs at least two entries")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    out = _output(out, "out", (G, N, K), torch.float32, dy.device)
-    _same_device(dy, x, offsets, out)
-    _call_on(dy, grouped_wgrad_raw, _ptr(dy), _ptr(x), _ptr(offsets), G, _ptr(out), 1 if accumulate else 0, M, N, K)
+    _need_like(x, "x", _BF16, (M, K), dev)
+    _need_like(offsets, "offsets", _I32, (G + 1,), dev)
+    out = _output(out, "out", _F32, (G, N, K), dev)
+    _call_on(dev, "fp8bs_grouped_wgrad", _ptr(dy), _ptr(x), _ptr(offsets), G, _ptr(out), 1 if accumulate else 0, M, N,
+             K)
     return out
 
 
@@ -581,18 +584,16 @@ def swiglu_quantize_tg128(gu: torch.Tensor, q: torch.Tensor | None = None, scale
     """bf16 [R, 2d] = [gate | up] -> silu(gate) * up, quantized as by quantize_tg128 from its fp32 values:
     (q uint8 [R, d], scales fp32 [R, ceil(d/128)]), plus the bf16 values [R, d] as a third element when
     ``want_y`` is true or ``y`` is given."""
-    _need(gu, "gu", torch.bfloat16, 2)
+    _need(gu, "gu", _BF16, 2)
     R, d2 = gu.shape
     if d2 % 2:
         raise ValueError("gu needs an even number of columns")
-    d = d2 // 2
-    q = _output(q, "q", (R, d), E4M3_DTYPES, gu.device)
-    scales = _output(scales, "scales", (R, _blocks128(d)), torch.float32, gu.device)
+    d, dev = d2 // 2, gu.device
+    q = _output(q, "q", E4M3_DTYPES, (R, d), dev)
+    scales = _output(scales, "scales", _F32, (R, _blocks128(d)), dev)
     if y is not None or want_y:
-        y = _output(y, "y", (R, d), torch.bfloat16, gu.device)
-        _same_device(gu, y)
-    _same_device(gu, q, scales)
-    _call_on(gu, swiglu_quantize_tg128_raw, _ptr(gu), R, d, _ptr(q), _ptr(scales), _ptr(y))
+        y = _output(y, "y", _BF16, (R, d), dev)
+    _call_on(dev, "fp8bs_swiglu_quantize_tg128", _ptr(gu), R, d, _ptr(q), _ptr(scales), _ptr(y))
     return (q, scales) if y is None else (q, scales, y)
 
 
@@ -602,17 +603,16 @@ def swiglu_backward_quantize_tg128(gu: torch.Tensor, dy: torch.Tensor, dgu: torc
     """The gradient of silu(gate) * up for bf16 gu [R, 2d] and dy [R, d]: (dgu bf16 [R, 2d], its codes uint8
     [R, 2d] and scales fp32 [R, ceil(2d/128)] as by quantize_tg128 from the fp32 values), plus the forward
     value bf16 [R, d] as a fourth element when ``want_y`` is true or ``y`` is given."""
-    _need(gu, "gu", torch.bfloat16, 2)
-    _need(dy, "dy", torch.bfloat16, 2)
+    _need(gu, "gu", _BF16, 2)
+    _need(dy, "dy", _BF16, 2)
     R, d = dy.shape
-    _need_shape(gu, "gu", (R, 2 * d))
-    dgu = _output(dgu, "dgu", (R, 2 * d), torch.bfloat16, gu.device)
-    q = _output(q, "q", (R, 2 * d), E4M3_DTYPES, gu.device)
-    scales = _output(scales, "scales", (R, _blocks128(2 * d)), torch.float32, gu.device)
+    dev = dy.device
+    _need_like(gu, "gu", _BF16, (R, 2 * d), dev)
+    dgu = _output(dgu, "dgu", _BF16, (R, 2 * d), dev)
+    q = _output(q, "q", E4M3_DTYPES, (R, 2 * d), dev)
+    scales = _output(scales, "scales", _F32, (R, _blocks128(2 * d)), dev)
     if y is not None or want_y:
-        y = _output(y, "y", (R, d), torch.bfloat16, gu.device)
-        _same_device(gu, y)
-    _same_device(gu, dy, dgu, q, scales)
-    _call_on(gu, swiglu_backward_quantize_tg128_raw, _ptr(gu), _ptr(dy), R, d, _ptr(dgu), _ptr(q), _ptr(scales),
+        y = _output(y, "y", _BF16, (R, d), dev)
+    _call_on(dev, "fp8bs_swiglu_backward_quantize_tg128", _ptr(gu), _ptr(dy), R, d, _ptr(dgu), _ptr(q), _ptr(scales),
              _ptr(y))
     return (dgu, q, scales) if y is None else (dgu, q, scales, y)

@@ -45,13 +45,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));
 }
 
-// Direct global->LDS load of 16 bytes per lane from a uniform base plus a
-// 32-bit offset per lane.
-__device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(off), "s"(base)
-               : "memory");
-}
-
 // ---- small and middle tiles: BM = 16*MI*WM rows by BN = 16*NJ*WN columns per
 // workgroup of WM x WN waves; wave (wm, wn) owns MI x NJ sub-tiles of 16x16.
 //
@@ -61,17 +54,6 @@ __device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint
 // piece p at position p ^ (r & 7), which spreads a fragment read over all
 // banks.  A's scales come eight K-blocks at a time, one or
 // two such chunks ahead; a weight scale is one value per wave and step, held by lane l for step 64c + l.
-// Waits until at most min(ahead, MOST) steps of P loads are in flight.
-template <int MOST, int P>
-__device__ __forceinline__ void wait_steps(int ahead) {
-  if constexpr (MOST == 0) {
-    wait_vmcnt<0>();
-  } else {
-    if (ahead >= MOST) wait_vmcnt<MOST * P>();
-    else wait_steps<MOST - 1, P>(ahead);
-  }
-}
-
 template <int MI, int NJ, int WM, int WN, int S, bool GROUPED>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,

@@ -1,4 +1,5 @@
-// Ragged row ranges: which rows and columns a workgroup's tile covers.
+// Ragged row ranges: which rows and columns a workgroup's tile covers; and the loads and
+// waits of LDS rings.
 #pragma once
 #include "common.hpp"
 
@@ -115,6 +116,25 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
     before = __shfl(upto, 63, 64);
   }
   return false;
+}
+
+// ---- rings of direct loads -------------------------------------------------------
+// Direct global->LDS load of 16 bytes per lane from a uniform base plus a
+// 32-bit offset per lane.
+__device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(off), "s"(base)
+               : "memory");
+}
+
+// Waits until at most min(ahead, MOST) steps of P loads are in flight.
+template <int MOST, int P>
+__device__ __forceinline__ void wait_steps(int ahead) {
+  if constexpr (MOST == 0) {
+    wait_vmcnt<0>();
+  } else {
+    if (ahead >= MOST) wait_vmcnt<MOST * P>();
+    else wait_steps<MOST - 1, P>(ahead);
+  }
 }
 
 }  // namespace fp8bs

@@ -17,13 +17,14 @@ namespace fp8bs {
 
 constexpr int WT = 32;  // rows (of dY and X) per step: the depth of one bf16 MFMA
 
-__device__ const uint4 wgrad_zeros = {0, 0, 0, 0};
-
 // LDS stage of one operand: WT rows of COLS bf16; the 32-byte chunk J of row r
 // lies at chunk J ^ sw(r).  A transpose read takes 32 bytes of four rows per
 // 16 lanes and of rows eight apart per neighbouring 16 lanes; sw puts these
-// eight on different banks.
-__device__ __forceinline__ int wg_sw(int r) { return (r & 3) | ((r >> 3) & 1) << 2; }
+// eight on different banks (a row of 64 columns has only four chunks: there the
+// four rows lie on different banks).
+__device__ __forceinline__ constexpr int wg_sw(int r, int cols) {
+  return (r & 3) | (cols >= 128 ? ((r >> 3) & 1) << 2 : 0);
+}
 
 // A tile of BK = 16*MI*WK columns of X by BN = 16*NJ*WN columns of dY per
 // workgroup of WK x WN waves; ring of S stages of WT rows.
@@ -38,6 +39,7 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   constexpr int X_BYTES = WT * BK * 2, STAGE = WT * (BK + BN) * 2;
   constexpr int X_PIECES = X_BYTES / 1024 / WAVES, Y_PIECES = WT * BN * 2 / 1024 / WAVES;
   static_assert(X_PIECES * WAVES * 1024 == X_BYTES && Y_PIECES * WAVES * 1024 == WT * BN * 2, "whole loads");
+  static_assert(MI % 2 == 0 && BK >= 64 && BN >= 64, "the swizzle and the epilogue's pairs");
   constexpr int PIECES = X_PIECES + Y_PIECES;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
 
@@ -45,10 +47,12 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   const int w = wave_id_uniform();
   const int wk = w / WN, wn = w % WN;
   const uint32_t per_group = tiles_n * tiles_k;
-  const uint32_t lin = xcd_run(blockIdx.x, gridDim.x);
-  const int gi = __builtin_amdgcn_readfirstlane(lin / per_group);
+  // Range by range, each one's tiles over all XCDs: ranges differ in rows, and an
+  // XCD with a run of long ones would finish last (16 uneven ranges of 32768 rows,
+  // 4096 x 2048: 707 us with runs over all tiles, 519 so).
+  const int gi = __builtin_amdgcn_readfirstlane(blockIdx.x / per_group);
   uint32_t tk, tn;
-  band_walk(lin - gi * per_group, tiles_k, tiles_n, tk, tn);
+  band_walk(xcd_run(blockIdx.x - gi * per_group, per_group), tiles_k, tiles_n, tk, tn);
   int64_t begin, end;
   range_of(offsets, gi, M, begin, end);
   begin = uniform64(begin);
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   auto source = [&](int p, int cols, int valid, int64_t ld, uint32_t& off, int& row) __attribute__((always_inline)) {
     const int byte = p * 1024 + lane * 16;
     row = byte / (cols * 2);
-    const int chunk = (byte % (cols * 2)) / 32 ^ wg_sw(row);
+    const int chunk = (byte % (cols * 2)) / 32 ^ wg_sw(row, cols);
     int col = chunk * 16 + (lane & 1) * 8;
     col = col < valid ? col : valid - 8;
     off = (uint32_t)row * (uint32_t)(ld * 2) + col * 2;
@@ -83,12 +87,8 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
   const uint32_t ring = (uint32_t)(uintptr_t)((lds_u8*)smem);
 
-  auto dma_at = [](const uint8_t* base, uint32_t off, uint32_t lds_base) __attribute__((always_inline)) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(off), "s"(base)
-                 : "memory");
-  };
-  // Steps past the last one load zeros into a slot that is never read, so that
-  // every wave always has the same number of loads in flight.
+  // In the last step the rows past the range read its last row; their LDS bytes
+  // are cleared before they are used.
   auto issue = [&](int t) __attribute__((always_inline)) {
     const uint32_t slot = ring + (t % S) * STAGE;
     const uint8_t* const xt = x0 + (int64_t)t * WT * K * 2;
@@ -96,29 +96,38 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
     const int left = rows - t * WT;
     if (left >= WT) {
 #pragma unroll
-      for (int i = 0; i < X_PIECES; ++i) dma_at(xt, x_off[i], slot + (w * X_PIECES + i) * 1024);
+      for (int i = 0; i < X_PIECES; ++i) dma16_at(xt, x_off[i], slot + (w * X_PIECES + i) * 1024);
 #pragma unroll
-      for (int i = 0; i < Y_PIECES; ++i) dma_at(yt, y_off[i], slot + X_BYTES + (w * Y_PIECES + i) * 1024);
+      for (int i = 0; i < Y_PIECES; ++i) dma16_at(yt, y_off[i], slot + X_BYTES + (w * Y_PIECES + i) * 1024);
     } else {
-      // rows past the range are zeros
-      const uint8_t* const zero = reinterpret_cast<const uint8_t*>(&wgrad_zeros);
 #pragma unroll
-      for (int i = 0; i < X_PIECES; ++i)
-        dma16(x_row[i] < left ? xt + x_off[i] : zero, slot + (w * X_PIECES + i) * 1024);
+      for (int i = 0; i < X_PIECES; ++i) {
+        const int back = x_row[i] < left ? 0 : x_row[i] - left + 1;
+        dma16_at(xt, x_off[i] - (uint32_t)back * (uint32_t)(K * 2), slot + (w * X_PIECES + i) * 1024);
+      }
 #pragma unroll
-      for (int i = 0; i < Y_PIECES; ++i)
-        dma16(y_row[i] < left ? yt + y_off[i] : zero, slot + X_BYTES + (w * Y_PIECES + i) * 1024);
+      for (int i = 0; i < Y_PIECES; ++i) {
+        const int back = y_row[i] < left ? 0 : y_row[i] - left + 1;
+        dma16_at(yt, y_off[i] - (uint32_t)back * (uint32_t)(N * 2), slot + X_BYTES + (w * Y_PIECES + i) * 1024);
+      }
     }
+  };
+  auto clear_rows = [&](int t) __attribute__((always_inline)) {
+    const int left = rows - t * WT;
+    unsigned char* const slot = smem + (t % S) * STAGE;
+    for (int b = left * BK * 2 + (int)threadIdx.x * 16; b < X_BYTES; b += 64 * WAVES * 16)
+      *reinterpret_cast<v4i*>(slot + b) = v4i{0, 0, 0, 0};
+    for (int b = left * BN * 2 + (int)threadIdx.x * 16; b < WT * BN * 2; b += 64 * WAVES * 16)
+      *reinterpret_cast<v4i*>(slot + X_BYTES + b) = v4i{0, 0, 0, 0};
   };
 
   // ---- fragments.  Lane (g, r, c) = (lane >> 4, (lane >> 2) & 3, lane & 3) reads 8
   // bytes of row 8g + 4h + r (h = 0, 1), columns 4c.. of the sub-tile's 16; it
-  // receives rows 8g + 4h .. + 3 of column lane & 15.  The row's swizzle is
-  // r | (g & 1) << 2 for both h, so sub-tile J is at chunk J ^ that.
+  // receives rows 8g + 4h .. + 3 of column lane & 15.  Both rows have the swizzle
+  // of row 8g + r, so sub-tile J is at chunk J ^ that.
   const int tg = lane >> 4, tr = (lane >> 2) & 3, tc = lane & 3;
-  const int sw = tr | (tg & 1) << 2;
   auto frag = [&](const unsigned char* base, int cols, int J) __attribute__((always_inline)) -> v8bf {
-    const unsigned char* const p = base + (8 * tg + tr) * cols * 2 + ((J ^ sw) << 5) + tc * 8;
+    const unsigned char* const p = base + (8 * tg + tr) * cols * 2 + ((J ^ wg_sw(8 * tg + tr, cols)) << 5) + tc * 8;
     const v4s h0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(p));
     const v4s h1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s_t*)(p + 4 * cols * 2));
     const v2i a = __builtin_bit_cast(v2i, h0), b = __builtin_bit_cast(v2i, h1);
@@ -131,14 +140,16 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  if (steps > 0) {
-#pragma unroll
-    for (int t = 0; t < S - 1; ++t) issue(t);
-  }
+  for (int t = 0; t < S - 1 && t < steps; ++t) issue(t);
+#pragma unroll 1
   for (int t = 0; t < steps; ++t) {
-    wait_vmcnt<PIECES*(S - 2)>();  // step t has landed
-    lds_barrier();                 // ... for every wave; step t-1's slot is free
-    issue(t + S - 1);
+    wait_steps<S - 2, PIECES>(steps - 1 - t);  // step t has landed
+    lds_barrier();                             // ... for every wave; step t-1's slot is free
+    if (t + S - 1 < steps) issue(t + S - 1);
+    if (t == steps - 1 && rows % WT) {
+      clear_rows(t);
+      lds_barrier();
+    }
     const unsigned char* const slot = smem + (t % S) * STAGE;
     v8bf yf[NJ];
 #pragma unroll
@@ -147,31 +158,45 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
     for (int i = 0; i < MI; ++i) {
       const v8bf xf = frag(slot, BK, wk * MI + i);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, yf[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, yf[j], acc[i][j], 0, 0, 0);
     }
   }
-  wait_vmcnt<0>();
 
-  // ---- lane holds n = 16j + (lane & 15), k = 16i + 4g .. +3 of its wave's part
+  // ---- lane (tg, lo) holds n = 16j + lo, k = 16i + 4 tg .. +3 of its wave's part: 64
+  // bytes of 16 rows per store.  Lanes lo and lo ^ 8 exchange one of two
+  // neighbouring sub-tiles i, so that a store covers 128 bytes of eight rows,
+  // and whole lines leave with a non-temporal hint (nothing here reads them
+  // again): 16 ranges of 512 rows, 4096 x 2048, 316 -> 228 us (the hint alone 251,
+  // the exchange alone 310).
   if (accumulate && rows == 0) return;
   const int lo = lane & 15;
+  const bool low = lo < 8;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int n = (wn * NJ + j) * 16 + lo;
-    if (n < n_valid) {
-      float* const row = dw + (n0 + n) * K + k0;
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int k = (wk * MI + i) * 16 + 4 * tg;
-        if (k < k_valid) {
-          v4f* const p = reinterpret_cast<v4f*>(row + k);
-          v4f v = acc[i][j];
+    for (int i = 0; i < MI; i += 2) {
+      v4f mine[2];  // rows lo & 7 and 8 + (lo & 7) of sub-tile i (low lanes) or i + 1
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int give = __builtin_bit_cast(int, low ? acc[i + 1][j][e] : acc[i][j][e]);
+        const float got = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, give, 0x128, 0xF, 0xF, true));
+        mine[0][e] = low ? acc[i][j][e] : got;
+        mine[1][e] = low ? got : acc[i + 1][j][e];
+      }
+      const int k = (wk * MI + i + (low ? 0 : 1)) * 16 + 4 * tg;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = (wn * NJ + j) * 16 + h * 8 + (lo & 7);
+        if (n < n_valid && k < k_valid) {
+          v4f* const p = reinterpret_cast<v4f*>(dw + (n0 + n) * K + k0 + k);
+          v4f v = mine[h];
           if (accumulate) {
             const v4f old = *p;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = old[e] + v[e];
           }
-          *p = v;
+          __builtin_nontemporal_store(v, p);
         }
       }
     }
@@ -195,19 +220,44 @@ static hipError_t launch_wgrad_t(const void* dy, const void* x, const int32_t* o
   return hipGetLastError();
 }
 
-hipError_t set_wgrad_attributes() {
-  hipError_t e = hipFuncSetAttribute((const void*)wgrad_kernel<8, 4, 2, 4, 4>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, wgrad_lds<8, 4, 2, 4, 4>());
-  if (e != hipSuccess) return e;
-  return hipFuncSetAttribute((const void*)wgrad_kernel<4, 4, 2, 2, 4>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                             wgrad_lds<4, 4, 2, 2, 4>());
+template <int MI, int NJ, int WK, int WN, int S>
+static hipError_t set_wgrad_t() {
+  return hipFuncSetAttribute((const void*)wgrad_kernel<MI, NJ, WK, WN, S>,
+                             hipFuncAttributeMaxDynamicSharedMemorySize, wgrad_lds<MI, NJ, WK, WN, S>());
 }
 
+hipError_t set_wgrad_attributes() {
+  hipError_t e = set_wgrad_t<8, 4, 2, 2, 3>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 3>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 2>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 2, 2, 2, 4>();
+  if (e == hipSuccess) e = set_wgrad_t<2, 2, 2, 2, 4>();
+  return e;
+}
+
+// The tile (columns of X x columns of dY) and the ring's depth.  Two or more
+// workgroups per CU let one write its tile while others compute; long ranges gain
+// from larger tiles and deeper rings, few tiles from smaller ones (ranges x rows
+// each, N x K, us):
+//   16 x 2048, 4096 x 2048   256x128 (3 steps) 519   128x128 (2) 564
+//   64 x 512, 2048 x 1024    256x128 (3) 234   128x128 (2) 249
+//   64 x 128, 2048 x 1024    128x128 (2) 101   256x128 (3) 107   128x128 (3) 105
+//   4 x 1024, 2048 x 2048    128x128 (3) 42    128x128 (2) 50
+//   1 x 8192, 2048 x 2048    128x64 (4) 87     128x128 (3) 94    64x64 (4) 138
+//   1 x 16384, 1024 x 1024   64x64 (4) 122     128x64 (4) 147
 hipError_t launch_grouped_wgrad(const void* dy, const void* x, const int32_t* offsets, int G, float* dw,
                                 bool accumulate, int64_t M_total, int64_t N, int64_t K, hipStream_t stream) {
-  const int64_t big = G * ((N + 255) / 256) * ((K + 255) / 256);
-  if (big >= 512) return launch_wgrad_t<8, 4, 2, 4, 4>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
-  return launch_wgrad_t<4, 4, 2, 2, 4>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  const int64_t avg = M_total / G;  // rows per range
+  auto tiles = [&](int64_t bk, int64_t bn) { return G * ((N + bn - 1) / bn) * ((K + bk - 1) / bk); };
+  if (avg >= 400 && tiles(256, 128) >= 1024)
+    return launch_wgrad_t<8, 4, 2, 2, 3>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  if (tiles(128, 128) > 400) {
+    if (avg >= 400) return launch_wgrad_t<4, 4, 2, 2, 3>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+    return launch_wgrad_t<4, 4, 2, 2, 2>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  }
+  if (tiles(128, 64) > 256)
+    return launch_wgrad_t<4, 2, 2, 2, 4>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  return launch_wgrad_t<2, 2, 2, 2, 4>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
 }
 
 }  // namespace fp8bs

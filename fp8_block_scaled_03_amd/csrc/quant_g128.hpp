@@ -5,6 +5,9 @@
 
 namespace fp8bs {
 
+// Regions of one launch (a workgroup takes every gridDim.x-th).
+constexpr int64_t MAX_GRID = 1 << 20, MAX_REGIONS = 0x7FFFFFFF - MAX_GRID;
+
 // Largest value of the 16 lanes of a DPP row, in every one of them (values with
 // a clear sign bit, compared as integers).  Lane exchanges inside a row of 16
 // go through the VALU: no LDS traffic.
@@ -15,6 +18,10 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   v = take(v, __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true));  // the other quad of eight
   v = take(v, __builtin_amdgcn_update_dpp(0, v, 0x140, 0xF, 0xF, true));  // the other eight
   return v;
+}
+
+__device__ __forceinline__ float row16_max(float v) {
+  return __builtin_bit_cast(float, row16_max(__builtin_bit_cast(uint32_t, v)));
 }
 
 // Largest |x| of eight bf16 values, as fp32 bits.
@@ -30,10 +37,31 @@ struct Scale {
   float s, r;  // scale, and its reciprocal where the reciprocal path is valid (else 0)
 };
 
+// amax / 448, rounded to nearest, as in quant_quotient (amax >= QUANT_RECIP_MIN_AMAX).
+__device__ __forceinline__ float over_448(float amax) {
+  constexpr float R = 1.0f / 448.0f;
+  const float q0 = amax * R;
+  return __builtin_fmaf(-__builtin_fmaf(q0, 448.0f, -amax), R, q0);
+}
+
+__device__ __forceinline__ Scale scale_of(float amax) {
+  if (amax >= QUANT_RECIP_MIN_AMAX) {
+    const float s = over_448(amax);
+    return {s, 1.0f / s};
+  }
+  return {amax / 448.0f, 0.0f};
+}
 __device__ __forceinline__ Scale scale_of(uint32_t amax_bits) {
-  const float amax = __builtin_bit_cast(float, amax_bits);
-  const float s = amax / 448.0f;
-  return {s, amax >= QUANT_RECIP_MIN_AMAX ? 1.0f / s : 0.0f};
+  return scale_of(__builtin_bit_cast(float, amax_bits));
+}
+
+// RN32(x / s) from r = RN32(1 / s): q0 = RN(x r), the exact remainder with its sign
+// turned (q0 s - x), then RN(q0 - remainder r) (Markstein, IBM J. Res. Dev.
+// 34(1), 1990; the same value as quant_quotient_recip).  In this form a zero keeps
+// x's sign by itself: for x = -0 the remainder is +0 and -0 - 0 is -0.
+__device__ __forceinline__ float quant_quotient(float x, float s, float r) {
+  const float q0 = x * r;
+  return __builtin_fmaf(-__builtin_fmaf(q0, s, -x), r, q0);
 }
 
 // Eight values -> eight codes.  With the reciprocal path |x / s| is at most
@@ -48,11 +76,19 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], Scale k) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x = v[4 * h + i];
-      t[i] = RECIP || k.r != 0.0f ? quant_quotient_recip(x, k.s, k.r) : sat448(quant_quotient_div(x, k.s));
+      t[i] = RECIP || k.r != 0.0f ? quant_quotient(x, k.s, k.r) : sat448(quant_quotient_div(x, k.s));
     }
     p[h] = pack_e4m3x4(t[0], t[1], t[2], t[3]);
   }
   return make_uint2(p[0], p[1]);
+}
+
+// Largest |v| of eight values.
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+  float m = __builtin_fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, __builtin_fabsf(v[i]));
+  return m;
 }
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {

@@ -11,29 +11,30 @@
 // by DPP exchanges inside a row of lanes.
 #include "launch_g128.hpp"
 #include "quant_g128.hpp"
+#include "ragged.hpp"
 
 #include <type_traits>
 
 namespace fp8bs {
 
-// One wave per region of 4U rows x 128 columns; all U loads of a lane are in
-// flight before any arithmetic.
+// A region is 4U rows x 512 columns, 128 columns (a group) per wave; all U loads of
+// a lane are in flight before any arithmetic.
 template <int U>
 __global__ void __launch_bounds__(256) quantize_tg128_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                              int64_t cols, uint8_t* __restrict__ q,
-                                                             float* __restrict__ scales, int64_t n_regions) {
+                                                             float* __restrict__ scales, uint32_t n_regions) {
   const int lane = threadIdx.x & 63;
   const int piece = lane & 15, rsub = lane >> 4;
-  const int64_t nb = (cols + 127) >> 7;
-  const int64_t waves_total = (int64_t)gridDim.x * 4;
-  for (int64_t reg = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); reg < n_regions; reg += waves_total) {
-    const int64_t rb = reg / nb, cb = reg - rb * nb;
-    const int64_t col = cb * 128 + piece * 8;
+  const uint32_t nb = (uint32_t)((cols + 127) >> 7), quads = (nb + 3) >> 2;
+  for (uint32_t reg = blockIdx.x; reg < n_regions; reg += gridDim.x) {
+    const uint32_t rb = reg / quads, cb = (reg - rb * quads) * 4 + (threadIdx.x >> 6);
+    const int64_t row0 = (int64_t)rb * (4 * U) + rsub;
+    const int64_t col = (int64_t)cb * 128 + piece * 8;
     uint4 w[U];
     bool ok[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int64_t row = rb * (4 * U) + 4 * k + rsub;
+      const int64_t row = row0 + 4 * k;
       ok[k] = row < rows && col < cols;
       w[k] = ok[k] ? *reinterpret_cast<const uint4*>(x + row * cols + col) : make_uint4(0, 0, 0, 0);
     }
@@ -47,7 +48,7 @@ __global__ void __launch_bounds__(256) quantize_tg128_kernel(const uint16_t* __r
     auto store = [&](auto RECIP_) __attribute__((always_inline)) {
 #pragma unroll
       for (int k = 0; k < U; ++k) {
-        const int64_t row = rb * (4 * U) + 4 * k + rsub;
+        const int64_t row = row0 + 4 * k;
         float v[8];
         unpack8(w[k], v);
         const uint2 p = codes8<decltype(RECIP_)::value>(v, sc[k]);
@@ -83,7 +84,13 @@ __device__ __forceinline__ void transpose4x4(uint32_t r0, uint32_t r1, uint32_t 
 // 128-byte rows of qt are written.
 constexpr int TPAD = 128 + 16;  // LDS row of 128 codes, 16-byte aligned, rows 4 banks apart
 
-template <bool TRANSPOSED>
+//
+// LINES: columns (and rows, with the transpose) are multiples of 128, so every
+// 128-byte row of codes is one line, written past the caches.  Otherwise neighbouring
+// blocks share lines: blocks are walked in runs per XCD and written through
+// its L2, which joins them (8 x 4112 x 2064 with the transpose: 76 us, 101 the other
+// way; 8 x 4096 x 2048: 51 as lines, 61 through the L2).
+template <bool TRANSPOSED, bool LINES>
 __global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                             int64_t cols, uint8_t* __restrict__ q,
                                                             float* __restrict__ scales, uint8_t* __restrict__ qt,
@@ -94,7 +101,8 @@ __global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __re
   const int lane = threadIdx.x & 63;
   const int w = threadIdx.x >> 6;
   const int piece = lane & 15, rsub = lane >> 4;
-  const uint32_t cb = blockIdx.x % cb_count, rest = blockIdx.x / cb_count;
+  const uint32_t id = LINES ? blockIdx.x : xcd_run(blockIdx.x, gridDim.x);
+  const uint32_t cb = id % cb_count, rest = id / cb_count;
   const uint32_t rb = rest % rb_count;
   const int64_t gi = rest / rb_count;
   x += gi * rows * cols;
@@ -145,7 +153,10 @@ __global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __re
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int64_t row = (int64_t)rb * 128 + r0 + k;
-    if (ok[k]) store_codes8(q + row * cols + col, p[k].x, p[k].y);
+    if (ok[k]) {
+      if constexpr (LINES) store_codes8(q + row * cols + col, p[k].x, p[k].y);
+      else *reinterpret_cast<uint2*>(q + row * cols + col) = p[k];
+    }
   }
   if (threadIdx.x == 0) {
     scales[(gi * rb_count + rb) * cb_count + cb] = sc.s;
@@ -176,31 +187,36 @@ __global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __re
 
 hipError_t launch_quantize_tg128(const void* x, int64_t rows, int64_t cols, void* q, float* scales,
                                  hipStream_t stream) {
-  const int64_t nb = (cols + 127) / 128;
-  auto go = [&](auto U_) {
-    constexpr int U = decltype(U_)::value;
-    const int64_t n_regions = ((rows + 4 * U - 1) / (4 * U)) * nb;
-    int64_t grid = (n_regions + 3) / 4;
-    if (grid > 65536) grid = 65536;
-    hipLaunchKernelGGL((quantize_tg128_kernel<U>), dim3((unsigned)grid), dim3(256), 0, stream, (const uint16_t*)x,
-                       rows, cols, (uint8_t*)q, scales, n_regions);
-  };
-  // a region of 32 rows per wave when that fills the chip, else of four
-  if ((rows + 31) / 32 * nb >= 4096) go(std::integral_constant<int, 8>{});
-  else go(std::integral_constant<int, 1>{});
+  const int64_t quads = (cols + 511) / 512;
+  // few rows: one load per lane, more waves
+  const int u = (rows + 7) / 8 * quads >= 512 ? 2 : 1;
+  const int64_t n_regions = (rows + 4 * u - 1) / (4 * u) * quads;
+  if (n_regions > MAX_REGIONS) return hipErrorNotSupported;
+  const dim3 grid((unsigned)(n_regions < MAX_GRID ? n_regions : MAX_GRID));
+  if (u == 2)
+    hipLaunchKernelGGL(quantize_tg128_kernel<2>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
+                       (uint8_t*)q, scales, (uint32_t)n_regions);
+  else
+    hipLaunchKernelGGL(quantize_tg128_kernel<1>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
+                       (uint8_t*)q, scales, (uint32_t)n_regions);
   return hipGetLastError();
 }
 
 hipError_t launch_quantize_b128(const void* x, int64_t G, int64_t rows, int64_t cols, void* q, float* scales,
                                 void* qt, float* scales_t, hipStream_t stream) {
   const int64_t rb = (rows + 127) / 128, cb = (cols + 127) / 128;
-  const dim3 grid((unsigned)(G * rb * cb));
-  if (qt)
-    hipLaunchKernelGGL(quantize_b128_kernel<true>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
+  auto go = [&](auto TRANSPOSED_, auto LINES_) {
+    hipLaunchKernelGGL((quantize_b128_kernel<decltype(TRANSPOSED_)::value, decltype(LINES_)::value>),
+                       dim3((unsigned)(G * rb * cb)), dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
                        (uint8_t*)q, scales, (uint8_t*)qt, scales_t, (uint32_t)rb, (uint32_t)cb);
-  else
-    hipLaunchKernelGGL(quantize_b128_kernel<false>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
-                       (uint8_t*)q, scales, (uint8_t*)nullptr, (float*)nullptr, (uint32_t)rb, (uint32_t)cb);
+  };
+  if (qt) {
+    if (cols % 128 == 0 && rows % 128 == 0) go(std::true_type{}, std::true_type{});
+    else go(std::true_type{}, std::false_type{});
+  } else {
+    if (cols % 128 == 0) go(std::false_type{}, std::true_type{});
+    else go(std::false_type{}, std::false_type{});
+  }
   return hipGetLastError();
 }
 

@@ -63,6 +63,28 @@ def test_wgrad_large_tiles():
     check_wgrad(fp8bs.grouped_wgrad(dy, x, i32_dev(off)), dy, x, off)
 
 
+@pytest.mark.parametrize("G,M,N,K", [(16, 6500, 2064, 2000), (4, 2000, 2048, 2064), (1, 8000, 2048, 2000),
+                                     (8, 333, 1040, 528), (1, 5000, 272, 144)])
+def test_wgrad_every_tile(G, M, N, K):
+    """Sizes that reach every tile, uneven ranges, against fp64 on the GPU; replacing and adding."""
+    rng = np.random.default_rng(G * M)
+    off = np.sort(rng.integers(0, M + 1, G + 1))
+    off[0], off[-1] = 0, M
+    dy, x = normal(3, M, N), normal(4, M, K)
+    say(f"wgrad {G} {M} {N}x{K}")
+    old = torch.randn(G, N, K, device=DEV)
+    dw = fp8bs.grouped_wgrad(dy, x, i32_dev(off))
+    added = fp8bs.grouped_wgrad(dy, x, i32_dev(off), old.clone(), accumulate=True)
+    for g in range(G):
+        r = slice(int(off[g]), int(off[g + 1]))
+        a, b = dy[r].double(), x[r].double()
+        ref, mag = a.t() @ b, a.abs().t() @ b.abs()
+        tol = (r.stop - r.start + 2) * 2.0 ** -23 * mag + 1e-300
+        assert ((dw[g] - ref).abs() <= tol).all(), g
+        # the sum again, added once in fp32
+        assert torch.equal(added[g], old[g] + dw[g]), g
+
+
 def test_wgrad_not_finite_rows_of_other_groups():
     """Rows past a range's end are another range's: an infinity or a NaN there stays there."""
     off = [0, 5, 40]

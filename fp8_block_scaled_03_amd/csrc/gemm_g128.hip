@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   constexpr int PIECES = (BM + BN) / 8 / WAVES;            // 1 KB loads per wave and step
   constexpr int S_PIECES = BM / 8;                         // 256-byte scale loads per chunk
   constexpr int S_STEPS = (S_PIECES + WAVES - 1) / WAVES;  // steps of a chunk that issue one per wave
-  constexpr int SSUB = 768, SBUF = BM / 16 * SSUB;         // as in the large tile
+  constexpr int SSUB = 576, SBUF = BM / 16 * SSUB;
   static_assert(PIECES * 8 * WAVES == BM + BN, "tile is a whole number of loads");
   static_assert(NJ * 16 <= 128 && 128 % (NJ * 16) == 0, "a wave's columns lie in one weight block");
   static_assert(S_STEPS + S <= SCH, "a chunk of scales has landed before its first step");
@@ -542,7 +542,7 @@ static hipError_t launch_big(const void* a, const float* sa, const void* bt, con
 
 template <int MI, int NJ, int WM, int WN, int S>
 constexpr int tile_lds() {
-  return S * (16 * MI * WM + 16 * NJ * WN) * GK + 2 * MI * WM * 768;
+  return S * (16 * MI * WM + 16 * NJ * WN) * GK + 2 * MI * WM * 576;
 }
 
 template <int MI, int NJ, int WM, int WN, int S>
@@ -743,21 +743,23 @@ hipError_t set_gemm_g128_attributes() {
 // The kernel is the largest tile that still gives the 256 CUs enough workgroups:
 // a larger tile moves fewer bytes per flop, but tiles that do not fill the chip
 // leave CUs idle (M x N x K, us):
-//   512 x 8192 x 8192    64x128 48   128x128 (256 tiles) 54
-//   1024 x 8192 x 8192   128x128 77  256x256 (128 tiles) 83   64x128 99
 //   512 x 28672 x 8192   256x256 (224 tiles) 110  128x128 156
-//   256 x 8192 x 8192    64x64 35    64x128 (256 tiles) 39
-//   128 x 8192 x 8192    32x64 28    64x64 (256 tiles) 34
-//   64 x 4096 x 4096     32x32 12    32x64 (128 tiles) 13
+//   1024 x 8192 x 8192   128x128 77   256x256 (128 tiles) 83   64x128 99
+//   2048 x 2048 x 7168   64x128 42    128x128 (256 tiles) 48   64x64 50
+//   512 x 8192 x 8192    64x128 49    128x128 (256 tiles) 54   64x64 58
+//   256 x 8192 x 8192    64x64 36     64x128 (256 tiles) 39    32x64 41
+//   128 x 8192 x 8192    32x64 28     64x64 (256 tiles) 34
+//   64 x 4096 x 4096     32x32 12     32x64 (128 tiles) 13
 // For ranges the count goes by their average, and a tile is not chosen much taller
-// than that: its rows past a range's end are work for nothing (64 ranges of 8
-// rows, N = 4096, K = 2048: 32x64 93, 128x128 over 110; 16 ranges of 56, K = 7168:
-// 128x128 91, 64x128 98; 16 of 125, K = 2048: 256x256 37, 128x128 41).
+// than that: its rows past a range's end are work for nothing (ranges x rows, N x
+// K: 64 x 8, 4096 x 2048: 32x64 92, 64x128 96; 64 x 64, 2048 x 2048: 64x128 62,
+// 128x128 70; 64 x 128: 128x128 84, 64x128 92, 256x256 94; 16 x 250, 2048 x
+// 4096: 256x256 55, 128x128 70).
 // Few rows of a narrow weight give too few tiles altogether (16 x 4096 x 4096: rows
 // 7.4, 32x32 11; 32 x 2048 x 7168: 14, 19), a wide weight enough (16 x 28672 x
 // 8192: rows 56, 32x64 48).  With one row tile the call is bound by the weight's
-// stream and a deeper ring pays (64 x 28672 x 8192: 64x64 with four steps 55,
-// with two 61; 1024 x 2064 x 1552, bound by compute and occupancy: 18 and 12).
+// stream and a deeper ring pays (64 x 28672 x 8192: 64x64 with four steps 54,
+// with two 61), else occupancy does (1017 x 2064 x 1552: 19 and 13).
 hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   if (!offsets && K > 0) {
@@ -767,8 +769,8 @@ hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, cons
   const int64_t live = G < M ? G : M;           // ranges that can have rows
   const int64_t avg = (M + live - 1) / live;    // rows of one
   auto tiles = [&](int64_t bm, int64_t bn) { return live * ((avg + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (avg >= 112 && tiles(256, 256) >= 200) return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (avg >= 40 && tiles(128, 128) > 256)
+  if (avg >= 200 && tiles(256, 256) >= 200) return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 128 && tiles(128, 128) > 256)
     return launch_tile<4, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (avg >= 20 && tiles(64, 128) > 256)
     return launch_tile<2, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);

@@ -45,6 +45,44 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2bf));
 }
 
+// Two accumulators of one lane (sub-tiles j and j + 1, four columns each) -> eight
+// neighbouring columns: lanes 16 apart swap, so that those of even g = lane >> 4 hold
+// columns 4g .. 4g+7 of sub-tile j and those of odd g columns 4g-4 .. 4g+3 of j + 1.
+__device__ __forceinline__ uint4 bf16_octet(v4f x, v4f y) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(bf16_pair(x[0], x[1]), bf16_pair(y[0], y[1]), false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(bf16_pair(x[2], x[3]), bf16_pair(y[2], y[3]), false, false);
+  return make_uint4(lo[0], hi[0], lo[1], hi[1]);
+}
+
+// The MI x NJ sub-tiles of a wave, from row and column `r0`, `c0` of the tile at `c`:
+// a lane holds row 16i + lo, columns 16j + 4g .. +3.
+template <int MI, int NJ>
+__device__ __forceinline__ void store_wave(uint16_t* c, int64_t N, const v4f (&acc)[MI][NJ], int r0, int c0, int m_valid,
+                                           int n_valid) {
+  const int g = (threadIdx.x & 63) >> 4, lo = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int r = r0 + 16 * i + lo;
+    uint16_t* const cr = c + r * N;
+    if constexpr (NJ % 2 == 0) {
+#pragma unroll
+      for (int j = 0; j < NJ; j += 2) {
+        const uint4 v = bf16_octet(acc[i][j], acc[i][j + 1]);
+        const int col = c0 + 16 * (j + (g & 1)) + 4 * (g & 2);
+        if (r < m_valid && col < n_valid) *reinterpret_cast<uint4*>(cr + col) = v;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int col = c0 + 16 * j + 4 * g;
+        if (r < m_valid && col < n_valid)
+          *reinterpret_cast<uint2*>(cr + col) =
+              make_uint2(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]));
+      }
+    }
+  }
+}
+
 // ---- small and middle tiles: BM = 16*MI*WM rows by BN = 16*NJ*WN columns per
 // workgroup of WM x WN waves; wave (wm, wn) owns MI x NJ sub-tiles of 16x16.
 //
@@ -84,7 +122,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 
   TileAt t;
   if constexpr (GROUPED) {
-    if (!find_tile<BM>(offsets, G, M, tiles_n, blockIdx.x, t)) return;
+    if (!find_tile<BM>(offsets, G, M, tiles_n, blockIdx.x, gridDim.x, t)) return;
     bt += (int64_t)t.group * N * K;
     sbt += (int64_t)t.group * ((N + 127) >> 7) * ((K + 127) >> 7);
   } else {
@@ -206,22 +244,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     }
   }
 
-  // ---- epilogue: lane holds row 16i + lo, columns 16j + 4g .. +3 of its wave
-  if (!wave_live) return;
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int r = wm * 16 * MI + 16 * i + lo;
-    if (r < m_valid) {
-      uint16_t* const cr = c + (row0 + r) * N + col0;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int col = wn * 16 * NJ + 16 * j + 4 * g;
-        if (col < n_valid)
-          *reinterpret_cast<uint2*>(cr + col) =
-              make_uint2(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]));
-      }
-    }
-  }
+  if (wave_live) store_wave<MI, NJ>(c + row0 * N + col0, N, acc, wm * 16 * MI, wn * 16 * NJ, m_valid, n_valid);
 }
 
 // ---- the large tile: 256 x 256 per workgroup, eight waves of 128 x 64 (2 row bands by
@@ -242,6 +265,10 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 //     for ks + 2 are issued; the next step's first fragments may be read.
 // Each load has about one and a half steps to land.  The waits count a wave's own
 // loads (they return in order); the barrier makes them everybody's.
+//
+// A workgroup takes every gridDim.x-th tile.  The next tile's first two steps are loaded
+// before the current one's results are written, so neither the writes nor the first
+// loads' way through memory leave the CU idle.
 constexpr int XBM = 256, XBN = 256, XTHREADS = 512;
 constexpr int X_A = 0, X_B = 2 * XBM * GK, X_S = X_B + 2 * XBN * GK;  // LDS: A slots, weight slots, scales
 constexpr int X_SLOT = XBM * GK;
@@ -255,7 +282,7 @@ template <bool GROUPED>
 __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
     const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
-    int64_t N, int64_t K, uint32_t tiles_n) {
+    int64_t N, int64_t K, uint32_t tiles_n, uint32_t tiles) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
   typedef __attribute__((address_space(3))) const v4i lds_v4i;
@@ -269,49 +296,64 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   const int wm = w >> 2, wn = w & 3;  // the waves of one SIMD (w, w + 4) are in different row bands
   const int g = lane >> 4, lo = lane & 15;
 
-  TileAt t;
-  if constexpr (GROUPED) {
-    if (!find_tile<XBM>(offsets, G, M, tiles_n, blockIdx.x, t)) return;
-    bt += (int64_t)t.group * N * K;
-    sbt += (int64_t)t.group * ((N + 127) >> 7) * ((K + 127) >> 7);
-  } else {
-    dense_tile<XBM>(M, tiles_n, blockIdx.x, gridDim.x, t);
-  }
-  const int64_t row0 = t.row0, col0 = (int64_t)t.tn * XBN;
-  const int m_valid = (int)(t.row_end - row0 < XBM ? t.row_end - row0 : XBM);
-  const int n_valid = (int)(N - col0 < XBN ? N - col0 : XBN);
   const int KB = (int)((K + 127) >> 7);
+  auto tile_at = [&](uint32_t id, TileAt& t) __attribute__((always_inline)) -> bool {
+    if (id >= tiles) return false;
+    if constexpr (GROUPED) return find_tile<XBM>(offsets, G, M, tiles_n, id, tiles, t);
+    dense_tile<XBM>(M, tiles_n, id, tiles, t);
+    return true;
+  };
+  TileAt t;
+  uint32_t id = blockIdx.x;
+  if (!tile_at(id, t)) return;
 
   // ---- direct loads of 8 rows each; lane l loads row l >> 3, 16-byte piece
   // (l & 7) ^ (row & 7).  Rows past the range read its last row.
-  const int piece = (lane & 7) ^ (lane >> 3);
   auto row_off = [&](int row, int valid) __attribute__((always_inline)) -> uint32_t {
     const int r = row + (lane >> 3);
-    return (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + piece * 16;
+    return (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + ((lane & 7) ^ (lane >> 3)) * 16;
   };
   const int a_first = (w >> 2) * 128 + (w & 3) * 16;  // rows of sub-tiles 0-3; those of 4-7 lie 64 further
-  uint32_t a_off[4], b_off[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a_off[i] = row_off(a_first + (i >> 1) * 64 + (i & 1) * 8, m_valid);
-    b_off[i] = row_off((w * 4 + i) * 8, n_valid);
-  }
-  const uint8_t* const a0 = uniform_ptr(a + row0 * K);
-  const uint8_t* const b0 = uniform_ptr(bt + col0 * K);
-  const uint8_t* const sa0 = uniform_ptr(reinterpret_cast<const uint8_t*>(sa + row0 * KB));
-  // In the partial last K-block the pieces past K read the last whole piece (the
-  // LDS bytes are cleared afterwards).
-  const int over = (KB - 1) * GK + piece * 16 + 16 - (int)K;
-  const uint32_t tail_back = over > 0 ? over : 0;
-  const bool partial = (K & 127) != 0;
-
-  auto issue_a = [&](int ks, int i) __attribute__((always_inline)) {  // i 0, 1: sub-tiles 0-3; 2, 3: 4-7
-    const uint32_t dst = lds0 + X_A + (ks & 1) * X_SLOT + (a_first + (i >> 1) * 64 + (i & 1) * 8) * GK;
-    dma16_at(a0 + (int64_t)ks * GK, a_off[i] - (ks == KB - 1 ? tail_back : 0u), dst);
+  // what the loads of the current tile need
+  int m_valid = 0, n_valid = 0, sb_lanes = 0;
+  uint32_t a_off[4] = {}, b_off[4] = {};
+  const uint8_t *a0 = nullptr, *b0 = nullptr, *sa0 = nullptr;
+  const float* sb_row = nullptr;
+  auto load_sb = [&](int ks) __attribute__((always_inline)) -> int {
+    return __builtin_bit_cast(int, sb_row[ks + lane < KB ? ks + lane : KB - 1]);
   };
-  auto issue_b = [&](int ks, int i) __attribute__((always_inline)) {
+  auto begin_tile = [&]() __attribute__((always_inline)) {
+    const int64_t col0 = (int64_t)t.tn * XBN;
+    m_valid = (int)(t.row_end - t.row0 < XBM ? t.row_end - t.row0 : XBM);
+    n_valid = (int)(N - col0 < XBN ? N - col0 : XBN);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a_off[i] = row_off(a_first + (i >> 1) * 64 + (i & 1) * 8, m_valid);
+      b_off[i] = row_off((w * 4 + i) * 8, n_valid);
+    }
+    a0 = uniform_ptr(a + t.row0 * K);
+    b0 = uniform_ptr(bt + ((int64_t)t.group * N + col0) * K);
+    sa0 = uniform_ptr(reinterpret_cast<const uint8_t*>(sa + t.row0 * KB));
+    const int64_t nbs = (N + 127) >> 7, nb = (col0 + wn * 64) >> 7;
+    sb_row = sbt + (t.group * nbs + (nb < nbs ? nb : 0)) * KB;
+  };
+  // In the partial last K-block the pieces past K read the last whole piece (the
+  // LDS bytes are cleared afterwards).  It is loaded by the last steps only (P =
+  // -1 below), whose loads ask for it.
+  const bool partial = (K & 127) != 0;
+  auto tail_back = [&](int ks) __attribute__((always_inline)) -> uint32_t {
+    if (!partial || ks != KB - 1) return 0u;
+    const int over = ((lane & 7) ^ (lane >> 3)) * 16 + 16 - (int)(K & 127);
+    return over > 0 ? over : 0;
+  };
+
+  auto issue_a = [&](int ks, int i, uint32_t back = 0) __attribute__((always_inline)) {  // i 0, 1: sub-tiles 0-3; 2, 3: 4-7
+    const uint32_t dst = lds0 + X_A + (ks & 1) * X_SLOT + (a_first + (i >> 1) * 64 + (i & 1) * 8) * GK;
+    dma16_at(a0 + (int64_t)ks * GK, a_off[i] - back, dst);
+  };
+  auto issue_b = [&](int ks, int i, uint32_t back = 0) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + X_B + (ks & 1) * X_SLOT + (w * 32 + i * 8) * GK;
-    dma16_at(b0 + (int64_t)ks * GK, b_off[i] - (ks == KB - 1 ? tail_back : 0u), dst);
+    dma16_at(b0 + (int64_t)ks * GK, b_off[i] - back, dst);
   };
   // Scales of eight rows x eight K-blocks, one per lane: part q (0..3) of this
   // wave's 32 rows of chunk `chunk`.
@@ -331,29 +373,22 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     for (int p = first; p < 8; ++p) *(lds_v4i_w*)(base + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
   };
 
-  const int64_t nb = (col0 + wn * 64) >> 7;
-  // The weight's scales, one per wave and step: lane l holds step 64c + l's.  Waited
-  // for where they are loaded, so that nothing in the loop waits for them.
-  const float* const sb_row = sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB;
-  auto load_sb = [&](int ks) __attribute__((always_inline)) -> int {
-    int v = __builtin_bit_cast(int, sb_row[ks + lane < KB ? ks + lane : KB - 1]);
-    asm volatile("" : "+v"(v));
-    return v;
-  };
-
   // The loads of step ks + 2, one at a time: after the middle barrier the scales
   // (even steps), sub-tiles 0-3 of A and the weight, after the end barrier
   // sub-tiles 4-7 of A.
-  auto issue_mid = [&](int ks, int n) __attribute__((always_inline)) {
+  auto issue_mid = [&](int ks, int n, bool last) __attribute__((always_inline)) {
+    const uint32_t back = last ? tail_back(ks + 2) : 0u;
     if (n == 0) {
       if ((ks & 1) == 0) issue_s((ks >> 3) + 1, (ks & 7) >> 1);
     } else if (n < 3) {
-      issue_a(ks + 2, n - 1);
+      issue_a(ks + 2, n - 1, back);
     } else {
-      issue_b(ks + 2, n - 3);
+      issue_b(ks + 2, n - 3, back);
     }
   };
-  auto issue_end = [&](int ks, int n) __attribute__((always_inline)) { issue_a(ks + 2, 2 + n); };
+  auto issue_end = [&](int ks, int n, bool last) __attribute__((always_inline)) {
+    issue_a(ks + 2, 2 + n, last ? tail_back(ks + 2) : 0u);
+  };
 
   // The waits and barriers of one step, between which `work` runs its parts: 0
   // before the middle, 1 to the end, 2 after it; part 1 issues the seven loads of
@@ -364,11 +399,12 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     constexpr int P = decltype(P_)::value;
     const bool loads = P >= 0 || ks + 2 < KB;
     if constexpr (P >= 0) __builtin_assume((ks & 1) == P);
-    work(std::integral_constant<int, 0>{}, loads);
+    constexpr auto LAST = std::integral_constant<bool, (P < 0)>{};
+    work(std::integral_constant<int, 0>{}, loads, LAST);
     if constexpr (P >= 0) wait_vmcnt<(P == 1 ? 9 : 8)>();
     else wait_vmcnt<0>();
     lds_barrier();
-    work(std::integral_constant<int, 1>{}, loads);
+    work(std::integral_constant<int, 1>{}, loads, LAST);
     if constexpr (P >= 0) wait_vmcnt<(P == 0 ? 9 : 8)>();
     else wait_vmcnt<0>();
     lds_barrier();
@@ -376,167 +412,183 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
       clear_tail();
       lds_barrier();
     }
-    work(std::integral_constant<int, 2>{}, loads);
+    work(std::integral_constant<int, 2>{}, loads, LAST);
   };
   auto run = [&](auto&& work) __attribute__((always_inline)) {
     int ks = 0;
+    const int steady = KB - (partial ? 4 : 3);
 #pragma unroll 1
-    for (; ks + 3 < KB; ks += 2) {
+    for (; ks < steady; ks += 2) {
       step(ks, std::integral_constant<int, 0>{},
-           [&](auto part, bool loads) __attribute__((always_inline)) { work(ks, part, loads); });
+           [&](auto part, bool loads, auto last) __attribute__((always_inline)) { work(ks, part, loads, last); });
       step(ks + 1, std::integral_constant<int, 1>{},
-           [&](auto part, bool loads) __attribute__((always_inline)) { work(ks + 1, part, loads); });
+           [&](auto part, bool loads, auto last) __attribute__((always_inline)) { work(ks + 1, part, loads, last); });
     }
 #pragma unroll 1
     for (; ks < KB; ++ks)
       step(ks, std::integral_constant<int, -1>{},
-           [&](auto part, bool loads) __attribute__((always_inline)) { work(ks, part, loads); });
+           [&](auto part, bool loads, auto last) __attribute__((always_inline)) { work(ks, part, loads, last); });
   };
 
-  v4f acc[8][4];
+  // The first two steps' loads of a tile, in the loop's order: sub-tiles 0-3 and the
+  // weight, then sub-tiles 4-7.
+  auto first_loads = [&]() __attribute__((always_inline)) {
+    auto mid = [&](int ks) __attribute__((always_inline)) {
+      const uint32_t back = tail_back(ks);
+      issue_a(ks, 0, back);
+      issue_a(ks, 1, back);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-  const bool wave_live = wm * 128 < m_valid && wn * 64 < n_valid;
-  if (KB > 0) {
+      for (int n = 0; n < 4; ++n) issue_b(ks, n, back);
+    };
 #pragma unroll
     for (int q = 0; q < 4; ++q) issue_s(0, q);
-    // as in the loop: (sub-tiles 0-3 and the weight), then sub-tiles 4-7
-    auto issue_first = [&](int ks) __attribute__((always_inline)) {
-      issue_a(ks, 0);
-      issue_a(ks, 1);
+    mid(0);
+    issue_a(0, 2, tail_back(0));
+    issue_a(0, 3, tail_back(0));
+    if (KB > 1) mid(1);
+    // The weight's scales, one per wave and step: lane l holds step 64c + l's.
+    sb_lanes = load_sb(0);
+  };
+
+  const int sw0 = 16 * (g ^ (lo & 7)), sw1 = 16 * ((4 + g) ^ (lo & 7));
+  const lds_u8* const ra0 = lds + X_A + (wm * 128 + lo) * GK + sw0;
+  const lds_u8* const ra1 = lds + X_A + (wm * 128 + lo) * GK + sw1;
+  const lds_u8* const rb0 = lds + X_B + (wn * 64 + lo) * GK + sw0;
+  const lds_u8* const rb1 = lds + X_B + (wn * 64 + lo) * GK + sw1;
+  const lds_u8* const rs = lds + X_S + wm * 8 * X_SSUB + (lo >> 3) * 288 + (lo & 7) * 4;
+  auto read = [&](const lds_u8* p0, const lds_u8* p1, int off) __attribute__((always_inline)) -> v8i_t {
+    const v4i x = *(lds_v4i*)(p0 + off), y = *(lds_v4i*)(p1 + off);
+    return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  };
+
+  begin_tile();
+  if (KB > 0) first_loads();
+#pragma unroll 1
+  for (;;) {
+    uint16_t* const ct = c + t.row0 * N + (int64_t)t.tn * XBN;
+    const int m_here = m_valid, n_here = n_valid;
+    const bool wave_live = wm * 128 < m_here && wn * 64 < n_here;
+    id += gridDim.x;
+    const bool more = tile_at(id, t);  // looked up while the first loads land
+
+    v4f acc[8][4];
 #pragma unroll
-      for (int n = 0; n < 4; ++n) issue_b(ks, n);
-    };
-    issue_first(0);
-    issue_a(0, 2);
-    issue_a(0, 3);
-    if (KB > 1) issue_first(1);
-    if (KB > 2) wait_vmcnt<8>();
-    else wait_vmcnt<0>();
-    lds_barrier();
-    if (KB > 1) {
-      issue_a(1, 2);
-      issue_a(1, 3);
-    }
-    if (partial && KB == 1) {
-      clear_tail();
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (KB > 0) {
+      // everything before this, a last tile's stores among it: they are not counted
+      // among the loads
+      wait_vmcnt<0>();
+      asm volatile("" : "+v"(sb_lanes));
       lds_barrier();
-    }
-
-    if (wave_live) {
-      const int sw0 = 16 * (g ^ (lo & 7)), sw1 = 16 * ((4 + g) ^ (lo & 7));
-      const lds_u8* const ra0 = lds + X_A + (wm * 128 + lo) * GK + sw0;
-      const lds_u8* const ra1 = lds + X_A + (wm * 128 + lo) * GK + sw1;
-      const lds_u8* const rb0 = lds + X_B + (wn * 64 + lo) * GK + sw0;
-      const lds_u8* const rb1 = lds + X_B + (wn * 64 + lo) * GK + sw1;
-      const lds_u8* const rs = lds + X_S + wm * 8 * X_SSUB + (lo >> 3) * 288 + (lo & 7) * 4;
-      auto read = [&](const lds_u8* p0, const lds_u8* p1, int off) __attribute__((always_inline)) -> v8i_t {
-        const v4i x = *(lds_v4i*)(p0 + off), y = *(lds_v4i*)(p1 + off);
-        return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-      };
-      v8i_t bf[4], af[2];
-      v4f p[4];
-      float sc[8];
-      int sb_lanes = load_sb(0);
-      // the first step's fragments; products of "row sub-tile 7 of the step before" are zeros
-      af[0] = read(ra0, ra1, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf[j] = read(rb0, rb1, j * 2048);
-        p[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      if (KB > 1) {
+        issue_a(1, 2, tail_back(1));
+        issue_a(1, 3, tail_back(1));
       }
+      if (partial && KB == 1) {
+        clear_tail();
+        lds_barrier();
+      }
+      if (wave_live) {
+        v8i_t bf[4], af[2];
+        v4f p[4];
+        float sc[8];
+        // the first step's fragments; products of "row sub-tile 7 of the step before" are zeros
+        af[0] = read(ra0, ra1, 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          bf[j] = read(rb0, rb1, j * 2048);
+          p[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[i] = 0.0f;
 
-      run([&](int ks, auto part_, bool loads) __attribute__((always_inline)) {
-        constexpr int part = decltype(part_)::value;
-        const int slot = (ks & 1) * X_SLOT;
-        if (part == 0 && (ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
-        constexpr int first = part == 0 ? 0 : part == 1 ? 3 : 7, last = part == 0 ? 3 : part == 1 ? 7 : 8;
-#pragma unroll
-        for (int i = first; i < last; ++i) {
-          if (i < 7) af[(i + 1) & 1] = read(ra0, ra1, slot + (i + 1) * 2048);
-          else af[0] = read(ra0, ra1, (X_SLOT - slot));  // after the last step: in bounds, never used
-          float s_raw[8];
-          if (i == 0) {
-            const lds_u8* const q = rs + ((ks >> 3) & 1) * X_SBUF + (ks & 7) * 32;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) s_raw[x] = *(lds_f32*)(q + x * X_SSUB);
+        run([&](int ks, auto part_, bool loads, auto last) __attribute__((always_inline)) {
+          constexpr int part = decltype(part_)::value;
+          const int slot = (ks & 1) * X_SLOT;
+          if (part == 0 && (ks & 63) == 0 && ks > 0) {
+            sb_lanes = load_sb(ks);
+            asm volatile("" : "+v"(sb_lanes));  // waited for here, not in every step
           }
-          __builtin_amdgcn_sched_barrier(0);
+          constexpr int first = part == 0 ? 0 : part == 1 ? 3 : 7, past = part == 0 ? 3 : part == 1 ? 7 : 8;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            promote(acc[(i + 7) & 7][j], p[j], sc[(i + 7) & 7]);
-            asm volatile("" : "+v"(acc[(i + 7) & 7][j]));  // here, not where it is next needed
+          for (int i = first; i < past; ++i) {
+            if (i < 7) af[(i + 1) & 1] = read(ra0, ra1, slot + (i + 1) * 2048);
+            else af[0] = read(ra0, ra1, (X_SLOT - slot));  // after the last step: in bounds, never used
+            float s_raw[8];
+            if (i == 0) {
+              const lds_u8* const q = rs + ((ks >> 3) & 1) * X_SBUF + (ks & 7) * 32;
+#pragma unroll
+              for (int x = 0; x < 8; ++x) s_raw[x] = *(lds_f32*)(q + x * X_SSUB);
+            }
             __builtin_amdgcn_sched_barrier(0);
-            p[j] = mfma_block(bf[j], af[i & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-            if (i == 7) bf[j] = read(rb0, rb1, (X_SLOT - slot) + j * 2048);
-            // one load per two MFMAs: a burst would hold up the wave's issue
-            if (j & 1) {
-              const int n = (i - first) * 2 + (j >> 1);
-              if (part == 1 && n < 7 && loads) issue_mid(ks, n);
-              if (part == 2 && loads) issue_end(ks, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              promote(acc[(i + 7) & 7][j], p[j], sc[(i + 7) & 7]);
+              asm volatile("" : "+v"(acc[(i + 7) & 7][j]));  // here, not where it is next needed
+              __builtin_amdgcn_sched_barrier(0);
+              p[j] = mfma_block(bf[j], af[i & 1]);
+              __builtin_amdgcn_sched_barrier(0);
+              if (i == 7) bf[j] = read(rb0, rb1, (X_SLOT - slot) + j * 2048);
+              // one load per two MFMAs: a burst would hold up the wave's issue
+              if (j & 1) {
+                const int n = (i - first) * 2 + (j >> 1);
+                if (part == 1 && n < 7 && loads) issue_mid(ks, n, last);
+                if (part == 2 && loads) issue_end(ks, n, last);
+              }
+            }
+            if (i == 0) {
+              const float sb = __builtin_bit_cast(float, __builtin_amdgcn_readlane(sb_lanes, ks & 63));
+#pragma unroll
+              for (int x = 0; x < 8; ++x) sc[x] = s_raw[x] * sb;
+              __builtin_amdgcn_sched_barrier(0);
             }
           }
-          if (i == 0) {
-            const float sb = __builtin_bit_cast(float, __builtin_amdgcn_readlane(sb_lanes, ks & 63));
+        });
 #pragma unroll
-            for (int x = 0; x < 8; ++x) sc[x] = s_raw[x] * sb;
-            __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < 4; ++j) promote(acc[7][j], p[j], sc[7]);
+      } else {
+        run([&](int ks, auto part_, bool loads, auto last) __attribute__((always_inline)) {
+          constexpr int part = decltype(part_)::value;
+          if (part == 1 && loads)
+#pragma unroll
+            for (int n = 0; n < 7; ++n) issue_mid(ks, n, last);
+          if (part == 2 && loads) {
+            issue_end(ks, 0, last);
+            issue_end(ks, 1, last);
           }
-        }
-      });
-#pragma unroll
-      for (int j = 0; j < 4; ++j) promote(acc[7][j], p[j], sc[7]);
-    } else {
-      run([&](int ks, auto part_, bool loads) __attribute__((always_inline)) {
-        constexpr int part = decltype(part_)::value;
-        if (part == 1 && loads)
-#pragma unroll
-          for (int n = 0; n < 7; ++n) issue_mid(ks, n);
-        if (part == 2 && loads) {
-          issue_end(ks, 0);
-          issue_end(ks, 1);
-        }
-      });
-    }
-    wait_vmcnt<0>();
-  }
-
-  // ---- epilogue: lane holds row 16i + lo, columns 16j + 4g .. +3 of its wave
-  if (!wave_live) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = wm * 128 + 16 * i + lo;
-    if (r < m_valid) {
-      uint16_t* const cr = c + (row0 + r) * N + col0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = wn * 64 + 16 * j + 4 * g;
-        if (col < n_valid)
-          *reinterpret_cast<uint2*>(cr + col) =
-              make_uint2(bf16_pair(acc[i][j][0], acc[i][j][1]), bf16_pair(acc[i][j][2], acc[i][j][3]));
+        });
       }
+      wait_vmcnt<0>();
+      if (more) {
+        lds_barrier();  // every wave has read the last step's fragments
+        begin_tile();
+        first_loads();
+      }
+    } else if (more) {
+      begin_tile();
     }
+    if (wave_live) store_wave<8, 4>(ct, N, acc, wm * 128, wn * 64, m_here, n_here);
+    if (!more) return;
   }
 }
 
 static hipError_t launch_big(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                              int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t tiles_n = (N + XBN - 1) / XBN;
+  // each range adds at most one partial tile
   const int64_t tiles_m = offsets ? (M + XBM - 1) / XBM + (G < M ? G : M) : (M + XBM - 1) / XBM;
-  if (tiles_m * tiles_n > (int64_t)0xFFFFFFFF / XTHREADS) return hipErrorNotSupported;
-  const dim3 grid((unsigned)(tiles_m * tiles_n));
+  const int64_t tiles = tiles_m * tiles_n;
+  if (tiles > 0x7FFFFFFF) return hipErrorNotSupported;
+  // one workgroup per CU (their LDS allows no second one)
+  const dim3 grid((unsigned)(tiles < 256 ? tiles : 256));
   if (offsets)
     hipLaunchKernelGGL(gemm_g128_big_kernel<true>, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa,
-                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n, (uint32_t)tiles);
   else
     hipLaunchKernelGGL(gemm_g128_big_kernel<false>, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa,
-                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n, (uint32_t)tiles);
   return hipGetLastError();
 }
 

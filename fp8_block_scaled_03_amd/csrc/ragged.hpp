@@ -60,12 +60,12 @@ __device__ __forceinline__ void range_of(const int32_t* offsets, int g, int64_t 
   end = e;
 }
 
-// The tile of workgroup `id` among all ranges' tiles (range by range); false
-// for a workgroup past the last one.  Every wave finds it for itself: lane l
+// Tile `id` of all ranges' tiles (range by range), of which at most `most` are
+// given out; false past the last one.  Every wave finds it for itself: lane l
 // looks at range 64c + l, a prefix sum over the lanes counts the row tiles.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int G, int64_t M, uint32_t tiles_n,
-                                          uint32_t id, TileAt& t) {
+                                          uint32_t id, uint32_t most, TileAt& t) {
   const int lane = threadIdx.x & 63;
   auto count = [&](int c, int64_t& begin, int64_t& end) __attribute__((always_inline)) -> uint32_t {
     const int gi = c * 64 + lane;
@@ -85,10 +85,11 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
   int64_t begin, end;
   uint32_t row_tiles = 0;
   for (int c = 0; c < chunks; ++c) row_tiles += __shfl(prefix(count(c, begin, end)), 63, 64);
-  // a bad table may count more tiles than the grid was sized for: every
-  // workgroup then still has one tile, inside [0, M]
+  row_tiles = __builtin_amdgcn_readfirstlane(row_tiles);
+  // a bad table may count more tiles than the launch was sized for: every tile is
+  // still inside [0, M]
   const uint64_t total64 = (uint64_t)row_tiles * tiles_n;
-  const uint32_t total = total64 < gridDim.x ? (uint32_t)total64 : gridDim.x;
+  const uint32_t total = total64 < most ? (uint32_t)total64 : most;
   if (id >= total) return false;
   const uint32_t lin = xcd_run(id, total);
   const uint32_t want = lin / tiles_n;

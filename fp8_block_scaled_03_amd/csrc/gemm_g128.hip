@@ -23,6 +23,7 @@
 #include "launch_g128.hpp"
 #include "ragged.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace fp8bs {
@@ -90,8 +91,10 @@ __device__ __forceinline__ void store_wave(uint16_t* c, int64_t N, const v4f (&a
 // LDS, S - 1 steps ahead: few workgroups (a decode step's tiles) then still keep
 // enough bytes in flight.  Row r of a stage holds its 128 bytes with 16-byte
 // piece p at position p ^ (r & 7), which spreads a fragment read over all
-// banks.  A's scales come eight K-blocks at a time, one or
-// two such chunks ahead; a weight scale is one value per wave and step, held by lane l for step 64c + l.
+// banks.  A's scales come eight K-blocks at a time, a chunk ahead; a weight scale is
+// one value per wave and step, held by lane l for step 64c + l.  A wave's MFMAs,
+// promotions and fragment reads are in the large tile's order (below); left to the
+// compiler's order 512 x 8192 x 8192 took 7% longer.
 template <int MI, int NJ, int WM, int WN, int S, bool GROUPED>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
@@ -164,10 +167,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   auto issue_s = [&](int chunk, int p) __attribute__((always_inline)) {
     const int r = p * 8 + (lane & 7), kb = chunk * SCH + (lane >> 3);
     const uint32_t o = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
-                     lds0 + S * STAGE + (chunk & 1) * SBUF + (p >> 1) * SSUB + (p & 1) * 288),
-                 "v"(o * 4), "s"(sa0)
-                 : "memory");
+    dma4_at(sa0, o * 4, lds0 + S * STAGE + (chunk & 1) * SBUF + (p >> 1) * SSUB + (p & 1) * 288);
   };
   const int64_t nb = (col0 + wn * 16 * NJ) >> 7;
   const float* const sb_row = sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB;
@@ -228,13 +228,21 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 #pragma unroll
         for (int i = 0; i < MI; ++i) sc[i] = *(lds_f32*)(q + i * SSUB);
         v4f p[NJ];
+        v8i_t af[2];
+        af[0] = frag(ra + slot * STAGE);
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          const v8i_t af = frag(ra + slot * STAGE + 16 * i * GK);
+          if (i + 1 < MI) af[(i + 1) & 1] = frag(ra + slot * STAGE + 16 * (i + 1) * GK);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            if (i > 0) promote(acc[i - 1][j], p[j], sc[i - 1] * sb);
-            p[j] = mfma_block(bf[j], af);
+            if (i > 0) {
+              promote(acc[i - 1][j], p[j], sc[i - 1] * sb);
+              asm volatile("" : "+v"(acc[i - 1][j]));  // here, not where it is next needed
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            p[j] = mfma_block(bf[j], af[i & 1]);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
 #pragma unroll
@@ -360,10 +368,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   auto issue_s = [&](int chunk, int q) __attribute__((always_inline)) {
     const int r = w * 32 + q * 8 + (lane & 7), kb = chunk * SCH + (lane >> 3);
     const uint32_t off = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
-                     lds0 + X_S + (chunk & 1) * X_SBUF + (w * 2 + (q >> 1)) * X_SSUB + (q & 1) * 288),
-                 "v"(off * 4), "s"(sa0)
-                 : "memory");
+    dma4_at(sa0, off * 4, lds0 + X_S + (chunk & 1) * X_SBUF + (w * 2 + (q >> 1)) * X_SSUB + (q & 1) * 288);
   };
   // Zeros behind K in the last K-block's slots, once its data are there for every wave.
   auto clear_tail = [&]() __attribute__((always_inline)) {
@@ -783,35 +788,40 @@ hipError_t set_gemm_g128_attributes() {
   if (e == hipSuccess)
     e = hipFuncSetAttribute((const void*)gemm_g128_big_kernel<true>, hipFuncAttributeMaxDynamicSharedMemorySize,
                             X_LDS);
+  if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 4, 3>();
   if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 2, 2>();
+  if (e == hipSuccess) e = set_tile_attributes<2, 4, 4, 2, 3>();
   if (e == hipSuccess) e = set_tile_attributes<2, 4, 2, 2, 2>();
-  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2, 2>();
-  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2, 4>();
-  if (e == hipSuccess) e = set_tile_attributes<1, 2, 2, 2, 4>();
+  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 4, 3>();
+  if (e == hipSuccess) e = set_tile_attributes<1, 2, 2, 2, 3>();
   if (e == hipSuccess) e = set_tile_attributes<1, 1, 2, 2, 4>();
   return e;
 }
 
 // The kernel is the largest tile that still gives the 256 CUs enough workgroups:
 // a larger tile moves fewer bytes per flop, but tiles that do not fill the chip
-// leave CUs idle (M x N x K, us):
-//   512 x 28672 x 8192   256x256 (224 tiles) 110  128x128 156
-//   1024 x 8192 x 8192   128x128 77   256x256 (128 tiles) 83   64x128 99
-//   2048 x 2048 x 7168   64x128 42    128x128 (256 tiles) 48   64x64 50
-//   512 x 8192 x 8192    64x128 49    128x128 (256 tiles) 54   64x64 58
-//   256 x 8192 x 8192    64x64 36     64x128 (256 tiles) 39    32x64 41
-//   128 x 8192 x 8192    32x64 28     64x64 (256 tiles) 34
-//   64 x 4096 x 4096     32x32 12     32x64 (128 tiles) 13
-// For ranges the count goes by their average, and a tile is not chosen much taller
-// than that: its rows past a range's end are work for nothing (ranges x rows, N x
-// K: 64 x 8, 4096 x 2048: 32x64 92, 64x128 96; 64 x 64, 2048 x 2048: 64x128 62,
-// 128x128 70; 64 x 128: 128x128 84, 64x128 92, 256x256 94; 16 x 250, 2048 x
-// 4096: 256x256 55, 128x128 70).
+// leave CUs idle (M x N x K, us; [n] = the tile's count; 8w = eight waves and three
+// K-blocks in the ring, one workgroup a CU, else four waves, two a CU or more):
+//   512 x 28672 x 8192   256x256 [224] 110   128x128 156
+//   256 x 28672 x 8192   128x256 8w [224] 77  128x128 [448] 87  256x256 [112] 97
+//   2048 x 4096 x 4096   128x256 8w [256] 39  128x128 [512] 40
+//   400 x 12288 x 1024   128x128 [384] 13.1   128x256 8w [192] 13.5
+//   128 x 28672 x 8192   128x128 8w [224] 60  64x128 [448] 72
+//   700 x 5120 x 5120    128x128 8w [240] 29  64x128 [440] 30
+//   3000 x 992 x 2048    64x128 [376] 13.6    128x128 8w [192] 14.3
+//   256 x 8192 x 8192    64x128 8w [256] 33   64x64 [512] 35    32x64 36
+//   1024 x 2048 x 7168   64x128 8w [256] 29   64x64 [512] 31    128x128 8w 41
+//   128 x 8192 x 8192    32x64 [512] 28       64x128 8w [128] 33
+//   64 x 4096 x 4096     32x32 [256] 12       32x64 [128] 13
+// A range has half a tile too much on average, which the count includes, and a tile
+// is not chosen much taller than the ranges: rows past a range's end are work for
+// nothing (ranges x average rows, N x K: 64 x 8, 4096 x 2048: 32x64 93, 64x128 95;
+// 16 x 25, 4096 x 7168: 64x128 75, 128x128 81; 16 x 56: 128x256 8w 85, 64x128 95;
+// 16 x 125, 4096 x 2048: 64x128 36, 128x256 8w 40; 16 x 250, 2048 x 4096: 256x256
+// 55, 128x128 64).
 // Few rows of a narrow weight give too few tiles altogether (16 x 4096 x 4096: rows
 // 7.4, 32x32 11; 32 x 2048 x 7168: 14, 19), a wide weight enough (16 x 28672 x
-// 8192: rows 56, 32x64 48).  With one row tile the call is bound by the weight's
-// stream and a deeper ring pays (64 x 28672 x 8192: 64x64 with four steps 54,
-// with two 61), else occupancy does (1017 x 2064 x 1552: 19 and 13).
+// 8192: rows 56, 32x64 48).
 hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   if (!offsets && K > 0) {
@@ -820,17 +830,24 @@ hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, cons
   }
   const int64_t live = G < M ? G : M;           // ranges that can have rows
   const int64_t avg = (M + live - 1) / live;    // rows of one
-  auto tiles = [&](int64_t bm, int64_t bn) { return live * ((avg + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (avg >= 200 && tiles(256, 256) >= 200) return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (avg >= 128 && tiles(128, 128) > 256)
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    const int64_t rows = offsets ? std::max(live, (M + live * (bm / 2)) / bm) : (M + bm - 1) / bm;
+    return rows * ((N + bn - 1) / bn);
+  };
+  const int64_t big = tiles(256, 256), wide = tiles(128, 256), square = tiles(128, 128), low = tiles(64, 128);
+  if (avg >= 160 && big >= (offsets ? 160 : 200))
+    return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 48 && wide >= 200 && wide <= 256)
+    return launch_tile<4, 4, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg > 64 && square >= 200 && square <= 256)
+    return launch_tile<2, 4, 4, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 128 && square > 256)
     return launch_tile<4, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (avg >= 20 && tiles(64, 128) > 256)
+  if (avg >= 20 && low > 256)
     return launch_tile<2, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (avg >= 20 && tiles(64, 64) > 256) {
-    if (avg <= 64) return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-    return launch_tile<2, 2, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  }
-  if (tiles(32, 64) >= 200) return launch_tile<1, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (avg >= 20 && low >= 200)
+    return launch_tile<2, 2, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (tiles(32, 64) >= 150) return launch_tile<1, 2, 2, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   return launch_tile<1, 1, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
 }
 

@@ -135,10 +135,18 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, i
 }
 
 // ---- rings of direct loads -------------------------------------------------------
-// Direct global->LDS load of 16 bytes per lane from a uniform base plus a
-// 32-bit offset per lane.
+// Direct global->LDS loads of 16 (4) bytes per lane from a uniform base plus a 32-bit
+// offset per lane, to a uniform LDS address.
 __device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(off), "s"(base)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds_base)),
+               "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void dma4_at(const uint8_t* base, uint32_t off, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(
+                   __builtin_amdgcn_readfirstlane(lds_base)),
+               "v"(off), "s"(base)
                : "memory");
 }
 

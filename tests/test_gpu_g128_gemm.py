@@ -72,6 +72,46 @@ def test_rows_do_not_depend_on_m(N, K):
             assert torch.equal(part.view(torch.int16), full[first:first + M].view(torch.int16)), (M, first)
 
 
+# One size for each tile that the dispatch can take, with a ragged last tile both ways and a partial last K-block.
+DENSE = [(9, 1040), (20, 2064), (40, 1040), (100, 4112), (500, 3600), (1000, 2320), (1000, 4624), (400, 7184),
+         (1700, 4112), (3500, 4112)]
+RANGED = [(7, 60, 1040), (7, 60, 3600), (5, 300, 4112), (5, 300, 5200), (3, 1000, 4368), (3, 1000, 3472),
+          (4, 2000, 3600), (4, 8000, 1296)]
+
+
+@pytest.mark.parametrize("K", [400, 1168])
+@pytest.mark.parametrize("M,N", DENSE)
+def test_every_tile(M, N, K):
+    say(f"gemm_tg128_nt {M}x{N}x{K}")
+    ops = operands(M + N + K, M, N, K)
+    a, sa, bt, sbt = dev(ops)
+    c = fp8bs.gemm_tg128_nt(a, sa, bt, sbt)
+    for r in sorted({0, M // 2, M - 1}):
+        one = fp8bs.gemm_tg128_nt(a[r:r + 1].clone(), sa[r:r + 1].clone(), bt, sbt)
+        assert torch.equal(one[0].view(torch.int16), c[r].view(torch.int16)), r
+    cols = np.unique(np.r_[0:8, N // 2:N // 2 + 8, N - 8:N])
+    rows = np.unique(np.linspace(0, M - 1, 12).astype(int))
+    ref, bound = oracle.gemm_g128_bound(ops[0][rows], ops[1][rows], ops[2], ops[3])
+    assert (np.abs(f64(c[torch.from_numpy(rows).to(DEV)]) - ref)[:, cols] <= bound[:, cols]).all()
+
+
+@pytest.mark.parametrize("K", [400, 1168])
+@pytest.mark.parametrize("G,M,N", RANGED)
+def test_every_tile_of_ranges(G, M, N, K):
+    rng = np.random.default_rng(G + M)
+    cuts = np.sort(rng.integers(0, M + 1, G + 1)).astype(np.int32)
+    a, sa, bt, sbt = dev(operands(G + N, M, N, K, G))
+    out = torch.full((M, N), 3.0, dtype=torch.bfloat16, device=DEV)
+    say(f"grouped {G} {M} {N} {K}")
+    fp8bs.grouped_gemm_tg128_nt(a, sa, bt, sbt, i32_dev(cuts), out)
+    for g in range(G):
+        r = slice(int(cuts[g]), int(cuts[g + 1]))
+        if r.start < r.stop:
+            one = fp8bs.gemm_tg128_nt(a[r].clone(), sa[r].clone(), bt[g].clone(), sbt[g].clone())
+            assert torch.equal(out[r].view(torch.int16), one.view(torch.int16)), g
+    assert (out[:cuts[0]] == 3.0).all() and (out[cuts[-1]:] == 3.0).all()
+
+
 def test_k_zero_and_empty():
     z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device=DEV)  # noqa: E731
     f = lambda *s: torch.zeros(*s, device=DEV)                     # noqa: E731

@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   constexpr int S_PIECES = BM / 8;                         // 256-byte scale loads per chunk
   constexpr int S_STEPS = (S_PIECES + WAVES - 1) / WAVES;  // steps of a chunk that issue one per wave
   constexpr int SSUB = 576, SBUF = BM / 16 * SSUB;
-  static_assert(PIECES * 8 * WAVES == BM + BN, "tile is a whole number of loads");
+  constexpr int A_PIECES = BM / 8 / WAVES;                 // of these A's
+  static_assert(PIECES * 8 * WAVES == BM + BN && A_PIECES * 8 * WAVES == BM, "tile is a whole number of loads");
+  static_assert(S_STEPS == 1 || S_STEPS * WAVES == S_PIECES, "every wave has a scale load in such a step");
   static_assert(NJ * 16 <= 128 && 128 % (NJ * 16) == 0, "a wave's columns lie in one weight block");
   static_assert(S_STEPS + S <= SCH, "a chunk of scales has landed before its first step");
   static_assert(PIECES * (S - 2) < 64, "vmcnt range");
@@ -143,31 +145,43 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   // K-block the pieces past K read the last whole piece (cleared afterwards).
   const int piece = (lane & 7) ^ (lane >> 3);
   uint32_t off[PIECES];
-  const uint8_t* from[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
     const int p = w + i * WAVES;
-    const bool of_a = p < BM / 8;
-    const int valid = of_a ? m_valid : n_valid;
-    const int r = (of_a ? p : p - BM / 8) * 8 + (lane >> 3);
+    const int valid = i < A_PIECES ? m_valid : n_valid;
+    const int r = (i < A_PIECES ? p : p - BM / 8) * 8 + (lane >> 3);
     off[i] = (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + piece * 16;
-    from[i] = uniform_ptr(of_a ? a + row0 * K : bt + col0 * K);
   }
-  const int over = (KB - 1) * GK + piece * 16 + 16 - (int)K;
-  const uint32_t tail_back = over > 0 ? over : 0;
-  const bool partial = (K & 127) != 0;
+  const uint8_t* const a0 = uniform_ptr(a + row0 * K);
+  const uint8_t* const b0 = uniform_ptr(bt + col0 * K);
   const uint8_t* const sa0 = uniform_ptr(reinterpret_cast<const uint8_t*>(sa + row0 * KB));
+  const bool partial = (K & 127) != 0;
+  const uint32_t dst = lds0 + w * 1024;  // (scalar)
 
-  auto issue = [&](int ks, int slot) __attribute__((always_inline)) {
-    const uint32_t back = ks == KB - 1 ? tail_back : 0u;
+  // The load of step ks into the slot at `at`; LAST: it may be the partial one.
+  auto issue = [&](int ks, uint32_t at, auto last) __attribute__((always_inline)) {
+    uint32_t back = 0;
+    if constexpr (decltype(last)::value) {
+      const int over = (KB - 1) * GK + piece * 16 + 16 - (int)K;
+      if (ks == KB - 1 && over > 0) back = over;
+    }
+    const int64_t k = (int64_t)ks * GK;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
-      dma16_at(from[i] + (int64_t)ks * GK, off[i] - back, lds0 + slot * STAGE + (w + i * WAVES) * 1024);
+      dma16_at((i < A_PIECES ? a0 : b0) + k, off[i] - back, dst + at + i * WAVES * 1024);
   };
-  auto issue_s = [&](int chunk, int p) __attribute__((always_inline)) {
-    const int r = p * 8 + (lane & 7), kb = chunk * SCH + (lane >> 3);
-    const uint32_t o = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
-    dma4_at(sa0, o * 4, lds0 + S * STAGE + (chunk & 1) * SBUF + (p >> 1) * SSUB + (p & 1) * 288);
+  // Scales of chunk `chunk`, the wave's share number q.  The chunk behind the last one
+  // is the last scale again, and is not used.
+  uint32_t s_off[S_STEPS];
+#pragma unroll
+  for (int q = 0; q < S_STEPS; ++q) {
+    const int r = (q * WAVES + w) * 8 + (lane & 7);
+    s_off[q] = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB;
+  }
+  auto issue_s = [&](int chunk, int q) __attribute__((always_inline)) {
+    const int p = q * WAVES + w, kb = chunk * SCH + (lane >> 3);
+    dma4_at(sa0, (s_off[q] + (kb < KB ? kb : KB - 1)) * 4,
+            lds0 + S * STAGE + (chunk & 1) * SBUF + (p >> 1) * SSUB + (p & 1) * 288);
   };
   const int64_t nb = (col0 + wn * 16 * NJ) >> 7;
   const float* const sb_row = sbt + (nb < ((N + 127) >> 7) ? nb : 0) * KB;
@@ -187,8 +201,8 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     int sb_lanes = load_sb(0);
 #pragma unroll
     for (int q = 0; q < S_STEPS; ++q)
-      if (q * WAVES + w < S_PIECES) issue_s(0, q * WAVES + w);
-    for (int ks = 0; ks < S - 1 && ks < KB; ++ks) issue(ks, ks);
+      if (q * WAVES + w < S_PIECES) issue_s(0, q);
+    for (int ks = 0; ks < S - 1 && ks < KB; ++ks) issue(ks, ks * STAGE, std::true_type());
 
     const int sw0 = 16 * (g ^ (lo & 7)), sw1 = 16 * ((4 + g) ^ (lo & 7));
     const lds_u8* const ra = lds + (wm * 16 * MI + lo) * GK;
@@ -198,57 +212,81 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
       const v4i x = *(lds_v4i*)(base + sw0), y = *(lds_v4i*)(base + sw1);
       return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     };
+    auto multiply = [&](int ks, uint32_t at) __attribute__((always_inline)) {
+      const float sb =
+          __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb_lanes), ks & 63));
+      const lds_u8* const q = rs + ((ks >> 3) & 1) * SBUF + (ks & 7) * 32;
+      float sc[MI];
+      v8i_t bf[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) bf[j] = frag(rb + at + 16 * j * GK);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) sc[i] = *(lds_f32*)(q + i * SSUB);
+      v4f p[NJ];
+      v8i_t af[2];
+      af[0] = frag(ra + at);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (i + 1 < MI) af[(i + 1) & 1] = frag(ra + at + 16 * (i + 1) * GK);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if (i > 0) {
+            promote(acc[i - 1][j], p[j], sc[i - 1] * sb);
+            asm volatile("" : "+v"(acc[i - 1][j]));  // here, not where it is next needed
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          p[j] = mfma_block(bf[j], af[i & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) promote(acc[MI - 1][j], p[j], sc[MI - 1] * sb);
+    };
 
-    int slot = 0;
+    // Steps that load another whole one, without a branch between them but for the
+    // scales, then the rest.
+    uint32_t at = 0, free = (S - 1) * STAGE;
+    auto turn = [&]() __attribute__((always_inline)) {
+      free = at;
+      at = at == (S - 1) * STAGE ? 0 : at + STAGE;
+    };
+    int ks = 0;
+    const int whole = KB - (S - 1) - (partial ? 1 : 0);
 #pragma unroll 1
-    for (int ks = 0; ks < KB; ++ks) {
+    for (; ks < whole; ++ks) {
       if ((ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
-      wait_steps<S - 2, PIECES>(KB - 1 - ks);  // step ks has landed (scale loads only make it stricter)
-      lds_barrier();                           // ... for every wave; step ks-1's slot is free
-      const int free = slot == 0 ? S - 1 : slot - 1;
-      if ((ks & 7) < S_STEPS && (ks >> 3) < (KB - 1) >> 3 && (ks & 7) * WAVES + w < S_PIECES)
-        issue_s((ks >> 3) + 1, (ks & 7) * WAVES + w);
-      if (ks + S - 1 < KB) issue(ks + S - 1, free);
+      wait_vmcnt<(S - 2) * PIECES>();  // step ks has landed (scale loads only make it stricter)
+      lds_barrier();                   // ... for every wave; step ks-1's slot is free
+      if constexpr (S_STEPS == 1) {
+        if ((ks & 7) == 0 && w < S_PIECES) issue_s((ks >> 3) + 1, 0);
+      } else {
+#pragma unroll
+        for (int q = 0; q < S_STEPS; ++q)
+          if ((ks & 7) == q) issue_s((ks >> 3) + 1, q);
+      }
+      issue(ks + S - 1, free, std::false_type());
+      if (wave_live) multiply(ks, at);
+      turn();
+    }
+#pragma unroll 1
+    for (; ks < KB; ++ks) {
+      if ((ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
+      wait_steps<S - 2, PIECES>(KB - 1 - ks);
+      lds_barrier();
+#pragma unroll
+      for (int q = 0; q < S_STEPS; ++q)
+        if ((ks & 7) == q && (ks >> 3) < (KB - 1) >> 3 && q * WAVES + w < S_PIECES) issue_s((ks >> 3) + 1, q);
+      if (ks + S - 1 < KB) issue(ks + S - 1, free, std::true_type());
       if (partial && ks == KB - 1) {
         for (int x = threadIdx.x; x < (BM + BN) * 8; x += 64 * WAVES) {
           const int r = x >> 3, p = x & 7;
-          if (p >= (int)(K & 127) >> 4)
-            *(lds_v4i_w*)(lds + slot * STAGE + r * GK + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
+          if (p >= (int)(K & 127) >> 4) *(lds_v4i_w*)(lds + at + r * GK + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
         }
         lds_barrier();
       }
-      if (wave_live) {
-        const float sb =
-            __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb_lanes), ks & 63));
-        const lds_u8* const q = rs + ((ks >> 3) & 1) * SBUF + (ks & 7) * 32;
-        float sc[MI];
-        v8i_t bf[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) bf[j] = frag(rb + slot * STAGE + 16 * j * GK);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) sc[i] = *(lds_f32*)(q + i * SSUB);
-        v4f p[NJ];
-        v8i_t af[2];
-        af[0] = frag(ra + slot * STAGE);
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          if (i + 1 < MI) af[(i + 1) & 1] = frag(ra + slot * STAGE + 16 * (i + 1) * GK);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            if (i > 0) {
-              promote(acc[i - 1][j], p[j], sc[i - 1] * sb);
-              asm volatile("" : "+v"(acc[i - 1][j]));  // here, not where it is next needed
-              __builtin_amdgcn_sched_barrier(0);
-            }
-            p[j] = mfma_block(bf[j], af[i & 1]);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) promote(acc[MI - 1][j], p[j], sc[MI - 1] * sb);
-      }
-      slot = slot == S - 1 ? 0 : slot + 1;
+      if (wave_live) multiply(ks, at);
+      turn();
     }
   }
 

@@ -111,11 +111,15 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   static_assert(S_STEPS == 1 || S_STEPS * WAVES == S_PIECES, "every wave has a scale load in such a step");
   static_assert(NJ * 16 <= 128 && 128 % (NJ * 16) == 0, "a wave's columns lie in one weight block");
   static_assert(S_STEPS + S <= SCH, "a chunk of scales has landed before its first step");
-  static_assert(PIECES * (S - 2) < 64, "vmcnt range");
+  static_assert(PIECES * (S - 1) < 64, "vmcnt range");
+  // A small tile's wave holds the next step's fragments while it multiplies this
+  // one's, so that reading them is not waited for; a larger tile has no registers
+  // for that and two waves a SIMD to fill the time (64 x 8192 x 8192 20.6 -> 17.9 us,
+  // 300 x 1040 x 4096 11.8 -> 10.3; 512 x 8192 x 8192 with it 45, without 43).
+  constexpr int AHEAD = MI * NJ <= 4 ? 1 : 0;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
   typedef __attribute__((address_space(3))) const v4i lds_v4i;
-  typedef __attribute__((address_space(3))) v4i lds_v4i_w;
   typedef __attribute__((address_space(3))) const float lds_f32;
   lds_u8* const lds = (lds_u8*)smem;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   // ---- direct loads: piece p = w + i*WAVES is rows 8p .. 8p+7 of the stage (A's rows,
   // then the weight's); lane l loads row l >> 3, 16-byte piece (l & 7) ^ (row & 7).
   // Rows past the range read its last row (never stored); in the partial last
-  // K-block the pieces past K read the last whole piece (cleared afterwards).
+  // K-block the pieces past K read the last whole piece (see frag_a).
   const int piece = (lane & 7) ^ (lane >> 3);
   uint32_t off[PIECES];
 #pragma unroll
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 #pragma unroll
     for (int q = 0; q < S_STEPS; ++q)
       if (q * WAVES + w < S_PIECES) issue_s(0, q);
-    for (int ks = 0; ks < S - 1 && ks < KB; ++ks) issue(ks, ks * STAGE, std::true_type());
+    for (int ks = 0; ks < S - 1 + AHEAD && ks < KB; ++ks) issue(ks, ks * STAGE, std::true_type());
 
     const int sw0 = 16 * (g ^ (lo & 7)), sw1 = 16 * ((4 + g) ^ (lo & 7));
     const lds_u8* const ra = lds + (wm * 16 * MI + lo) * GK;
@@ -212,81 +216,108 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
       const v4i x = *(lds_v4i*)(base + sw0), y = *(lds_v4i*)(base + sw1);
       return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     };
-    auto multiply = [&](int ks, uint32_t at) __attribute__((always_inline)) {
+    // A's fragment.  LAST: zeros behind K, where the loads left the row's last piece
+    // again; the weight's keeps it, which is no NaN that its column has not.
+    auto frag_a = [&](const lds_u8* base, int ks, auto last) __attribute__((always_inline)) -> v8i_t {
+      v8i_t f = frag(base);
+      if constexpr (decltype(last)::value) {
+        const int rest = (int)K - ks * GK;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[e] = 16 * g < rest ? f[e] : 0;
+          f[4 + e] = 64 + 16 * g < rest ? f[4 + e] : 0;
+        }
+      }
+      return f;
+    };
+    struct Block {  // one K-block of the wave's part
+      v8i_t a[MI], b[NJ];
+      float sc[MI];
+    };
+    auto read = [&](Block& f, int ks, uint32_t at, auto last) __attribute__((always_inline)) {
+      const lds_u8* const q = rs + ((ks >> 3) & 1) * SBUF + (ks & 7) * 32;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) f.b[j] = frag(rb + at + 16 * j * GK);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) f.sc[i] = *(lds_f32*)(q + i * SSUB);
+#pragma unroll
+      for (int i = 0; i < (AHEAD ? MI : 1); ++i) f.a[i] = frag_a(ra + at + 16 * i * GK, ks, last);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto multiply = [&](Block& f, int ks, uint32_t at, auto last) __attribute__((always_inline)) {
       const float sb =
           __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sb_lanes), ks & 63));
-      const lds_u8* const q = rs + ((ks >> 3) & 1) * SBUF + (ks & 7) * 32;
-      float sc[MI];
-      v8i_t bf[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) bf[j] = frag(rb + at + 16 * j * GK);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) sc[i] = *(lds_f32*)(q + i * SSUB);
       v4f p[NJ];
-      v8i_t af[2];
-      af[0] = frag(ra + at);
 #pragma unroll
       for (int i = 0; i < MI; ++i) {
-        if (i + 1 < MI) af[(i + 1) & 1] = frag(ra + at + 16 * (i + 1) * GK);
+        if (!AHEAD && i + 1 < MI) f.a[i + 1] = frag_a(ra + at + 16 * (i + 1) * GK, ks, last);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           if (i > 0) {
-            promote(acc[i - 1][j], p[j], sc[i - 1] * sb);
+            promote(acc[i - 1][j], p[j], f.sc[i - 1] * sb);
             asm volatile("" : "+v"(acc[i - 1][j]));  // here, not where it is next needed
             __builtin_amdgcn_sched_barrier(0);
           }
-          p[j] = mfma_block(bf[j], af[i & 1]);
+          p[j] = mfma_block(f.b[j], f.a[i]);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) promote(acc[MI - 1][j], p[j], sc[MI - 1] * sb);
+      for (int j = 0; j < NJ; ++j) promote(acc[MI - 1][j], p[j], f.sc[MI - 1] * sb);
     };
-
-    // Steps that load another whole one, without a branch between them but for the
-    // scales, then the rest.
-    uint32_t at = 0, free = (S - 1) * STAGE;
-    auto turn = [&]() __attribute__((always_inline)) {
-      free = at;
-      at = at == (S - 1) * STAGE ? 0 : at + STAGE;
-    };
+    // One step.  REST: one of the last, whose own or next loads may be the partial
+    // K-block or lie behind the last one; without it the only branch is the scales'.
     int ks = 0;
-    const int whole = KB - (S - 1) - (partial ? 1 : 0);
-#pragma unroll 1
-    for (; ks < whole; ++ks) {
+    uint32_t at = 0, before = (S - 1) * STAGE;
+    auto step = [&](Block& now, Block& then, auto rest) __attribute__((always_inline)) {
+      constexpr bool REST = decltype(rest)::value;
       if ((ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
-      wait_vmcnt<(S - 2) * PIECES>();  // step ks has landed (scale loads only make it stricter)
-      lds_barrier();                   // ... for every wave; step ks-1's slot is free
-      if constexpr (S_STEPS == 1) {
-        if ((ks & 7) == 0 && w < S_PIECES) issue_s((ks >> 3) + 1, 0);
-      } else {
+      const uint32_t after = at == (S - 1) * STAGE ? 0 : at + STAGE;
+      if (!REST || ks + AHEAD < KB) {
+        if constexpr (REST) wait_steps<S - 2, PIECES>(KB - 1 - AHEAD - ks);
+        else wait_vmcnt<(S - 2) * PIECES>();  // step ks + AHEAD has landed (scale loads only make it stricter)
+        lds_barrier();                        // ... for every wave; step ks + AHEAD - 1's slot is free
 #pragma unroll
         for (int q = 0; q < S_STEPS; ++q)
-          if ((ks & 7) == q) issue_s((ks >> 3) + 1, q);
-      }
-      issue(ks + S - 1, free, std::false_type());
-      if (wave_live) multiply(ks, at);
-      turn();
-    }
-#pragma unroll 1
-    for (; ks < KB; ++ks) {
-      if ((ks & 63) == 0 && ks > 0) sb_lanes = load_sb(ks);
-      wait_steps<S - 2, PIECES>(KB - 1 - ks);
-      lds_barrier();
-#pragma unroll
-      for (int q = 0; q < S_STEPS; ++q)
-        if ((ks & 7) == q && (ks >> 3) < (KB - 1) >> 3 && q * WAVES + w < S_PIECES) issue_s((ks >> 3) + 1, q);
-      if (ks + S - 1 < KB) issue(ks + S - 1, free, std::true_type());
-      if (partial && ks == KB - 1) {
-        for (int x = threadIdx.x; x < (BM + BN) * 8; x += 64 * WAVES) {
-          const int r = x >> 3, p = x & 7;
-          if (p >= (int)(K & 127) >> 4) *(lds_v4i_w*)(lds + at + r * GK + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
+          if ((ks & 7) == q && (!REST || (ks >> 3) < (KB - 1) >> 3) && (S_STEPS > 1 || w < S_PIECES))
+            issue_s((ks >> 3) + 1, q);
+        if (!REST || ks + S - 1 + AHEAD < KB) issue(ks + S - 1 + AHEAD, AHEAD ? at : before, rest);
+        if constexpr (AHEAD) {
+          if (wave_live) read(then, ks + 1, after, rest);
         }
-        lds_barrier();
       }
-      if (wave_live) multiply(ks, at);
-      turn();
+      if (wave_live) {
+        if constexpr (!AHEAD) read(now, ks, at, rest);
+        multiply(now, ks, at, rest);
+      }
+      before = at;
+      at = after;
+      ++ks;
+    };
+    Block f0, f1;
+    if constexpr (AHEAD) {
+      wait_steps<S - 1, PIECES>(KB - 1);
+      lds_barrier();
+      if (wave_live) read(f0, 0, 0, std::true_type());
+    }
+    const int whole = KB - (S - 1) - AHEAD - (partial ? 1 : 0);
+    if constexpr (AHEAD) {
+#pragma unroll 1
+      while (ks + 2 <= whole) {
+        step(f0, f1, std::false_type());
+        step(f1, f0, std::false_type());
+      }
+#pragma unroll 1
+      while (ks < KB) {
+        step(f0, f1, std::true_type());
+        if (ks < KB) step(f1, f0, std::true_type());
+      }
+    } else {
+#pragma unroll 1
+      while (ks < whole) step(f0, f0, std::false_type());
+#pragma unroll 1
+      while (ks < KB) step(f0, f0, std::true_type());
     }
   }
 
@@ -670,120 +701,95 @@ static hipError_t launch_tile(const void* a, const float* sa, const void* bt, co
   return hipGetLastError();
 }
 
-// ---- few rows of a narrow weight: it is streamed once, straight to registers, by
-// workgroups of four waves that own 16 columns of C and all K, so that the few
+// ---- up to 16 rows of a narrow weight: it is streamed once, straight to registers,
+// by workgroups of four waves that own 16 columns of C and all K, so that the few
 // columns still occupy every CU.
 //
-// The waves share K: wave w forms the products of K-blocks KC*r + w*U .. +U-1 of
-// round r (KC = 4*U) and puts them into LDS beside their scale products; after
-// one barrier the same threads add the round's KC products to their
-// accumulators in ascending order.  So many K-blocks are in flight at once, yet
-// an element's sequence of operations is that of the tiles, whatever M is.  The
-// next round's loads are issued before the round's products are formed.
-template <int MT, int U>
+// The waves share K: wave w forms the products of K-blocks 8r + 2w and 8r + 2w + 1
+// of round r and puts them into LDS beside their scale products; after one barrier
+// the same threads add the round's eight products to their accumulators in
+// ascending order.  So many K-blocks are in flight at once, yet an element's
+// sequence of operations is that of the tiles, whatever M is.  The next round's
+// loads are issued before the round's products are formed.
+constexpr int RU = 2, RKC = 4 * RU;  // K-blocks of a wave and of a round
+
 __global__ void __launch_bounds__(256) gemm_g128_rows_kernel(const uint8_t* __restrict__ a,
                                                              const float* __restrict__ sa,
                                                              const uint8_t* __restrict__ bt,
                                                              const float* __restrict__ sbt,
                                                              uint16_t* __restrict__ c, int64_t M, int64_t N,
                                                              int64_t K) {
-  constexpr int KC = 4 * U;
-  constexpr int SL = (MT * U + 3) / 4;  // scale products per lane and round
-  __shared__ __attribute__((aligned(16))) float part[2][KC][MT * 256];
-  __shared__ float sprod[2][KC][16 * MT];
+  __shared__ __attribute__((aligned(16))) float part[2][RKC][256];
+  __shared__ float sprod[2][RKC][16];
   const int lane = threadIdx.x & 63;
   const int w = wave_id_uniform();
   const int g = lane >> 4, lo = lane & 15;
   const int KB = (int)((K + 127) >> 7);
   const bool partial = (K & 127) != 0;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int rounds = (KB + KC - 1) / KC;
+  const int rounds = (KB + RKC - 1) / RKC;
   const int last = (int)K - 16;  // K offset of the last whole piece
+  const int64_t a_row = lo < M ? lo : M - 1;
+  const uint8_t* const ap = a + a_row * K;
   const uint8_t* const bp = bt + (n0 + lo) * K;
+  const float* const sap = sa + a_row * KB;
   const float* const sbp = sbt + (n0 >> 7) * KB;
-  const uint8_t* ap[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) ap[i] = a + (16 * i + lo < M ? 16 * i + lo : M - 1) * K;
 
   struct Set {
-    v4i b[U][2], a[U][MT][2];
-    float sa[SL], sb[SL];
+    v4i b[RU][2], a[RU][2];
+    float sa, sb;  // of K-block g of the wave's, lanes g < RU
   };
   // Loads past the last K-block repeat it and are not used; pieces past K read the
   // last whole piece and are replaced by zeros.
   auto load = [&](Set& s, int r) __attribute__((always_inline)) {
-    const int kb0 = r * KC + w * U;
+    const int kb0 = r * RKC + w * RU;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < RU; ++u) {
       const int kb = kb0 + u < KB ? kb0 + u : KB - 1;
       int o0 = kb * GK + 16 * g, o1 = o0 + 64;
       o0 = o0 < last ? o0 : last;
       o1 = o1 < last ? o1 : last;
       s.b[u][0] = *reinterpret_cast<const v4i*>(bp + o0);
       s.b[u][1] = *reinterpret_cast<const v4i*>(bp + o1);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        s.a[u][i][0] = *reinterpret_cast<const v4i*>(ap[i] + o0);
-        s.a[u][i][1] = *reinterpret_cast<const v4i*>(ap[i] + o1);
-      }
+      s.a[u][0] = *reinterpret_cast<const v4i*>(ap + o0);
+      s.a[u][1] = *reinterpret_cast<const v4i*>(ap + o1);
     }
-    // scale product x of the lane: K-block u and row sub-tile i with u*MT + i = 4x + g
-#pragma unroll
-    for (int x = 0; x < SL; ++x) {
-      const int ui = 4 * x + g < MT * U ? 4 * x + g : MT * U - 1;
-      const int kb = kb0 + ui / MT < KB ? kb0 + ui / MT : KB - 1;
-      const int64_t row = 16 * (ui % MT) + lo;
-      s.sa[x] = sa[(row < M ? row : M - 1) * KB + kb];
-      s.sb[x] = sbp[kb];
-    }
+    const int u = g < RU ? g : RU - 1, kb = kb0 + u < KB ? kb0 + u : KB - 1;
+    s.sa = sap[kb];
+    s.sb = sbp[kb];
   };
   auto products = [&](Set& s, int r) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = r * KC + w * U + u;
+    for (int u = 0; u < RU; ++u) {
+      const int kb = r * RKC + w * RU + u;
       if (partial && kb == KB - 1) {
         const v4i z = {0, 0, 0, 0};
         const bool in0 = kb * GK + 16 * g < K, in1 = kb * GK + 64 + 16 * g < K;
         s.b[u][0] = in0 ? s.b[u][0] : z;
         s.b[u][1] = in1 ? s.b[u][1] : z;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          s.a[u][i][0] = in0 ? s.a[u][i][0] : z;
-          s.a[u][i][1] = in1 ? s.a[u][i][1] : z;
-        }
+        s.a[u][0] = in0 ? s.a[u][0] : z;
+        s.a[u][1] = in1 ? s.a[u][1] : z;
       }
       auto join = [](v4i x, v4i y) __attribute__((always_inline)) {
         return v8i_t{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
       };
-      const v8i_t bf = join(s.b[u][0], s.b[u][1]);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-        *reinterpret_cast<v4f*>(&part[r & 1][w * U + u][i * 256 + lane * 4]) =
-            mfma_block(bf, join(s.a[u][i][0], s.a[u][i][1]));
+      *reinterpret_cast<v4f*>(&part[r & 1][w * RU + u][lane * 4]) =
+          mfma_block(join(s.b[u][0], s.b[u][1]), join(s.a[u][0], s.a[u][1]));
     }
-#pragma unroll
-    for (int x = 0; x < SL; ++x) {
-      const int ui = 4 * x + g;
-      if (MT * U % 4 == 0 || ui < MT * U) sprod[r & 1][w * U + ui / MT][16 * (ui % MT) + lo] = s.sa[x] * s.sb[x];
-    }
+    if (g < RU) sprod[r & 1][w * RU + g][lo] = s.sa * s.sb;
   };
 
-  // thread t owns elements t*MT .. +MT-1 of the MT x 64 lanes x 4 results
-  const int e = threadIdx.x * MT;
-  const int row = (e >> 8) * 16 + ((e >> 2) & 15), col = ((e >> 6) & 3) * 4 + (e & 3);
-  float acc[MT];
-#pragma unroll
-  for (int x = 0; x < MT; ++x) acc[x] = 0.0f;
+  // thread t owns result t & 3 of lane t >> 2
+  const int row = (threadIdx.x >> 2) & 15, col = (threadIdx.x >> 6) * 4 + (threadIdx.x & 3);
+  float acc = 0.0f;
   auto chain = [&](int r) __attribute__((always_inline)) {
-    const int n = KB - r * KC < KC ? KB - r * KC : KC;
+    const int n = KB - r * RKC < RKC ? KB - r * RKC : RKC;
     auto add = [&](int k) __attribute__((always_inline)) {
-      const float s = sprod[r & 1][k][row];
-#pragma unroll
-      for (int x = 0; x < MT; ++x) acc[x] = __builtin_fmaf(part[r & 1][k][e + x], s, acc[x]);
+      acc = __builtin_fmaf(part[r & 1][k][threadIdx.x], sprod[r & 1][k][row], acc);
     };
-    if (n == KC) {
+    if (n == RKC) {
 #pragma unroll
-      for (int k = 0; k < KC; ++k) add(k);
+      for (int k = 0; k < RKC; ++k) add(k);
     } else {
       for (int k = 0; k < n; ++k) add(k);
     }
@@ -805,19 +811,7 @@ __global__ void __launch_bounds__(256) gemm_g128_rows_kernel(const uint8_t* __re
       chain(r + 1);
     }
   }
-  if (row < M) {
-    uint16_t* const cp = c + row * N + n0 + col;
-    if constexpr (MT == 1) *cp = (uint16_t)bf16_pair(acc[0], 0.0f);
-    else *reinterpret_cast<uint32_t*>(cp) = bf16_pair(acc[0], acc[1]);
-  }
-}
-
-template <int MT, int U>
-static hipError_t launch_rows(const void* a, const float* sa, const void* bt, const float* sbt, void* c, int64_t M,
-                              int64_t N, int64_t K, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_g128_rows_kernel<MT, U>), dim3((unsigned)(N / 16)), dim3(256), 0, stream,
-                     (const uint8_t*)a, sa, (const uint8_t*)bt, sbt, (uint16_t*)c, M, N, K);
-  return hipGetLastError();
+  if (row < M) c[row * N + n0 + col] = (uint16_t)bf16_pair(acc, 0.0f);
 }
 
 hipError_t set_gemm_g128_attributes() {
@@ -831,6 +825,7 @@ hipError_t set_gemm_g128_attributes() {
   if (e == hipSuccess) e = set_tile_attributes<2, 4, 4, 2, 3>();
   if (e == hipSuccess) e = set_tile_attributes<2, 4, 2, 2, 2>();
   if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 4, 3>();
+  if (e == hipSuccess) e = set_tile_attributes<2, 2, 2, 2, 4>();
   if (e == hipSuccess) e = set_tile_attributes<1, 2, 2, 2, 3>();
   if (e == hipSuccess) e = set_tile_attributes<1, 1, 2, 2, 4>();
   return e;
@@ -839,48 +834,53 @@ hipError_t set_gemm_g128_attributes() {
 // The kernel is the largest tile that still gives the 256 CUs enough workgroups:
 // a larger tile moves fewer bytes per flop, but tiles that do not fill the chip
 // leave CUs idle (M x N x K, us; [n] = the tile's count; 8w = eight waves and three
-// K-blocks in the ring, one workgroup a CU, else four waves, two a CU or more):
+// K-blocks in the ring, else four waves):
 //   512 x 28672 x 8192   256x256 [224] 110   128x128 156
-//   256 x 28672 x 8192   128x256 8w [224] 77  128x128 [448] 87  256x256 [112] 97
+//   256 x 28672 x 8192   128x256 8w [224] 78  128x128 [448] 87  256x256 [112] 97
 //   2048 x 4096 x 4096   128x256 8w [256] 39  128x128 [512] 40
-//   400 x 12288 x 1024   128x128 [384] 13.1   128x256 8w [192] 13.5
+//   400 x 12288 x 1024   128x128 [384] 12.4   128x256 8w [192] 13.1
 //   128 x 28672 x 8192   128x128 8w [224] 60  64x128 [448] 72
-//   700 x 5120 x 5120    128x128 8w [240] 29  64x128 [440] 30
-//   3000 x 992 x 2048    64x128 [376] 13.6    128x128 8w [192] 14.3
-//   256 x 8192 x 8192    64x128 8w [256] 33   64x64 [512] 35    32x64 36
-//   1024 x 2048 x 7168   64x128 8w [256] 29   64x64 [512] 31    128x128 8w 41
-//   128 x 8192 x 8192    32x64 [512] 28       64x128 8w [128] 33
-//   64 x 4096 x 4096     32x32 [256] 12       32x64 [128] 13
+//   700 x 5120 x 5120    128x128 8w [240] 28  64x128 [440] 29
+//   3000 x 992 x 2048    64x128 [376] 13.3    128x128 8w [192] 13.9
+//   256 x 8192 x 8192    64x128 8w [256] 30   64x128 [256] 38     32x64 34
+//   1024 x 2048 x 7168   64x128 8w [256] 27   128x128 8w [128] 41
+//   128 x 8192 x 8192    32x64 [512] 23       64x128 8w [128] 29
+//   64 x 4096 x 4096     32x32 [256] 9.9      32x64 [128] 10.3
+//   8 x 8192 x 8192      32x32 [256] 13.8     32x64 [128] 17     rows 16.6
+//   16 x 4096 x 4096     rows [256 x 16 columns] 6.9   32x32 [128] 8.5
+// One row tile of a wide weight is bound by the weight's stream, which needs bytes in
+// flight: the ring of 64x64 is four K-blocks deep (8 x 28672 x 8192: 46, 32x64 with
+// three 50; 64 x 28672 x 8192: 53, 55).
 // A range has half a tile too much on average, which the count includes, and a tile
 // is not chosen much taller than the ranges: rows past a range's end are work for
-// nothing (ranges x average rows, N x K: 64 x 8, 4096 x 2048: 32x64 93, 64x128 95;
-// 16 x 25, 4096 x 7168: 64x128 75, 128x128 81; 16 x 56: 128x256 8w 85, 64x128 95;
-// 16 x 125, 4096 x 2048: 64x128 36, 128x256 8w 40; 16 x 250, 2048 x 4096: 256x256
-// 55, 128x128 64).
-// Few rows of a narrow weight give too few tiles altogether (16 x 4096 x 4096: rows
-// 7.4, 32x32 11; 32 x 2048 x 7168: 14, 19), a wide weight enough (16 x 28672 x
-// 8192: rows 56, 32x64 48).
+// nothing (ranges x average rows, N x K: 64 x 8, 4096 x 2048: 32x64 94, 64x128 95;
+// 16 x 25, 4096 x 7168: 64x128 75, 128x128 82; 16 x 56: 128x256 8w 85, 64x128 95;
+// 16 x 125, 4096 x 2048: 64x128 34, 128x256 8w 40; 16 x 250, 2048 x 4096: 256x256
+// 56, 128x128 65).
 hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
-  if (!offsets && K > 0) {
-    if (M <= 16 && N <= 8192) return launch_rows<1, 2>(a, sa, bt, sbt, c, M, N, K, stream);
-    if (M <= 32 && N <= 4096) return launch_rows<2, 1>(a, sa, bt, sbt, c, M, N, K, stream);
-  }
   const int64_t live = G < M ? G : M;           // ranges that can have rows
   const int64_t avg = (M + live - 1) / live;    // rows of one
   auto tiles = [&](int64_t bm, int64_t bn) {
     const int64_t rows = offsets ? std::max(live, (M + live * (bm / 2)) / bm) : (M + bm - 1) / bm;
     return rows * ((N + bn - 1) / bn);
   };
+  if (!offsets && K > 0 && M <= 16 && tiles(32, 32) < 200) {
+    hipLaunchKernelGGL(gemm_g128_rows_kernel, dim3((unsigned)(N / 16)), dim3(256), 0, stream, (const uint8_t*)a, sa,
+                       (const uint8_t*)bt, sbt, (uint16_t*)c, M, N, K);
+    return hipGetLastError();
+  }
   const int64_t big = tiles(256, 256), wide = tiles(128, 256), square = tiles(128, 128), low = tiles(64, 128);
   if (avg >= 160 && big >= (offsets ? 160 : 200))
     return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (avg >= 48 && wide >= 200 && wide <= 256)
+  if (avg >= (offsets ? 48 : 65) && wide >= 200 && wide <= 256)
     return launch_tile<4, 4, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (avg > 64 && square >= 200 && square <= 256)
     return launch_tile<2, 4, 4, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (avg >= 128 && square > 256)
     return launch_tile<4, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+  if (!offsets && M <= 64 && tiles(64, 64) > 256)
+    return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (avg >= 20 && low > 256)
     return launch_tile<2, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (avg >= 20 && low >= 200)

@@ -78,30 +78,42 @@ __device__ __forceinline__ void transpose4x4(uint32_t r0, uint32_t r1, uint32_t 
   o[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
 }
 
+// 16 bytes, past the caches if PAST.
+template <bool PAST>
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  if constexpr (PAST) {
+    typedef unsigned v4u __attribute__((ext_vector_type(4)));
+    const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  } else {
+    return *reinterpret_cast<const uint4*>(p);
+  }
+}
+
 // One 256-thread workgroup per 128x128 block.  Lane (piece, rsub) of wave w holds
 // rows 32w + 8 rsub .. +7 of columns 8 piece .. +7, an 8x8 square that it transposes
 // by byte permutes; the transposed codes go through LDS so that whole
 // 128-byte rows of qt are written.
 constexpr int TPAD = 128 + 16;  // LDS row of 128 codes, 16-byte aligned, rows 4 banks apart
 
-//
-// LINES: columns (and rows, with the transpose) are multiples of 128, so every
-// 128-byte row of codes is one line, written past the caches.  Otherwise neighbouring
-// blocks share lines: blocks are walked in runs per XCD and written through
-// its L2, which joins them (8 x 4112 x 2064 with the transpose: 76 us, 101 the other
-// way; 8 x 4096 x 2048: 51 as lines, 61 through the L2).
+// LINES: columns are multiples of 128, so the lines of a block's rows belong to it
+// alone: they are read and written past the caches (8 x 4096 x 2048 with the
+// transpose 51 us, 61 through the L2).  Otherwise, or if the transposed rows are no
+// multiples of 128, neighbouring blocks share lines: they are walked in runs per
+// XCD and the shared lines go through its L2, which joins them (8 x 4112 x 2064 with
+// the transpose 76 us, past the caches 93; 8 x 4112 x 2048 63 us).
 template <bool TRANSPOSED, bool LINES>
 __global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                             int64_t cols, uint8_t* __restrict__ q,
                                                             float* __restrict__ scales, uint8_t* __restrict__ qt,
                                                             float* __restrict__ scales_t, uint32_t rb_count,
-                                                            uint32_t cb_count) {
+                                                            uint32_t cb_count, bool runs) {
   __shared__ uint32_t wave_max[4];
   __shared__ __attribute__((aligned(16))) uint8_t tile[TRANSPOSED ? 128 * TPAD : 16];
   const int lane = threadIdx.x & 63;
   const int w = threadIdx.x >> 6;
   const int piece = lane & 15, rsub = lane >> 4;
-  const uint32_t id = LINES ? blockIdx.x : xcd_run(blockIdx.x, gridDim.x);
+  const uint32_t id = runs ? xcd_run(blockIdx.x, gridDim.x) : blockIdx.x;
   const uint32_t cb = id % cb_count, rest = id / cb_count;
   const uint32_t rb = rest % rb_count;
   const int64_t gi = rest / rb_count;
@@ -116,7 +128,7 @@ __global__ void __launch_bounds__(256) quantize_b128_kernel(const uint16_t* __re
   for (int k = 0; k < 8; ++k) {
     const int64_t row = (int64_t)rb * 128 + r0 + k;
     ok[k] = row < rows && col < cols;
-    v[k] = ok[k] ? *reinterpret_cast<const uint4*>(x + row * cols + col) : make_uint4(0, 0, 0, 0);
+    v[k] = ok[k] ? load16<LINES>(x + row * cols + col) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -205,18 +217,17 @@ hipError_t launch_quantize_tg128(const void* x, int64_t rows, int64_t cols, void
 hipError_t launch_quantize_b128(const void* x, int64_t G, int64_t rows, int64_t cols, void* q, float* scales,
                                 void* qt, float* scales_t, hipStream_t stream) {
   const int64_t rb = (rows + 127) / 128, cb = (cols + 127) / 128;
+  const bool runs = cols % 128 != 0 || (qt && rows % 128 != 0);
   auto go = [&](auto TRANSPOSED_, auto LINES_) {
     hipLaunchKernelGGL((quantize_b128_kernel<decltype(TRANSPOSED_)::value, decltype(LINES_)::value>),
                        dim3((unsigned)(G * rb * cb)), dim3(256), 0, stream, (const uint16_t*)x, rows, cols,
-                       (uint8_t*)q, scales, (uint8_t*)qt, scales_t, (uint32_t)rb, (uint32_t)cb);
+                       (uint8_t*)q, scales, (uint8_t*)qt, scales_t, (uint32_t)rb, (uint32_t)cb, runs);
   };
-  if (qt) {
-    if (cols % 128 == 0 && rows % 128 == 0) go(std::true_type{}, std::true_type{});
-    else go(std::true_type{}, std::false_type{});
-  } else {
-    if (cols % 128 == 0) go(std::false_type{}, std::true_type{});
-    else go(std::false_type{}, std::false_type{});
-  }
+  const bool lines = cols % 128 == 0;
+  if (qt && lines) go(std::true_type{}, std::true_type{});
+  else if (qt) go(std::true_type{}, std::false_type{});
+  else if (lines) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 

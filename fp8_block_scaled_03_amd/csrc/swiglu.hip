@@ -1,7 +1,8 @@
 // y = silu(gate) * up with the row quantizer of its result, and its gradient.
 //
 //   sigma = 1 / (1 + exp(-g)),  y = g sigma u
-//   dg = dy u sigma (1 + g (1 - sigma)),  du = dy g sigma
+//   dg = dy u sigma (1 + g (1 - sigma)) = dy u (sigma + g sigma (1 - sigma)),
+//   du = dy g sigma
 // in fp32 from bf16 inputs; the codes are taken from the fp32 values.  With
 // e = exp(-|g|) <= 1 the two sigmoids sigma(|g|) = 1 / (1 + e) and sigma(-|g|) =
 // e / (1 + e) never overflow and 1 - sigma loses nothing.  The hardware's exp2
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(256) swiglu_quant_kernel(const uint16_t* __res
 __device__ __forceinline__ void swiglu_grad(float g, float u, float dy, float& dg, float& du, float& y) {
   const Sigmoid k = sigmoid(g);
   const float silu = g * k.s;
-  dg = dy * u * (k.s * (1.0f + g * k.c));
+  dg = dy * u * __builtin_fmaf(silu, k.c, k.s);  // dy u is exact
   du = dy * silu;
   y = silu * u;
 }

@@ -2,6 +2,7 @@
 // hold (eight values each): the group's maximum and the codes.
 #pragma once
 #include "common.hpp"
+#include "ragged.hpp"
 
 namespace fp8bs {
 
@@ -108,6 +109,19 @@ __device__ __forceinline__ uint32_t bf16_round_pair(float lo, float hi) {
 __device__ __forceinline__ uint4 bf16_round8(const float (&v)[8]) {
   return make_uint4(bf16_round_pair(v[0], v[1]), bf16_round_pair(v[2], v[3]), bf16_round_pair(v[4], v[5]),
                     bf16_round_pair(v[6], v[7]));
+}
+
+// Eight codes of a lane.  LINES: the rows of codes are multiples of 128, so each line
+// has one writer and is written past the caches; else neighbouring regions share
+// lines, and their writes meet in the L2 of the XCD that has the run of both.
+template <bool LINES>
+__device__ __forceinline__ void put_codes8(uint8_t* dst, uint2 codes) {
+  if constexpr (LINES) store_codes8(dst, codes.x, codes.y);
+  else *reinterpret_cast<uint2*>(dst) = codes;
+}
+template <bool LINES>
+__device__ __forceinline__ uint32_t region_at(uint32_t id, uint32_t n_regions) {
+  return LINES ? id : xcd_run(id, n_regions);
 }
 
 }  // namespace fp8bs

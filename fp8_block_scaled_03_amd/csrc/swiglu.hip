@@ -42,14 +42,17 @@ __device__ __forceinline__ Sigmoid sigmoid(float g) {
 
 // A region is 4 rows x 512 columns of y; a wave takes 128 columns (a group) of the
 // four rows.  (Two or four such loads per lane are slower: 8192 x 2048 forward
-// 16.2 us against 18.1, backward 37.4 against 39.5.)
+// 16.2 us against 18.1, backward 37.4 against 39.5.)  LINES as in put_codes8
+// (1500 x 4112 with it 10.1 us, without 8.6).
+template <bool LINES>
 __global__ void __launch_bounds__(256) swiglu_quant_kernel(const uint16_t* __restrict__ gu, int64_t rows, int64_t d,
                                                            uint8_t* __restrict__ q, float* __restrict__ scales,
                                                            uint16_t* __restrict__ y, uint32_t n_regions) {
   const int lane = threadIdx.x & 63;
   const int piece = lane & 15, rsub = lane >> 4;
   const uint32_t nb = (uint32_t)((d + 127) >> 7), quads = (nb + 3) >> 2;
-  for (uint32_t reg = blockIdx.x; reg < n_regions; reg += gridDim.x) {
+  for (uint32_t id = blockIdx.x; id < n_regions; id += gridDim.x) {
+    const uint32_t reg = region_at<LINES>(id, n_regions);
     const uint32_t rb = reg / quads, cb = (reg - rb * quads) * 4 + (threadIdx.x >> 6);
     const int64_t row = (int64_t)rb * 4 + rsub, col = (int64_t)cb * 128 + piece * 8;
     const bool ok = row < rows && col < d;
@@ -65,7 +68,7 @@ __global__ void __launch_bounds__(256) swiglu_quant_kernel(const uint16_t* __res
     // every group of the wave on the reciprocal path (the common case): no branches
     const uint2 codes = __all(sc.r != 0.0f || !ok) ? codes8<true>(v, sc) : codes8<false>(v, sc);
     if (ok) {
-      store_codes8(q + row * d + col, codes.x, codes.y);
+      put_codes8<LINES>(q + row * d + col, codes);
       if (y != nullptr) *reinterpret_cast<uint4*>(y + row * d + col) = bf16_round8(v);
       if (piece == 0) scales[row * nb + cb] = sc.s;
     }
@@ -84,8 +87,8 @@ __device__ __forceinline__ void swiglu_grad(float g, float u, float dy, float& d
 // in one half): a region of 4 rows x 512 columns of d gives the groups of both
 // halves from one load of its inputs.  Otherwise a group may reach over the
 // middle: regions run over the 2d columns, and a lane takes the half that its
-// eight columns lie in (d % 8 == 0); the inputs are then read twice, mostly from
-// the L2.
+// eight columns lie in (d % 8 == 0; the second needs no `up`); the inputs are then
+// read twice.
 template <bool HALVES>
 __global__ void __launch_bounds__(256) swiglu_backward_kernel(const uint16_t* __restrict__ gu,
                                                               const uint16_t* __restrict__ dy, int64_t rows,
@@ -96,7 +99,8 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(const uint16_t* __
   const int piece = lane & 15, rsub = lane >> 4;
   const uint32_t nb = (uint32_t)((2 * d + 127) >> 7);
   const uint32_t blocks = HALVES ? (uint32_t)(d >> 7) : nb, quads = (blocks + 3) >> 2;
-  for (uint32_t reg = blockIdx.x; reg < n_regions; reg += gridDim.x) {
+  for (uint32_t id = blockIdx.x; id < n_regions; id += gridDim.x) {
+    const uint32_t reg = region_at<HALVES>(id, n_regions);
     const uint32_t rb = reg / quads, cb = (reg - rb * quads) * 4 + (threadIdx.x >> 6);
     const int64_t row = (int64_t)rb * 4 + rsub, out_col = (int64_t)cb * 128 + piece * 8;
     const bool ok = row < rows && out_col < (HALVES ? d : 2 * d);
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(const uint16_t* __
     const int64_t col = second ? out_col - d : out_col;
     const uint16_t* const p = gu + row * 2 * d + col;
     const uint4 wg = ok ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-    const uint4 wu = ok ? *reinterpret_cast<const uint4*>(p + d) : make_uint4(0, 0, 0, 0);
+    const uint4 wu = ok && !second ? *reinterpret_cast<const uint4*>(p + d) : make_uint4(0, 0, 0, 0);
     const uint4 wd = ok ? *reinterpret_cast<const uint4*>(dy + row * d + col) : make_uint4(0, 0, 0, 0);
     float dg[8], du[8], dv[8], yv[8];
     unpack8(wg, dg);
@@ -117,7 +121,7 @@ __global__ void __launch_bounds__(256) swiglu_backward_kernel(const uint16_t* __
       const uint2 codes = __all(sc.r != 0.0f || !ok) ? codes8<true>(v, sc) : codes8<false>(v, sc);
       if (ok) {
         *reinterpret_cast<uint4*>(dgu + row * 2 * d + at) = bf16_round8(v);
-        store_codes8(q + row * 2 * d + at, codes.x, codes.y);
+        put_codes8<HALVES>(q + row * 2 * d + at, codes);
         if (piece == 0) scales[row * nb + block] = sc.s;
       }
     };
@@ -138,8 +142,13 @@ hipError_t launch_swiglu_quantize_tg128(const void* gu, int64_t rows, int64_t d,
                                         hipStream_t stream) {
   const int64_t n_regions = (rows + 3) / 4 * ((d + 511) / 512);
   if (n_regions > MAX_REGIONS) return hipErrorNotSupported;
-  hipLaunchKernelGGL(swiglu_quant_kernel, dim3((unsigned)(n_regions < MAX_GRID ? n_regions : MAX_GRID)), dim3(256),
-                     0, stream, (const uint16_t*)gu, rows, d, (uint8_t*)q, scales, (uint16_t*)y, (uint32_t)n_regions);
+  const dim3 grid((unsigned)(n_regions < MAX_GRID ? n_regions : MAX_GRID));
+  if (d % 128 == 0)
+    hipLaunchKernelGGL(swiglu_quant_kernel<true>, grid, dim3(256), 0, stream, (const uint16_t*)gu, rows, d,
+                       (uint8_t*)q, scales, (uint16_t*)y, (uint32_t)n_regions);
+  else
+    hipLaunchKernelGGL(swiglu_quant_kernel<false>, grid, dim3(256), 0, stream, (const uint16_t*)gu, rows, d,
+                       (uint8_t*)q, scales, (uint16_t*)y, (uint32_t)n_regions);
   return hipGetLastError();
 }
 

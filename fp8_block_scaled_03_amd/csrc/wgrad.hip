@@ -13,9 +13,11 @@
 #include "launch_g128.hpp"
 #include "ragged.hpp"
 
+#include <type_traits>
+
 namespace fp8bs {
 
-constexpr int WT = 32;  // rows (of dY and X) per step: the depth of one bf16 MFMA
+constexpr int WT = 32;  // rows (of dY and X): the depth of one bf16 MFMA
 
 // LDS stage of one operand: WT rows of COLS bf16; the 32-byte chunk J of row r
 // lies at chunk J ^ sw(r).  A transpose read takes 32 bytes of four rows per
@@ -27,8 +29,11 @@ __device__ __forceinline__ constexpr int wg_sw(int r, int cols) {
 }
 
 // A tile of BK = 16*MI*WK columns of X by BN = 16*NJ*WN columns of dY per
-// workgroup of WK x WN waves; ring of S stages of WT rows.
-template <int MI, int NJ, int WK, int WN, int S>
+// workgroup of WK x WN waves; ring of S stages of R*WT rows.  The steps that load
+// another whole stage have no branch between them: with few small tiles the loop's
+// own instructions were most of the time (1 x 16384 x 1024 x 1024 with 64x64 128 us,
+// 78 so, 68 with two times WT rows between the barriers).
+template <int MI, int NJ, int WK, int WN, int S, int R>
 __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __restrict__ dy,
                                                              const uint16_t* __restrict__ x,
                                                              const int32_t* __restrict__ offsets,
@@ -36,9 +41,9 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
                                                              int64_t N, int64_t K, uint32_t tiles_n,
                                                              uint32_t tiles_k) {
   constexpr int BK = 16 * MI * WK, BN = 16 * NJ * WN, WAVES = WK * WN;
-  constexpr int X_BYTES = WT * BK * 2, STAGE = WT * (BK + BN) * 2;
-  constexpr int X_PIECES = X_BYTES / 1024 / WAVES, Y_PIECES = WT * BN * 2 / 1024 / WAVES;
-  static_assert(X_PIECES * WAVES * 1024 == X_BYTES && Y_PIECES * WAVES * 1024 == WT * BN * 2, "whole loads");
+  constexpr int RT = R * WT, X_BYTES = RT * BK * 2, STAGE = RT * (BK + BN) * 2;
+  constexpr int X_PIECES = X_BYTES / 1024 / WAVES, Y_PIECES = RT * BN * 2 / 1024 / WAVES;
+  static_assert(X_PIECES * WAVES * 1024 == X_BYTES && Y_PIECES * WAVES * 1024 == RT * BN * 2, "whole loads");
   static_assert(MI % 2 == 0 && BK >= 64 && BN >= 64, "the swizzle and the epilogue's pairs");
   constexpr int PIECES = X_PIECES + Y_PIECES;
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(tn) * BN;
   const int k_valid = (int)(K - k0 < BK ? K - k0 : BK), n_valid = (int)(N - n0 < BN ? N - n0 : BN);
   const int rows = (int)(end - begin);
-  const int steps = (rows + WT - 1) / WT;
+  const int steps = (rows + RT - 1) / RT;
   dw += (int64_t)gi * N * K;
 
   // ---- direct loads: 16 bytes (eight columns) per lane; lane l of piece p fills
@@ -87,37 +92,31 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
   const uint32_t ring = (uint32_t)(uintptr_t)((lds_u8*)smem);
 
-  // In the last step the rows past the range read its last row; their LDS bytes
-  // are cleared before they are used.
-  auto issue = [&](int t) __attribute__((always_inline)) {
-    const uint32_t slot = ring + (t % S) * STAGE;
-    const uint8_t* const xt = x0 + (int64_t)t * WT * K * 2;
-    const uint8_t* const yt = y0 + (int64_t)t * WT * N * 2;
-    const int left = rows - t * WT;
-    if (left >= WT) {
+  // The load of step t into the slot at `at`.  LAST: it may be the last one, where rows
+  // past the range read its last row; their LDS bytes are cleared before they are used.
+  auto issue = [&](int t, uint32_t at, auto last) __attribute__((always_inline)) {
+    const uint8_t* const xt = x0 + (int64_t)t * RT * K * 2;
+    const uint8_t* const yt = y0 + (int64_t)t * RT * N * 2;
+    const int left = rows - t * RT;
 #pragma unroll
-      for (int i = 0; i < X_PIECES; ++i) dma16_at(xt, x_off[i], slot + (w * X_PIECES + i) * 1024);
+    for (int i = 0; i < X_PIECES; ++i) {
+      uint32_t back = 0;
+      if constexpr (decltype(last)::value) back = x_row[i] < left ? 0 : x_row[i] - left + 1;
+      dma16_at(xt, x_off[i] - back * (uint32_t)(K * 2), ring + at + (w * X_PIECES + i) * 1024);
+    }
 #pragma unroll
-      for (int i = 0; i < Y_PIECES; ++i) dma16_at(yt, y_off[i], slot + X_BYTES + (w * Y_PIECES + i) * 1024);
-    } else {
-#pragma unroll
-      for (int i = 0; i < X_PIECES; ++i) {
-        const int back = x_row[i] < left ? 0 : x_row[i] - left + 1;
-        dma16_at(xt, x_off[i] - (uint32_t)back * (uint32_t)(K * 2), slot + (w * X_PIECES + i) * 1024);
-      }
-#pragma unroll
-      for (int i = 0; i < Y_PIECES; ++i) {
-        const int back = y_row[i] < left ? 0 : y_row[i] - left + 1;
-        dma16_at(yt, y_off[i] - (uint32_t)back * (uint32_t)(N * 2), slot + X_BYTES + (w * Y_PIECES + i) * 1024);
-      }
+    for (int i = 0; i < Y_PIECES; ++i) {
+      uint32_t back = 0;
+      if constexpr (decltype(last)::value) back = y_row[i] < left ? 0 : y_row[i] - left + 1;
+      dma16_at(yt, y_off[i] - back * (uint32_t)(N * 2), ring + at + X_BYTES + (w * Y_PIECES + i) * 1024);
     }
   };
-  auto clear_rows = [&](int t) __attribute__((always_inline)) {
-    const int left = rows - t * WT;
-    unsigned char* const slot = smem + (t % S) * STAGE;
+  auto clear_rows = [&](int t, uint32_t at) __attribute__((always_inline)) {
+    const int left = rows - t * RT;
+    unsigned char* const slot = smem + at;
     for (int b = left * BK * 2 + (int)threadIdx.x * 16; b < X_BYTES; b += 64 * WAVES * 16)
       *reinterpret_cast<v4i*>(slot + b) = v4i{0, 0, 0, 0};
-    for (int b = left * BN * 2 + (int)threadIdx.x * 16; b < WT * BN * 2; b += 64 * WAVES * 16)
+    for (int b = left * BN * 2 + (int)threadIdx.x * 16; b < RT * BN * 2; b += 64 * WAVES * 16)
       *reinterpret_cast<v4i*>(slot + X_BYTES + b) = v4i{0, 0, 0, 0};
   };
 
@@ -140,28 +139,48 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int t = 0; t < S - 1 && t < steps; ++t) issue(t);
-#pragma unroll 1
-  for (int t = 0; t < steps; ++t) {
-    wait_steps<S - 2, PIECES>(steps - 1 - t);  // step t has landed
-    lds_barrier();                             // ... for every wave; step t-1's slot is free
-    if (t + S - 1 < steps) issue(t + S - 1);
-    if (t == steps - 1 && rows % WT) {
-      clear_rows(t);
+  auto multiply = [&](uint32_t at) __attribute__((always_inline)) {
+    const unsigned char* const slot = smem + at;
+#pragma unroll
+    for (int h = 0; h < R; ++h) {
+      const unsigned char* const xs = slot + h * WT * BK * 2;
+      const unsigned char* const ys = slot + X_BYTES + h * WT * BN * 2;
+      v8bf yf[NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) yf[j] = frag(ys, BN, wn * NJ + j);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const v8bf xf = frag(xs, BK, wk * MI + i);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, yf[j], acc[i][j], 0, 0, 0);
+      }
+    }
+  };
+  for (int t = 0; t < S - 1 && t < steps; ++t) issue(t, t * STAGE, std::true_type());
+  uint32_t at = 0, before = (S - 1) * STAGE;
+  int t = 0;
+  auto step = [&](auto rest) __attribute__((always_inline)) {
+    constexpr bool REST = decltype(rest)::value;
+    if constexpr (REST) wait_steps<S - 2, PIECES>(steps - 1 - t);
+    else wait_vmcnt<(S - 2) * PIECES>();  // step t has landed
+    lds_barrier();                        // ... for every wave; step t-1's slot is free
+    if (!REST || t + S - 1 < steps) issue(t + S - 1, before, rest);
+    if (REST && t == steps - 1 && rows % RT) {
+      clear_rows(t, at);
       lds_barrier();
     }
-    const unsigned char* const slot = smem + (t % S) * STAGE;
-    v8bf yf[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) yf[j] = frag(slot + X_BYTES, BN, wn * NJ + j);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const v8bf xf = frag(slot, BK, wk * MI + i);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, yf[j], acc[i][j], 0, 0, 0);
-    }
-  }
+    multiply(at);
+    before = at;
+    at = at == (S - 1) * STAGE ? 0 : at + STAGE;
+    ++t;
+  };
+  // the steps that load another whole one, then the rest
+  const int whole = steps - (S - 1) - (rows % RT ? 1 : 0);
+#pragma unroll 1
+  while (t < whole) step(std::false_type());
+#pragma unroll 1
+  while (t < steps) step(std::true_type());
 
   // ---- lane (tg, lo) holds n = 16j + lo, k = 16i + 4 tg .. +3 of its wave's part: 64
   // bytes of 16 rows per store.  Lanes lo and lo ^ 8 exchange one of two
@@ -203,35 +222,35 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
   }
 }
 
-template <int MI, int NJ, int WK, int WN, int S>
+template <int MI, int NJ, int WK, int WN, int S, int R>
 constexpr int wgrad_lds() {
-  return S * WT * (16 * MI * WK + 16 * NJ * WN) * 2;
+  return S * R * WT * (16 * MI * WK + 16 * NJ * WN) * 2;
 }
 
-template <int MI, int NJ, int WK, int WN, int S>
+template <int MI, int NJ, int WK, int WN, int S, int R>
 static hipError_t launch_wgrad_t(const void* dy, const void* x, const int32_t* offsets, int G, float* dw,
                                  bool accumulate, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   constexpr int BK = 16 * MI * WK, BN = 16 * NJ * WN, THREADS = 64 * WK * WN;
   const int64_t tiles_n = (N + BN - 1) / BN, tiles_k = (K + BK - 1) / BK;
   if (G * tiles_n * tiles_k > (int64_t)0xFFFFFFFF / THREADS) return hipErrorNotSupported;
-  hipLaunchKernelGGL((wgrad_kernel<MI, NJ, WK, WN, S>), dim3((unsigned)(G * tiles_n * tiles_k)), dim3(THREADS),
-                     (wgrad_lds<MI, NJ, WK, WN, S>()), stream, (const uint16_t*)dy, (const uint16_t*)x, offsets, dw,
+  hipLaunchKernelGGL((wgrad_kernel<MI, NJ, WK, WN, S, R>), dim3((unsigned)(G * tiles_n * tiles_k)), dim3(THREADS),
+                     (wgrad_lds<MI, NJ, WK, WN, S, R>()), stream, (const uint16_t*)dy, (const uint16_t*)x, offsets, dw,
                      accumulate ? 1 : 0, M, N, K, (uint32_t)tiles_n, (uint32_t)tiles_k);
   return hipGetLastError();
 }
 
-template <int MI, int NJ, int WK, int WN, int S>
+template <int MI, int NJ, int WK, int WN, int S, int R>
 static hipError_t set_wgrad_t() {
-  return hipFuncSetAttribute((const void*)wgrad_kernel<MI, NJ, WK, WN, S>,
-                             hipFuncAttributeMaxDynamicSharedMemorySize, wgrad_lds<MI, NJ, WK, WN, S>());
+  return hipFuncSetAttribute((const void*)wgrad_kernel<MI, NJ, WK, WN, S, R>,
+                             hipFuncAttributeMaxDynamicSharedMemorySize, wgrad_lds<MI, NJ, WK, WN, S, R>());
 }
 
 hipError_t set_wgrad_attributes() {
-  hipError_t e = set_wgrad_t<8, 4, 2, 2, 3>();
-  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 3>();
-  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 2>();
-  if (e == hipSuccess) e = set_wgrad_t<4, 2, 2, 2, 4>();
-  if (e == hipSuccess) e = set_wgrad_t<2, 2, 2, 2, 4>();
+  hipError_t e = set_wgrad_t<8, 4, 2, 2, 3, 1>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 3, 1>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 2, 1>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 2, 2, 2, 4, 1>();
+  if (e == hipSuccess) e = set_wgrad_t<2, 2, 2, 2, 3, 2>();
   return e;
 }
 
@@ -239,25 +258,26 @@ hipError_t set_wgrad_attributes() {
 // workgroups per CU let one write its tile while others compute; long ranges gain
 // from larger tiles and deeper rings, few tiles from smaller ones (ranges x rows
 // each, N x K, us):
-//   16 x 2048, 4096 x 2048   256x128 (3 steps) 519   128x128 (2) 564
-//   64 x 512, 2048 x 1024    256x128 (3) 234   128x128 (2) 249
-//   64 x 128, 2048 x 1024    128x128 (2) 101   256x128 (3) 107   128x128 (3) 105
-//   4 x 1024, 2048 x 2048    128x128 (3) 42    128x128 (2) 50
-//   1 x 8192, 2048 x 2048    128x64 (4) 87     128x128 (3) 94    64x64 (4) 138
-//   1 x 16384, 1024 x 1024   64x64 (4) 122     128x64 (4) 147
+//   16 x 512, 4096 x 2048    256x128 (3 steps) 208   128x128 (2) 222
+//   64 x 512, 2048 x 1024    256x128 (3) 232   128x128 (2) 242
+//   64 x 128, 2048 x 1024    128x128 (2) 100   128x128 (3) 103   256x128 (3) 108
+//   4 x 4096, 2048 x 2048    128x128 (3) 147   256x128 (3) 152   128x128 (2) 174
+//   1 x 8192, 2048 x 2048    128x128 (3) 77    128x64 (4) 82
+//   3 x 2300, 1200 x 896     128x64 (4) 34     64x64 35
+//   1 x 16384, 1024 x 1024   64x64 68          128x64 (4) 118
 hipError_t launch_grouped_wgrad(const void* dy, const void* x, const int32_t* offsets, int G, float* dw,
                                 bool accumulate, int64_t M_total, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t avg = M_total / G;  // rows per range
   auto tiles = [&](int64_t bk, int64_t bn) { return G * ((N + bn - 1) / bn) * ((K + bk - 1) / bk); };
   if (avg >= 400 && tiles(256, 128) >= 1024)
-    return launch_wgrad_t<8, 4, 2, 2, 3>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
-  if (tiles(128, 128) > 400) {
-    if (avg >= 400) return launch_wgrad_t<4, 4, 2, 2, 3>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
-    return launch_wgrad_t<4, 4, 2, 2, 2>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+    return launch_wgrad_t<8, 4, 2, 2, 3, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  if (tiles(128, 128) > (avg >= 400 ? 200 : 400)) {
+    if (avg >= 400) return launch_wgrad_t<4, 4, 2, 2, 3, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+    return launch_wgrad_t<4, 4, 2, 2, 2, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
   }
   if (tiles(128, 64) > 256)
-    return launch_wgrad_t<4, 2, 2, 2, 4>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
-  return launch_wgrad_t<2, 2, 2, 2, 4>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+    return launch_wgrad_t<4, 2, 2, 2, 4, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  return launch_wgrad_t<2, 2, 2, 2, 3, 2>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
 }
 
 }  // namespace fp8bs

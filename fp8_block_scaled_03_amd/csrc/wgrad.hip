@@ -139,23 +139,26 @@ __global__ void __launch_bounds__(64 * WK * WN) wgrad_kernel(const uint16_t* __r
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // All of a step's fragments are asked for before its first MFMA (4096 rows, 4096 x
+  // 4096: 122 us, 134 in the compiler's order).
   auto multiply = [&](uint32_t at) __attribute__((always_inline)) {
     const unsigned char* const slot = smem + at;
+    v8bf xf[R][MI], yf[R][NJ];
 #pragma unroll
     for (int h = 0; h < R; ++h) {
-      const unsigned char* const xs = slot + h * WT * BK * 2;
-      const unsigned char* const ys = slot + X_BYTES + h * WT * BN * 2;
-      v8bf yf[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) yf[j] = frag(ys, BN, wn * NJ + j);
+      for (int j = 0; j < NJ; ++j) yf[h][j] = frag(slot + X_BYTES + h * WT * BN * 2, BN, wn * NJ + j);
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const v8bf xf = frag(xs, BK, wk * MI + i);
+      for (int i = 0; i < MI; ++i) xf[h][i] = frag(slot + h * WT * BK * 2, BK, wk * MI + i);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < R; ++h)
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, yf[j], acc[i][j], 0, 0, 0);
-      }
-    }
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[h][i], yf[h][j], acc[i][j], 0, 0, 0);
   };
   for (int t = 0; t < S - 1 && t < steps; ++t) issue(t, t * STAGE, std::true_type());
   uint32_t at = 0, before = (S - 1) * STAGE;
@@ -247,6 +250,7 @@ static hipError_t set_wgrad_t() {
 
 hipError_t set_wgrad_attributes() {
   hipError_t e = set_wgrad_t<8, 4, 2, 2, 3, 1>();
+  if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 4, 3, 1>();
   if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 3, 1>();
   if (e == hipSuccess) e = set_wgrad_t<4, 4, 2, 2, 2, 1>();
   if (e == hipSuccess) e = set_wgrad_t<4, 2, 2, 2, 4, 1>();
@@ -258,19 +262,22 @@ hipError_t set_wgrad_attributes() {
 // workgroups per CU let one write its tile while others compute; long ranges gain
 // from larger tiles and deeper rings, few tiles from smaller ones (ranges x rows
 // each, N x K, us):
-//   16 x 512, 4096 x 2048    256x128 (3 steps) 208   128x128 (2) 222
-//   64 x 512, 2048 x 1024    256x128 (3) 232   128x128 (2) 242
-//   64 x 128, 2048 x 1024    128x128 (2) 100   128x128 (3) 103   256x128 (3) 108
-//   4 x 4096, 2048 x 2048    128x128 (3) 147   256x128 (3) 152   128x128 (2) 174
-//   1 x 8192, 2048 x 2048    128x128 (3) 77    128x64 (4) 82
-//   3 x 2300, 1200 x 896     128x64 (4) 34     64x64 35
-//   1 x 16384, 1024 x 1024   64x64 68          128x64 (4) 118
+//   16 x 512, 4096 x 2048    256x128 (3 steps) 208   128x256 (3) 209   128x128 (2) 222
+//   64 x 512, 2048 x 1024    256x128 (3) 232   128x256 (3) 239   128x128 (2) 242
+//   64 x 128, 2048 x 1024    128x128 (2) 99    128x128 (3) 108   128x256 (3) 110
+//   1 x 4096, 4096 x 4096    128x256 (3) 113   256x128 (3) 118   128x128 (3) 122
+//   4 x 4096, 2048 x 2048    128x256 (3) 143   128x128 (3) 148   256x128 (3) 152
+//   1 x 8192, 2048 x 2048    128x128 (3) 71    128x64 (4) 80
+//   3 x 2300, 1200 x 896     128x128 (3) 31    128x64 (4) 32     64x64 34
+//   1 x 16384, 1024 x 1024   64x64 66          128x64 (4) 118
 hipError_t launch_grouped_wgrad(const void* dy, const void* x, const int32_t* offsets, int G, float* dw,
                                 bool accumulate, int64_t M_total, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t avg = M_total / G;  // rows per range
   auto tiles = [&](int64_t bk, int64_t bn) { return G * ((N + bn - 1) / bn) * ((K + bk - 1) / bk); };
   if (avg >= 400 && tiles(256, 128) >= 1024)
     return launch_wgrad_t<8, 4, 2, 2, 3, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
+  if (avg >= 400 && tiles(128, 256) >= 512)
+    return launch_wgrad_t<4, 4, 2, 4, 3, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
   if (tiles(128, 128) > (avg >= 400 ? 200 : 400)) {
     if (avg >= 400) return launch_wgrad_t<4, 4, 2, 2, 3, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);
     return launch_wgrad_t<4, 4, 2, 2, 2, 1>(dy, x, offsets, G, dw, accumulate, M_total, N, K, stream);

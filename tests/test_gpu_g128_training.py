@@ -64,7 +64,7 @@ def test_wgrad_large_tiles():
 
 
 @pytest.mark.parametrize("G,M,N,K", [(16, 6500, 2064, 2000), (4, 2000, 2048, 2064), (1, 8000, 2048, 2000),
-                                     (8, 333, 1040, 528), (1, 5000, 272, 144)])
+                                     (3, 1500, 2048, 2000), (8, 333, 1040, 528), (1, 5000, 272, 144)])
 def test_wgrad_every_tile(G, M, N, K):
     """Sizes that reach every tile, uneven ranges, against fp64 on the GPU; replacing and adding."""
     rng = np.random.default_rng(G * M)

@@ -108,7 +108,7 @@ def _need(t: torch.Tensor, name: str, dtypes, ndim: int) -> None:
         raise ValueError(f"{name}: expected {ndim} dims, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
 
 
@@ -500,7 +500,7 @@ def quantize_tg128(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch
     dev = x.device
     q = _output(q, "q", E4M3_DTYPES, (R, C), dev)
     scales = _output(scales, "scales", _F32, (R, _blocks128(C)), dev)
-    _call_on(dev, "fp8bs_quantize_tg128", _ptr(x), R, C, _ptr(q), _ptr(scales))
+    _call_on(dev, "fp8bs_quantize_tg128", x.data_ptr(), R, C, q.data_ptr(), scales.data_ptr())
     return q, scales
 
 
@@ -526,7 +526,8 @@ def quantize_b128(x: torch.Tensor, q: torch.Tensor | None = None, scales: torch.
     if transposed:
         qt = _output(qt, "qt", E4M3_DTYPES, lead + (C, R), dev)
         scales_t = _output(scales_t, "scales_t", _F32, lead + (_blocks128(C), _blocks128(R)), dev)
-    _call_on(dev, "fp8bs_quantize_b128", _ptr(x), G, R, C, _ptr(q), _ptr(scales), _ptr(qt), _ptr(scales_t))
+    _call_on(dev, "fp8bs_quantize_b128", x.data_ptr(), G, R, C, q.data_ptr(), scales.data_ptr(), _ptr(qt),
+             _ptr(scales_t))
     return (q, scales, qt, scales_t) if transposed else (q, scales)
 
 
@@ -541,7 +542,8 @@ def gemm_tg128_nt(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, sbt: torc
     _need_like(sa, "sa", _F32, (M, KB), dev)
     _need_like(sbt, "sbt", _F32, (_blocks128(N), KB), dev)
     out = _output(out, "out", _BF16, (M, N), dev)
-    _call_on(dev, "fp8bs_gemm_tg128_nt", _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(out), M, N, K)
+    _call_on(dev, "fp8bs_gemm_tg128_nt", a.data_ptr(), sa.data_ptr(), bt.data_ptr(), sbt.data_ptr(), out.data_ptr(), M,
+             N, K)
     return out
 
 
@@ -561,8 +563,8 @@ def grouped_gemm_tg128_nt(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, s
     _need_like(sa, "sa", _F32, (M, KB), dev)
     _need_like(sbt, "sbt", _F32, (G, _blocks128(N), KB), dev)
     out = _output(out, "out", _BF16, (M, N), dev)
-    _call_on(dev, "fp8bs_grouped_gemm_tg128_nt", _ptr(a), _ptr(sa), _ptr(bt), _ptr(sbt), _ptr(offsets), G, _ptr(out),
-             M, N, K)
+    _call_on(dev, "fp8bs_grouped_gemm_tg128_nt", a.data_ptr(), sa.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
+             offsets.data_ptr(), G, out.data_ptr(), M, N, K)
     return out
 
 
@@ -582,8 +584,8 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out:
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     out = _output(out, "out", _F32, (G, N, K), dev)
-    _call_on(dev, "fp8bs_grouped_wgrad", _ptr(dy), _ptr(x), _ptr(offsets), G, _ptr(out), 1 if accumulate else 0, M, N,
-             K)
+    _call_on(dev, "fp8bs_grouped_wgrad", dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), G, out.data_ptr(),
+             1 if accumulate else 0, M, N, K)
     return out
 
 
@@ -601,7 +603,7 @@ def swiglu_quantize_tg128(gu: torch.Tensor, q: torch.Tensor | None = None, scale
     scales = _output(scales, "scales", _F32, (R, _blocks128(d)), dev)
     if y is not None or want_y:
         y = _output(y, "y", _BF16, (R, d), dev)
-    _call_on(dev, "fp8bs_swiglu_quantize_tg128", _ptr(gu), R, d, _ptr(q), _ptr(scales), _ptr(y))
+    _call_on(dev, "fp8bs_swiglu_quantize_tg128", gu.data_ptr(), R, d, q.data_ptr(), scales.data_ptr(), _ptr(y))
     return (q, scales) if y is None else (q, scales, y)
 
 
@@ -621,6 +623,6 @@ def swiglu_backward_quantize_tg128(gu: torch.Tensor, dy: torch.Tensor, dgu: torc
     scales = _output(scales, "scales", _F32, (R, _blocks128(2 * d)), dev)
     if y is not None or want_y:
         y = _output(y, "y", _BF16, (R, d), dev)
-    _call_on(dev, "fp8bs_swiglu_backward_quantize_tg128", _ptr(gu), _ptr(dy), R, d, _ptr(dgu), _ptr(q), _ptr(scales),
-             _ptr(y))
+    _call_on(dev, "fp8bs_swiglu_backward_quantize_tg128", gu.data_ptr(), dy.data_ptr(), R, d, dgu.data_ptr(),
+             q.data_ptr(), scales.data_ptr(), _ptr(y))
     return (dgu, q, scales) if y is None else (dgu, q, scales, y)

@@ -58,8 +58,8 @@ __device__ __forceinline__ uint4 bf16_octet(v4f x, v4f y) {
 // The MI x NJ sub-tiles of a wave, from row and column `r0`, `c0` of the tile at `c`:
 // a lane holds row 16i + lo, columns 16j + 4g .. +3.
 template <int MI, int NJ>
-__device__ __forceinline__ void store_wave(uint16_t* c, int64_t N, const v4f (&acc)[MI][NJ], int r0, int c0, int m_valid,
-                                           int n_valid) {
+__device__ __forceinline__ void store_wave(uint16_t* c, int64_t N, const v4f (&acc)[MI][NJ], int r0, int c0,
+                                           int m_valid, int n_valid) {
   const int g = (threadIdx.x & 63) >> 4, lo = threadIdx.x & 15;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     return over > 0 ? over : 0;
   };
 
-  auto issue_a = [&](int ks, int i, uint32_t back = 0) __attribute__((always_inline)) {  // i 0, 1: sub-tiles 0-3; 2, 3: 4-7
+  // i 0, 1: row sub-tiles 0-3; 2, 3: 4-7
+  auto issue_a = [&](int ks, int i, uint32_t back = 0) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + X_A + (ks & 1) * X_SLOT + (a_first + (i >> 1) * 64 + (i & 1) * 8) * GK;
     dma16_at(a0 + (int64_t)ks * GK, a_off[i] - back, dst);
   };

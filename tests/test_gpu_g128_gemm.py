@@ -145,8 +145,9 @@ def test_zero_is_stored_as_plus_zero():
 
 
 # ---- groups --------------------------------------------------------------------------------
-GROUPS = [[5], [0], [1, 0, 3], [0, 0, 130, 1, 0], [33, 64, 2, 17], [300, 1, 0, 257], [1] * 70, [0] * 40 + [9] + [0] * 90,
-          [1] * 20 + [700] + [0, 3] * 12, [64, 65, 63, 0, 66, 20, 31], [20] * 3 + [200], [0] * 1000 + [5] + [0] * 23]
+GROUPS = [[5], [0], [1, 0, 3], [0, 0, 130, 1, 0], [33, 64, 2, 17], [300, 1, 0, 257], [1] * 70,
+          [0] * 40 + [9] + [0] * 90, [1] * 20 + [700] + [0, 3] * 12,
+          [64, 65, 63, 0, 66, 20, 31], [20] * 3 + [200], [0] * 1000 + [5] + [0] * 23]
 
 
 @pytest.mark.parametrize("sizes", GROUPS, ids=lambda s: f"{len(s)}x{sum(s)}")

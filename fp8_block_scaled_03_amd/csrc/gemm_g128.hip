@@ -40,6 +40,16 @@ __device__ __forceinline__ v4f mfma_block(v8i_t w, v8i_t x) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, z, 0, 0, 0, 0, 0, 0);
 }
 
+// The lane's number, anew: what is computed from it is not kept, and spilled, from one
+// tile of a persistent workgroup to the next.  (Spilled row addresses put a memory
+// wait between the stores of the large tile: 8 ranges of 8192 rows, 4096 x 2048, 92 us,
+// 84 so; 2048 x 8192 x 512 19.5 and 16.5.)
+__device__ __forceinline__ int fresh_lane() {
+  int l = threadIdx.x & 63;
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
 // Two accumulators -> two bf16 (nearest even, NaN kept), a zero stored as +0.
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const v2f_t v = {lo + 0.0f, hi + 0.0f};
@@ -60,7 +70,7 @@ __device__ __forceinline__ uint4 bf16_octet(v4f x, v4f y) {
 template <int MI, int NJ>
 __device__ __forceinline__ void store_wave(uint16_t* c, int64_t N, const v4f (&acc)[MI][NJ], int r0, int c0,
                                            int m_valid, int n_valid) {
-  const int g = (threadIdx.x & 63) >> 4, lo = threadIdx.x & 15;
+  const int lane = fresh_lane(), g = lane >> 4, lo = lane & 15;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int r = r0 + 16 * i + lo;
@@ -386,9 +396,9 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
 
   // ---- direct loads of 8 rows each; lane l loads row l >> 3, 16-byte piece
   // (l & 7) ^ (row & 7).  Rows past the range read its last row.
-  auto row_off = [&](int row, int valid) __attribute__((always_inline)) -> uint32_t {
-    const int r = row + (lane >> 3);
-    return (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + ((lane & 7) ^ (lane >> 3)) * 16;
+  auto row_off = [&](int l, int row, int valid) __attribute__((always_inline)) -> uint32_t {
+    const int r = row + (l >> 3);
+    return (uint32_t)(r < valid ? r : valid - 1) * (uint32_t)K + ((l & 7) ^ (l >> 3)) * 16;
   };
   const int a_first = (w >> 2) * 128 + (w & 3) * 16;  // rows of sub-tiles 0-3; those of 4-7 lie 64 further
   // what the loads of the current tile need
@@ -403,10 +413,11 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     const int64_t col0 = (int64_t)t.tn * XBN;
     m_valid = (int)(t.row_end - t.row0 < XBM ? t.row_end - t.row0 : XBM);
     n_valid = (int)(N - col0 < XBN ? N - col0 : XBN);
+    const int l = fresh_lane();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      a_off[i] = row_off(a_first + (i >> 1) * 64 + (i & 1) * 8, m_valid);
-      b_off[i] = row_off((w * 4 + i) * 8, n_valid);
+      a_off[i] = row_off(l, a_first + (i >> 1) * 64 + (i & 1) * 8, m_valid);
+      b_off[i] = row_off(l, (w * 4 + i) * 8, n_valid);
     }
     a0 = uniform_ptr(a + t.row0 * K);
     b0 = uniform_ptr(bt + ((int64_t)t.group * N + col0) * K);
@@ -435,16 +446,16 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   };
   // Scales of eight rows x eight K-blocks, one per lane: part q (0..3) of this
   // wave's 32 rows of chunk `chunk`.
-  auto issue_s = [&](int chunk, int q) __attribute__((always_inline)) {
-    const int r = w * 32 + q * 8 + (lane & 7), kb = chunk * SCH + (lane >> 3);
+  auto issue_s = [&](int chunk, int q, int l) __attribute__((always_inline)) {
+    const int r = w * 32 + q * 8 + (l & 7), kb = chunk * SCH + (l >> 3);
     const uint32_t off = (uint32_t)(r < m_valid ? r : m_valid - 1) * (uint32_t)KB + (kb < KB ? kb : KB - 1);
     dma4_at(sa0, off * 4, lds0 + X_S + (chunk & 1) * X_SBUF + (w * 2 + (q >> 1)) * X_SSUB + (q & 1) * 288);
   };
   // Zeros behind K in the last K-block's slots, once its data are there for every wave.
   auto clear_tail = [&]() __attribute__((always_inline)) {
     const int first = (int)(K & 127) >> 4;  // first piece past K
-    const int r = threadIdx.x & 255;
-    lds_u8* const base = lds + (threadIdx.x < 256 ? X_A : X_B) + ((KB - 1) & 1) * X_SLOT + r * GK;
+    const int r = (w & 3) * 64 + fresh_lane();
+    lds_u8* const base = lds + (w < 4 ? X_A : X_B) + ((KB - 1) & 1) * X_SLOT + r * GK;
     for (int p = first; p < 8; ++p) *(lds_v4i_w*)(base + 16 * (p ^ (r & 7))) = v4i{0, 0, 0, 0};
   };
 
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   auto issue_mid = [&](int ks, int n, bool last) __attribute__((always_inline)) {
     const uint32_t back = last ? tail_back(ks + 2) : 0u;
     if (n == 0) {
-      if ((ks & 1) == 0) issue_s((ks >> 3) + 1, (ks & 7) >> 1);
+      if ((ks & 1) == 0) issue_s((ks >> 3) + 1, (ks & 7) >> 1, lane);
     } else if (n < 3) {
       issue_a(ks + 2, n - 1, back);
     } else {
@@ -515,8 +526,9 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
 #pragma unroll
       for (int n = 0; n < 4; ++n) issue_b(ks, n, back);
     };
+    const int l = fresh_lane();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) issue_s(0, q);
+    for (int q = 0; q < 4; ++q) issue_s(0, q, l);
     mid(0);
     issue_a(0, 2, tail_back(0));
     issue_a(0, 3, tail_back(0));

@@ -94,6 +94,45 @@ __device__ __forceinline__ void store_wave(uint16_t* c, int64_t N, const v4f (&a
   }
 }
 
+// 16 bytes, past the caches if LINES.
+template <bool LINES>
+__device__ __forceinline__ void put16(uint16_t* p, uint4 v) {
+  typedef unsigned v4u __attribute__((ext_vector_type(4)));
+  if constexpr (LINES) __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
+  else *reinterpret_cast<uint4*>(p) = v;
+}
+
+// 64 columns of a row from a multiple of 64 are one line of C.
+__device__ __forceinline__ bool whole_lines(const uint16_t* c, int64_t N) {
+  return N % 64 == 0 && (uintptr_t)c % 128 == 0;
+}
+
+// The same for NJ = 4, 128 bytes of a row of C per wave: lanes lo and lo ^ 8 exchange
+// half a row, so that a store covers eight whole rows' 128 bytes.  LINES: they are
+// lines of C and leave past the caches (8192 x 8192 x 1024 79 us, as 16 half rows
+// through the L2 87, whole rows through it 84; 8192 x 14336 x 2048 214, 229, 229;
+// with the 128x128 tile 8192 x 1024 x 1024 12.8 and 14.3).
+template <bool LINES, int MI>
+__device__ __forceinline__ void store_wave_rows(uint16_t* c, int64_t N, const v4f (&acc)[MI][4], int r0, int c0,
+                                                int m_valid, int n_valid) {
+  const int ln = fresh_lane(), g = ln >> 4, lo = ln & 15;
+  const bool low = lo < 8;
+  const int col = c0 + 16 * (g & 1) + 4 * (g & 2) + (low ? 0 : 32);
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const uint4 v0 = bf16_octet(acc[i][0], acc[i][1]), v1 = bf16_octet(acc[i][2], acc[i][3]);
+    auto ror8 = [](uint32_t x) __attribute__((always_inline)) -> uint32_t {
+      return __builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, true);
+    };
+    const uint4 got = make_uint4(ror8(low ? v1.x : v0.x), ror8(low ? v1.y : v0.y), ror8(low ? v1.z : v0.z),
+                                 ror8(low ? v1.w : v0.w));
+    const int r = r0 + 16 * i + (lo & 7);
+    const uint4 a = low ? v0 : got, b = low ? got : v1;
+    if (r < m_valid && col < n_valid) put16<LINES>(c + r * N + col, a);
+    if (r + 8 < m_valid && col < n_valid) put16<LINES>(c + (r + 8) * N + col, b);
+  }
+}
+
 // ---- small and middle tiles: BM = 16*MI*WM rows by BN = 16*NJ*WN columns per
 // workgroup of WM x WN waves; wave (wm, wn) owns MI x NJ sub-tiles of 16x16.
 //
@@ -331,7 +370,15 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     }
   }
 
-  if (wave_live) store_wave<MI, NJ>(c + row0 * N + col0, N, acc, wm * 16 * MI, wn * 16 * NJ, m_valid, n_valid);
+  if (!wave_live) return;
+  uint16_t* const ct = c + row0 * N + col0;
+  if constexpr (NJ == 4) {
+    if (whole_lines(c, N)) {
+      store_wave_rows<true>(ct, N, acc, wm * 16 * MI, wn * 16 * NJ, m_valid, n_valid);
+      return;
+    }
+  }
+  store_wave<MI, NJ>(ct, N, acc, wm * 16 * MI, wn * 16 * NJ, m_valid, n_valid);
 }
 
 // ---- the large tile: 256 x 256 per workgroup, eight waves of 128 x 64 (2 row bands by
@@ -384,6 +431,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   const int g = lane >> 4, lo = lane & 15;
 
   const int KB = (int)((K + 127) >> 7);
+  const bool lines = whole_lines(c, N);
   auto tile_at = [&](uint32_t id, TileAt& t) __attribute__((always_inline)) -> bool {
     if (id >= tiles) return false;
     if constexpr (GROUPED) return find_tile<XBM>(offsets, G, M, tiles_n, id, tiles, t);
@@ -656,7 +704,10 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     } else if (more) {
       begin_tile();
     }
-    if (wave_live) store_wave<8, 4>(ct, N, acc, wm * 128, wn * 64, m_here, n_here);
+    if (wave_live) {
+      if (lines) store_wave_rows<true>(ct, N, acc, wm * 128, wn * 64, m_here, n_here);
+      else store_wave_rows<false>(ct, N, acc, wm * 128, wn * 64, m_here, n_here);
+    }
     if (!more) return;
   }
 }

@@ -85,7 +85,8 @@ def test_swiglu_on_moved_tensors(rows, d):
         check()
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 272, 400), (50, 1040, 272), (700, 528, 400), (3500, 4112, 144)])
+@pytest.mark.parametrize("M,N,K", [(5, 272, 400), (50, 1040, 272), (700, 528, 400), (3500, 4112, 144),
+                                   (3500, 4160, 144)])
 def test_products_on_moved_tensors(M, N, K):
     say(f"moved products {M}x{N}x{K}")
     a, sa = code_bytes(5, M, K), scale_values(6, M, -(-K // 128))

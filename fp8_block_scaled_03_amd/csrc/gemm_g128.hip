@@ -901,29 +901,28 @@ hipError_t set_gemm_g128_attributes() {
 // and three K-blocks in the ring, one or two workgroups a CU; else four waves and
 // two to four; the last column is the whole call's overhead at 256 tiles, us):
 //              128   256   288   512   768   1024
-//   256x256   1040  1533        3039                12
-//   128x256 8w 840   971  1702  1924  2915  4333     7
-//   128x128 8w 561   581  1069  1192  1774  2413     5
-//   128x128    686   704   803   974  1640  1979     5
-//   64x128 8w  380   388   542   642   983  1287     4
-//   64x128     557   571   558   606   918  1367     3
-//   64x64      273   284   365   409   643   779     4
-//   32x64      221   236   285   296   434   566     3
-//   32x32      188   204   230   239   297   407     3
-// So 256x256 wants a full round or several (1536 x 7168 x 4096 [168 tiles] 50, 128x128
-// 59; 1225 x 13664 x 1200 [270] 49, 128x128 40), 64x128 with eight waves is better
-// than 32x64 from 129 of its tiles on (1540 x 832 x 7648 30 against 41).
-// One row tile of a wide weight is bound by the weight's stream, which needs bytes in
-// flight: the ring of 64x64 is four K-blocks deep (8 x 28672 x 8192: 46, 32x64 with
-// three 50; 64 x 28672 x 8192: 53, 55).  Up to 16 rows of a narrow weight: 16 x 4096
-// x 4096 rows 6.9, 32x32 [128] 8.5; 8 x 8192 x 8192 32x32 [256] 13.8, rows 16.6.
+//   256x256   1045  1506        3092                9
+//   128x256 8w 848  1024  1742  1977  2980  3825     5
+//   128x128 8w 554   591  1105  1258  1866  2390     4
+//   128x128    664   703   809   994  1655  1992     4
+//   64x128 8w  389   408   539   628  1001  1257     4
+//   64x128     556   572   560   611   965  1428     3
+//   64x64      262   295   365   427   635   777     4
+//   32x64      226   240   284   304   445   568     3
+//   32x32      189   206   230   237   313   410     3
+// (1536 x 7168 x 4096: 256x256 [168 tiles] 47 us, 128x128 59; 256 x 28672 x 8192:
+// 128x256 8w [224] 75, 128x128 [448] 87; 1540 x 832 x 7648: 64x128 8w [175] 30, 32x64
+// 41.)  One row tile of a wide weight is bound by the weight's stream, which needs
+// bytes in flight: the ring of 64x64 is four K-blocks deep (8 x 28672 x 8192: 45,
+// 32x64 with three 48).  Up to 16 rows of a narrow weight: 16 x 4096 x 4096 rows 6.9,
+// 32x32 [128] 8.5; 8 x 8192 x 8192 32x32 [256] 13.8, rows 16.6.
 // A range has half a tile too much on average, which the count includes, and a tile
 // is not chosen much taller than the ranges: rows past a range's end are work for
-// nothing (ranges x average rows, N x K: 64 x 8, 4096 x 2048: 32x64 94, 64x128 95;
-// 16 x 25, 4096 x 7168: 64x128 75, 128x128 82; 16 x 56: 128x256 8w 85, 64x128 95;
-// 16 x 125, 4096 x 2048: 64x128 34, 128x256 8w 40; 16 x 250, 2048 x 4096: 256x256
-// 56, 128x128 65).  Over 90 dense and 90 ragged sizes drawn from 17 to 8192 rows the
-// choice is 2.5% and 3% slower than the best tile of each on average.
+// nothing (ranges x average rows, N x K: 64 x 8, 4096 x 2048: 32x64 94, 64x128 94;
+// 16 x 25, 4096 x 7168: 64x128 74, 128x128 82; 16 x 56: 128x256 8w 84, 64x128 95;
+// 16 x 125, 4096 x 2048: 256x256 35, 128x256 8w 41, 64x128 44; 16 x 250, 2048 x 4096:
+// 256x256 55, 128x128 70).  Over 90 dense and 90 ragged sizes drawn from 17 to 8192
+// rows the choice is 1.5% and 3% slower than the best tile of each on average.
 hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t live = G < M ? G : M;           // ranges that can have rows
@@ -939,7 +938,7 @@ hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, cons
   }
   const int64_t big = tiles(256, 256), wide = tiles(128, 256), square = tiles(128, 128), low = tiles(64, 128);
   const int64_t small = tiles(64, 64);
-  if (avg >= 160 && big >= 160 && (big <= 256 || big >= 384))
+  if (avg >= (offsets ? 112 : 160) && big >= 160)
     return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
   if (avg >= (offsets ? 48 : 65) && wide >= 150 && wide <= 256)
     return launch_tile<4, 4, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);

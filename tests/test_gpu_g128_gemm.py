@@ -72,12 +72,14 @@ def test_rows_do_not_depend_on_m(N, K):
             assert torch.equal(part.view(torch.int16), full[first:first + M].view(torch.int16)), (M, first)
 
 
-# One size for each tile that the dispatch can take, with a ragged last tile both ways and a partial last K-block.
+# One size for each tile that the dispatch can take, with a ragged last tile both ways and a partial last K-block;
+# where waves have 64 columns, one with N a multiple of that as well.
 DENSE = [(9, 1040), (20, 2064), (40, 1040), (13, 8208), (30, 10256), (50, 16528), (100, 4112), (500, 3600),
          (1000, 2320), (1000, 4624), (1000, 9232), (400, 7184), (1700, 4112), (3500, 4112),
-         (3500, 4160)]
+         (1000, 2368), (1000, 9280), (400, 7232), (1700, 4160), (3500, 4160)]
 RANGED = [(7, 60, 1040), (7, 60, 3600), (5, 300, 1808), (5, 300, 4112), (5, 300, 5200), (3, 1000, 4368),
-          (3, 1000, 3472), (3, 1000, 7200), (4, 2000, 3600), (4, 8000, 1296), (4, 8000, 1344)]
+          (3, 1000, 3472), (3, 1000, 7200), (4, 2000, 3600), (4, 8000, 1296), (4, 8000, 1344),
+          (5, 300, 5248), (3, 1000, 7232)]
 
 
 @pytest.mark.parametrize("K", [400, 1168])

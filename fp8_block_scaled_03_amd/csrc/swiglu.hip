@@ -5,11 +5,14 @@
 //   du = dy g sigma
 // in fp32 from bf16 inputs; the codes are taken from the fp32 values.  With
 // e = exp(-|g|) <= 1 the two sigmoids sigma(|g|) = 1 / (1 + e) and sigma(-|g|) =
-// e / (1 + e) never overflow and 1 - sigma loses nothing.  The hardware's exp2
-// sees a rounded exponent and the rest enters as a first-order factor; the
-// reciprocal is the hardware's with one Newton step.  Both are within about
-// 1.5 ulp, the order of the rounding of the products around them: an error there
-// moves the scale of a whole group and the codes next to a border.
+// e / (1 + e) never overflow and 1 - sigma loses nothing.  The exponent is split
+// into a whole number and a rest of at most 1/2, whose exp2 the hardware takes (a
+// rest taken from the rounded exponent costs a far gate more bits the farther it
+// lies: 46 x 2^-24 at -60); the reciprocal is the hardware's with one Newton step.
+// With one ulp for exp2 sigma(-|g|) is within 2.9 ulp for every gate (where its fp32
+// value is not subnormal), and y / 448 was within 3.9 x 2^-24 for every bf16 gate
+// of [2^-7, 80] and either sign: an error there moves the scale of a whole group
+// and the codes next to a border.
 //
 // Bound by HBM traffic: 5 bytes per value forward, 12 backward (14 with y).
 // Mapping as in quantize_g128.hip: 16 lanes hold a group's 128 columns of one
@@ -26,13 +29,15 @@ struct Sigmoid {
 __device__ __forceinline__ Sigmoid sigmoid(float g) {
   constexpr float L_HI = 1.44269502162933349609375f;   // log2(e) rounded to fp32
   constexpr float L_LO = 1.92596299112661746887e-8f;   // the rest
+  constexpr float ROUND = 0x1.8p23f;                   // adding it rounds to a whole number, which the low bits hold
   const float a = fminf(__builtin_fabsf(g), 128.0f);   // exp(-128) is below every fp32 value
-  // 2^24 e = 2^(24 - a log2(e)): the hardware's exp2 flushes subnormal results,
-  // which the factor keeps away
-  const float d = __builtin_fmaf(-a, L_HI, 24.0f);
-  const float rest = __builtin_fmaf(-a, L_LO, __builtin_fmaf(-a, L_HI, 24.0f - d));  // 24 - a log2(e) - d
-  float e = __builtin_amdgcn_exp2f(d);
-  e = __builtin_fmaf(e * 0.693147180559945f, rest, e);
+  const float t = __builtin_fmaf(a, L_HI, ROUND);
+  const float n = t - ROUND;
+  // n - a log2(e): the first product and sum lose nothing of a far gate
+  const float rest = __builtin_fmaf(-a, L_LO, __builtin_fmaf(-a, L_HI, n));
+  // 2^24 e, the factor so that a subnormal e keeps its bits until sigma is rounded
+  const int up = 24 + __builtin_bit_cast(int, ROUND) - __builtin_bit_cast(int, t);
+  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), up);
   const float b = __builtin_fmaf(e, 0x1p-24f, 1.0f);  // in [1, 2]
   const float r = __builtin_amdgcn_rcpf(b);
   const float large = __builtin_fmaf(__builtin_fmaf(-b, r, 1.0f), r, r);

@@ -7,9 +7,16 @@
 // instruction with the full FP8 rate (its 32-deep relatives run at half of
 // it), so P is one MFMA with a zero accumulator and the promotion is four fp32
 // fmas per lane and 16x16x128 products: 16 VALU cycles beside 32 matrix
-// cycles.  The instruction cuts small products (2^-13 below the largest of
-// their group of eight); the cut is below the bf16 rounding of C and is not
-// carried along K, because the sum over K-blocks is the fp32 accumulator's.
+// cycles.
+//
+// Precision: the instruction cuts each product toward zero to 2^-13 of the largest
+// exponent sum of its group of eight K, before it sums in fp32 (the header states
+// the bound).  That is the price of the rate: the exact bf16 MFMA of the 32-value
+// forms has half of it.  The cut is relative to the products and not to
+// C: on quantized normal rows with a few strong channels (64 x 128 x 1024) it is
+// 2.6e-5 of C, rms, and it exceeds half a bf16 step of C in 0.5% of the elements, by
+// up to 200 times, where products cancel.  It is not carried along K, because the
+// sum over K-blocks is the fp32 accumulator's.
 //
 // Every kernel here runs the same sequence per element - the same MFMA operands,
 // s = RN(sa * sb), acc = fma(P, s, acc), kb ascending - so a row's result does
@@ -387,9 +394,10 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
 // In a wave every MFMA of row sub-tile i is preceded by the four promotion fmas of
 // the product that the same column sub-tile had for row sub-tile i - 1, so the
 // fmas run under the matrix pipe and no product is waited for (a register-only
-// loop in this order reaches 4.84 PFLOP/s, the MFMAs alone 4.92).  Fragments of
-// row sub-tile i + 1 are read from LDS one sub-tile ahead; the weight fragments of
-// the next step replace the current ones as the last row sub-tile's MFMAs issue.
+// loop in this order reaches 4.84 PFLOP/s on constants, the MFMAs alone 4.92; 4.1 to
+// 4.3 on random data, whose power lowers the clock).  Fragments of row sub-tile
+// i + 1 are read from LDS one sub-tile ahead; the weight fragments of the next step
+// replace the current ones as the last row sub-tile's MFMAs issue.
 //
 // A step's data arrive in three parts with two barriers per step:
 //   middle (before row sub-tile 3): rows of sub-tiles 0-3 of A's slot and the
@@ -922,7 +930,9 @@ hipError_t set_gemm_g128_attributes() {
 // 16 x 25, 4096 x 7168: 64x128 74, 128x128 82; 16 x 56: 128x256 8w 84, 64x128 95;
 // 16 x 125, 4096 x 2048: 256x256 35, 128x256 8w 41, 64x128 44; 16 x 250, 2048 x 4096:
 // 256x256 55, 128x128 70).  Over 90 dense and 90 ragged sizes drawn from 17 to 8192
-// rows the choice is 1.5% and 3% slower than the best tile of each on average.
+// rows the choice is 1.5% and 3% slower than the best of these tiles on average; what
+// none of them reaches this does not see (32 x 576 x 7168 is 18 workgroups of 56
+// K-blocks one after another: 13.7 us).
 hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
   const int64_t live = G < M ? G : M;           // ranges that can have rows

@@ -14,7 +14,8 @@ _BINDING_NAMES = ("Fp8bsError", "quantize", "gemm", "grouped_gemm", "gemm_nt", "
                   "quantize_tg128", "quantize_b128", "gemm_tg128_nt", "grouped_gemm_tg128_nt", "grouped_wgrad",
                   "swiglu_quantize_tg128", "swiglu_backward_quantize_tg128", "quantize_tg128_raw",
                   "quantize_b128_raw", "gemm_tg128_nt_raw", "grouped_gemm_tg128_nt_raw", "grouped_wgrad_raw",
-                  "swiglu_quantize_tg128_raw", "swiglu_backward_quantize_tg128_raw")
+                  "swiglu_quantize_tg128_raw", "swiglu_backward_quantize_tg128_raw",
+                  "grad_norm", "clip_grads", "clip_grad_norm", "grad_norm_raw", "clip_grads_raw", "clip_grad_norm_raw")
 
 __all__ = list(_BINDING_NAMES)
 

@@ -2,12 +2,13 @@
 
 Every function here checks torch dtypes, shapes, contiguity and devices, then
 passes raw device pointers and the current HIP stream to the C ABI declared in
-include/fp8bs.h and include/fp8bs_g128.h.  No arithmetic of the method happens in Python; if the library
-is missing the call raises ``Fp8bsError`` - there is no fallback path.
+include/fp8bs.h, include/fp8bs_g128.h and include/fp8bs_layer.h.  No arithmetic of the method happens in Python; if
+the library is missing the call raises ``Fp8bsError`` - there is no fallback path.
 """
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -79,6 +80,15 @@ def load_library() -> ctypes.CDLL:
         lib.fp8bs_swiglu_quantize_tg128.restype = ctypes.c_int
         lib.fp8bs_swiglu_backward_quantize_tg128.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
         lib.fp8bs_swiglu_backward_quantize_tg128.restype = ctypes.c_int
+        f64 = ctypes.c_double
+        lib.fp8bs_grad_norm_workspace.argtypes = [i32]
+        lib.fp8bs_grad_norm_workspace.restype = i64
+        lib.fp8bs_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp]
+        lib.fp8bs_grad_norm.restype = ctypes.c_int
+        lib.fp8bs_clip_grads.argtypes = [vp, vp, vp, vp, i32, vp, f64, f64, vp]
+        lib.fp8bs_clip_grads.restype = ctypes.c_int
+        lib.fp8bs_clip_grad_norm.argtypes = [vp, vp, vp, vp, i32, f64, f64, vp, vp, i64, vp]
+        lib.fp8bs_clip_grad_norm.restype = ctypes.c_int
         lib.fp8bs_status_str.argtypes = [ctypes.c_int]
         lib.fp8bs_status_str.restype = ctypes.c_char_p
         _lib = lib
@@ -194,6 +204,19 @@ def swiglu_quantize_tg128_raw(gu_ptr, rows, d, q_ptr, s_ptr, y_ptr, stream=None)
 def swiglu_backward_quantize_tg128_raw(gu_ptr, dy_ptr, rows, d, dgu_ptr, q_ptr, s_ptr, y_ptr, stream=None) -> int:
     return load_library().fp8bs_swiglu_backward_quantize_tg128(gu_ptr, dy_ptr, rows, d, dgu_ptr, q_ptr, s_ptr, y_ptr,
                                                                stream)
+
+
+def grad_norm_raw(grads, counts, types, n, norm_ptr, ws_ptr, ws_bytes, stream=None) -> int:
+    return load_library().fp8bs_grad_norm(grads, counts, types, n, norm_ptr, ws_ptr, ws_bytes, stream)
+
+
+def clip_grads_raw(grads, outs, counts, types, n, norm_ptr, max_norm, eps, stream=None) -> int:
+    return load_library().fp8bs_clip_grads(grads, outs, counts, types, n, norm_ptr, max_norm, eps, stream)
+
+
+def clip_grad_norm_raw(grads, outs, counts, types, n, max_norm, eps, norm_ptr, ws_ptr, ws_bytes, stream=None) -> int:
+    return load_library().fp8bs_clip_grad_norm(grads, outs, counts, types, n, max_norm, eps, norm_ptr, ws_ptr,
+                                               ws_bytes, stream)
 
 
 # ---- tensor entry points -----------------------------------------------------------------
@@ -626,3 +649,95 @@ def swiglu_backward_quantize_tg128(gu: torch.Tensor, dy: torch.Tensor, dgu: torc
     _call_on(dev, "fp8bs_swiglu_backward_quantize_tg128", gu.data_ptr(), dy.data_ptr(), R, d, dgu.data_ptr(),
              q.data_ptr(), scales.data_ptr(), _ptr(y))
     return (dgu, q, scales) if y is None else (dgu, q, scales, y)
+
+
+# ---- between the products of a block (include/fp8bs_layer.h) ----------------------------------
+_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _addresses(values, code: str):
+    """A host array of whole numbers (kept alive by the caller) and its address."""
+    a = array.array(code, values)
+    return a, a.buffer_info()[0]
+
+
+def _scalar(t: torch.Tensor | None, name: str, device: torch.device) -> torch.Tensor:
+    """The caller's fp32 tensor without dimensions, checked, or a new one."""
+    return torch.empty((), dtype=torch.float32, device=device) if t is None else _need_like(t, name, _F32, (), device)
+
+
+def _workspace(size: int, device: torch.device) -> torch.Tensor:
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _gradients(grads, name: str):
+    """The tensors of a sequence, checked: (list, counts, type codes, device)."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError(f"{name} is empty")
+    for g in grads:
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"{name} must hold tensors")
+        if g.dtype not in _GRAD_TYPES:
+            raise TypeError(f"{name}: dtype {g.dtype} not accepted ({tuple(_GRAD_TYPES)})")
+        if not g.is_cuda:
+            raise ValueError(f"{name} must be on a GPU")
+        if not g.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    device = grads[0].device
+    if any(g.device != device for g in grads):
+        raise ValueError("all tensors must be on the same device")
+    return grads, [g.numel() for g in grads], [_GRAD_TYPES[g.dtype] for g in grads], device
+
+
+def _clip_outputs(grads, counts, types, device, out):
+    if out is None:
+        return grads
+    out, out_counts, out_types, out_device = _gradients(out, "out")
+    if out_counts != counts or out_types != types or out_device != device:
+        raise ValueError("out must match the gradients in number, types, sizes and device")
+    return out
+
+
+def grad_norm(grads, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The norm over all values of a sequence of contiguous fp32 and bf16 tensors: sqrt(sum of squares), summed
+    in 64 bits, as an fp32 tensor without dimensions (on the device; nothing is copied to the host)."""
+    grads, counts, types, dev = _gradients(grads, "grads")
+    out = _scalar(out, "out", dev)
+    n, lib = len(grads), _lib or load_library()
+    size = lib.fp8bs_grad_norm_workspace(n)
+    ws = _workspace(size, dev)
+    (keep_g, g), (keep_c, c), (keep_t, t) = (_addresses([x.data_ptr() for x in grads], "Q"), _addresses(counts, "q"),
+                                             _addresses(types, "i"))
+    _call_on(dev, "fp8bs_grad_norm", g, c, t, n, out.data_ptr(), ws.data_ptr(), size)
+    return out
+
+
+def clip_grads(grads, norm: torch.Tensor, max_norm: float, out=None, eps: float = 1e-6) -> None:
+    """Scales the gradients by min(1, max_norm / (norm + eps)) for an fp32 ``norm`` on the device, in place, or into
+    the tensors ``out`` (each of its gradient's type and shape; a gradient itself, or memory of its own)."""
+    grads, counts, types, dev = _gradients(grads, "grads")
+    outs = _clip_outputs(grads, counts, types, dev, out)
+    _need_like(norm, "norm", _F32, (), dev)
+    (keep_g, g), (keep_o, o) = (_addresses([x.data_ptr() for x in grads], "Q"),
+                                _addresses([x.data_ptr() for x in outs], "Q"))
+    (keep_c, c), (keep_t, t) = _addresses(counts, "q"), _addresses(types, "i")
+    _call_on(dev, "fp8bs_clip_grads", g, o, c, t, len(grads), norm.data_ptr(), float(max_norm), float(eps))
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, eps: float = 1e-6,
+                   norm: torch.Tensor | None = None) -> torch.Tensor:
+    """The norm over all gradients (as by grad_norm), which is returned, and their scaling by
+    min(1, max_norm / (norm + eps)), in place or into ``out`` (as by clip_grads)."""
+    grads, counts, types, dev = _gradients(grads, "grads")
+    outs = _clip_outputs(grads, counts, types, dev, out)
+    norm = _scalar(norm, "norm", dev)
+    n, lib = len(grads), _lib or load_library()
+    size = lib.fp8bs_grad_norm_workspace(n)
+    ws = _workspace(size, dev)
+    (keep_g, g), (keep_o, o) = (_addresses([x.data_ptr() for x in grads], "Q"),
+                                _addresses([x.data_ptr() for x in outs], "Q"))
+    (keep_c, c), (keep_t, t) = _addresses(counts, "q"), _addresses(types, "i")
+    _call_on(dev, "fp8bs_clip_grad_norm", g, o, c, t, n, float(max_norm), float(eps), norm.data_ptr(), ws.data_ptr(),
+             size)
+    return norm

@@ -1,0 +1,121 @@
+// C ABI of the operators between the products (see include/fp8bs_layer.h).
+// Host-side argument checks, then the launches on the caller's stream.
+#include "fp8bs_layer.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "launch_layer.hpp"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// hipErrorNotSupported from a launcher: the grid would be too large
+fp8bs_status from_launch(hipError_t e) {
+  if (e == hipErrorNotSupported) return FP8BS_ESHAPE;
+  return e == hipSuccess ? FP8BS_OK : FP8BS_EHIP;
+}
+
+constexpr int64_t MAX_COUNT = int64_t(1) << 36;  // a launch's chunks of 32 KB stay below 2^31
+
+fp8bs_status check_grads(const void* const* grads, void* const* outs, bool clips, const int64_t* counts,
+                         const int32_t* types, int32_t n) {
+  if (n < 0 || n > FP8BS_MAX_TENSORS) return FP8BS_EINVAL;
+  if (n > 0 && (!grads || !counts || !types || (clips && !outs))) return FP8BS_EINVAL;
+  for (int32_t i = 0; i < n; ++i) {
+    if (counts[i] < 0 || (types[i] != FP8BS_F32 && types[i] != FP8BS_BF16)) return FP8BS_EINVAL;
+    if (counts[i] > MAX_COUNT) return FP8BS_ESHAPE;
+    if (counts[i] == 0) continue;
+    if (!grads[i] || (clips && !outs[i])) return FP8BS_EINVAL;
+    const uintptr_t size = types[i] == FP8BS_F32 ? 4 : 2;
+    if (!aligned(grads[i], size) || (clips && !aligned(outs[i], size))) return FP8BS_EALIGN;
+  }
+  return FP8BS_OK;
+}
+
+// Does a tensor that is written overlap another one?  (outs[i] == grads[i] is one tensor.)
+bool overlapping(const void* const* grads, void* const* outs, const int64_t* counts, const int32_t* types,
+                 int32_t n) {
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * (size_t)n);
+  for (int32_t i = 0; i < n; ++i) {
+    if (counts[i] == 0) continue;
+    const uintptr_t bytes = (uintptr_t)counts[i] * (types[i] == FP8BS_F32 ? 4 : 2);
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
+    spans.push_back({o, o + bytes, true});
+    if (g != o) spans.push_back({g, g + bytes, false});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, written = 0;  // the furthest ends so far
+  for (const Span& s : spans) {
+    if (s.begin < written || (s.written && s.begin < any)) return true;
+    any = std::max(any, s.end);
+    if (s.written) written = std::max(written, s.end);
+  }
+  return false;
+}
+
+fp8bs_status check_clip(const void* const* grads, void* const* outs, const int64_t* counts, const int32_t* types,
+                        int32_t n, double max_norm, double eps, const float* norm) {
+  const fp8bs_status st = check_grads(grads, outs, true, counts, types, n);
+  if (st != FP8BS_OK) return st;
+  if (!(max_norm >= 0) || !(eps >= 0) || std::isinf(max_norm) || std::isinf(eps) || !norm) return FP8BS_EINVAL;
+  if (!aligned(norm, 4)) return FP8BS_EALIGN;
+  try {
+    if (overlapping(grads, outs, counts, types, n)) return FP8BS_EINVAL;
+  } catch (...) {  // no host memory
+    return FP8BS_EHIP;
+  }
+  return FP8BS_OK;
+}
+
+fp8bs_status check_workspace(const void* workspace, int64_t have, int64_t need) {
+  if (!workspace || have < need) return FP8BS_EINVAL;
+  return aligned(workspace, 16) ? FP8BS_OK : FP8BS_EALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8bs_grad_norm_workspace(int32_t n) { return fp8bs::grad_norm_workspace(n > 0 ? n : 0); }
+
+fp8bs_status fp8bs_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* types, int32_t n,
+                             float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  fp8bs_status st = check_grads(grads, nullptr, false, counts, types, n);
+  if (st == FP8BS_OK && !norm) st = FP8BS_EINVAL;
+  if (st == FP8BS_OK && !aligned(norm, 4)) st = FP8BS_EALIGN;
+  if (st == FP8BS_OK) st = check_workspace(workspace, workspace_bytes, fp8bs_grad_norm_workspace(n));
+  if (st != FP8BS_OK) return st;
+  return from_launch(fp8bs::launch_grad_norm({grads, nullptr, counts, types, n}, norm, (double*)workspace,
+                                             (hipStream_t)stream));
+}
+
+fp8bs_status fp8bs_clip_grads(const void* const* grads, void* const* outs, const int64_t* counts,
+                              const int32_t* types, int32_t n, const float* norm, double max_norm, double eps,
+                              void* stream) {
+  const fp8bs_status st = check_clip(grads, outs, counts, types, n, max_norm, eps, norm);
+  if (st != FP8BS_OK) return st;
+  return from_launch(fp8bs::launch_clip_grads({grads, outs, counts, types, n}, max_norm, eps,
+                                              const_cast<float*>(norm), nullptr, (hipStream_t)stream));
+}
+
+fp8bs_status fp8bs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts,
+                                  const int32_t* types, int32_t n, double max_norm, double eps, float* norm,
+                                  void* workspace, int64_t workspace_bytes, void* stream) {
+  fp8bs_status st = check_clip(grads, outs, counts, types, n, max_norm, eps, norm);
+  if (st == FP8BS_OK) st = check_workspace(workspace, workspace_bytes, fp8bs_grad_norm_workspace(n));
+  if (st != FP8BS_OK) return st;
+  return from_launch(fp8bs::launch_clip_grads({grads, outs, counts, types, n}, max_norm, eps, norm,
+                                              (double*)workspace, (hipStream_t)stream));
+}
+
+}  // extern "C"

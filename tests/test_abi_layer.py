@@ -1,0 +1,94 @@
+"""The entry points of include/fp8bs_layer.h are exported and refuse bad arguments on the host before any launch
+(CPU only: no GPU call is made)."""
+
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import fp8_block_scaled_03_amd as fp8bs
+from fp8_block_scaled_03_amd import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, EINVAL, ESHAPE, EALIGN = 0, 1, 2, 3
+A16 = 0x10000          # fake, 16-byte aligned "device" addresses: never dereferenced
+A4 = 0x10004
+BIG = 1 << 30
+
+
+def test_library_exports_every_declared_symbol():
+    lib = binding.load_library()
+    text = open(os.path.join(ROOT, "include", "fp8bs_layer.h")).read()
+    names = set(re.findall(r"^(?:fp8bs_status|int64_t) (fp8bs_[a-z0-9_]+)\(", text, re.M))
+    assert "fp8bs_clip_grad_norm" in names
+    for n in names:
+        assert hasattr(lib, n), n
+        if not n.endswith("_workspace"):
+            assert hasattr(fp8bs, n[len("fp8bs_"):]), n
+
+
+# ---- gradients ---------------------------------------------------------------------------
+def _arrays(pointers, counts, types):
+    n = len(pointers)
+    return (ctypes.c_void_p * n)(*pointers), (ctypes.c_int64 * n)(*counts), (ctypes.c_int32 * n)(*types)
+
+
+def _norm(pointers, counts, types, norm=A4, ws=A16, size=None, n=None):
+    p, c, t = _arrays(pointers, counts, types)
+    n = len(pointers) if n is None else n
+    size = binding.load_library().fp8bs_grad_norm_workspace(n) if size is None else size
+    return binding.grad_norm_raw(p, c, t, n, norm, ws, size)
+
+
+def _clip(pointers, outs, counts, types, max_norm=1.0, eps=1e-6, norm=A4, ws=A16, size=1 << 20):
+    p, c, t = _arrays(pointers, counts, types)
+    o = (ctypes.c_void_p * len(outs))(*outs)
+    both = binding.clip_grad_norm_raw(p, o, c, t, len(pointers), max_norm, eps, norm, ws, size)
+    if ws == A16 and size == 1 << 20:
+        assert binding.clip_grads_raw(p, o, c, t, len(pointers), norm, max_norm, eps) == both
+    return both
+
+
+def test_grad_norm_refusals():
+    assert _norm([A16], [4], [0], n=-1) == EINVAL and _norm([A16], [4], [0], n=65537) == EINVAL
+    assert _norm([A16], [-1], [0]) == EINVAL and _norm([A16], [4], [2]) == EINVAL and _norm([A16], [4], [-1]) == EINVAL
+    assert _norm([None], [4], [0]) == EINVAL and _norm([A16], [4], [0], norm=None) == EINVAL
+    assert _norm([A16], [4], [0], ws=None) == EINVAL and _norm([A16], [4], [0], size=64) == EINVAL
+    assert _norm([A16 + 2], [4], [0]) == EALIGN and _norm([A16 + 1], [4], [1]) == EALIGN
+    assert _norm([A16], [4], [0], norm=A4 + 2) == EALIGN and _norm([A16], [4], [0], ws=A16 + 8) == EALIGN
+    assert _norm([A16], [(1 << 36) + 1], [0]) == ESHAPE
+    lib = binding.load_library()
+    assert lib.fp8bs_grad_norm(None, None, None, 1, A4, A16, 1 << 20, None) == EINVAL
+    assert lib.fp8bs_grad_norm_workspace(1) <= lib.fp8bs_grad_norm_workspace(1000)
+
+
+def test_clip_refusals():
+    far = A16 + (1 << 20)
+    for bad in (-1.0, float("nan"), float("inf")):
+        assert _clip([A16], [A16], [4], [0], max_norm=bad) == EINVAL
+        assert _clip([A16], [A16], [4], [0], eps=bad) == EINVAL
+    assert _clip([A16], [None], [4], [0]) == EINVAL and _clip([A16], [far + 2], [4], [0]) == EALIGN
+    assert _clip([A16], [A16], [4], [0], norm=None) == EINVAL
+    assert _clip([A16], [A16], [4], [0], ws=None) == EINVAL and _clip([A16], [A16], [4], [0], size=8) == EINVAL
+    # the same tensor twice, tensors that overlap, outputs over another gradient or over each other
+    assert _clip([A16, A16], [A16, A16], [4, 4], [0, 0]) == EINVAL
+    assert _clip([A16, A16 + 8], [A16, A16 + 8], [4, 4], [0, 0]) == EINVAL
+    assert _clip([A16 + 8, A16], [A16 + 8, A16], [4, 4], [0, 1 - 1]) == EINVAL
+    assert _clip([A16], [A16 + 4], [4], [0]) == EINVAL
+    assert _clip([A16, far], [far, far + 64], [4, 4], [0, 0]) == EINVAL
+    assert _clip([A16, A16 + 16], [far, far + 8], [4, 4], [0, 0]) == EINVAL
+
+
+def test_gradient_lists_are_checked_without_gpu():
+    x = torch.zeros(4, 32)
+    for call in (fp8bs.grad_norm, lambda g: fp8bs.clip_grad_norm(g, 1.0)):
+        with pytest.raises(ValueError):
+            call([])
+        with pytest.raises(ValueError):
+            call([x])                       # not on a GPU
+        with pytest.raises(TypeError):
+            call([x.half()])
+        with pytest.raises(TypeError):
+            call([1.0])

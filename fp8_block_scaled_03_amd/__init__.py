@@ -15,6 +15,8 @@ _BINDING_NAMES = ("Fp8bsError", "quantize", "gemm", "grouped_gemm", "gemm_nt", "
                   "swiglu_quantize_tg128", "swiglu_backward_quantize_tg128", "quantize_tg128_raw",
                   "quantize_b128_raw", "gemm_tg128_nt_raw", "grouped_gemm_tg128_nt_raw", "grouped_wgrad_raw",
                   "swiglu_quantize_tg128_raw", "swiglu_backward_quantize_tg128_raw",
+                  "layernorm_quantize_tg128", "layernorm", "layernorm_backward", "layernorm_quantize_tg128_raw",
+                  "layernorm_raw", "layernorm_backward_raw",
                   "grad_norm", "clip_grads", "clip_grad_norm", "grad_norm_raw", "clip_grads_raw", "clip_grad_norm_raw")
 
 __all__ = list(_BINDING_NAMES)

@@ -80,7 +80,15 @@ def load_library() -> ctypes.CDLL:
         lib.fp8bs_swiglu_quantize_tg128.restype = ctypes.c_int
         lib.fp8bs_swiglu_backward_quantize_tg128.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp, vp]
         lib.fp8bs_swiglu_backward_quantize_tg128.restype = ctypes.c_int
-        f64 = ctypes.c_double
+        f32, f64 = ctypes.c_float, ctypes.c_double
+        lib.fp8bs_layernorm_quantize_tg128.argtypes = [vp, vp, vp, vp, f32, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+        lib.fp8bs_layernorm_quantize_tg128.restype = ctypes.c_int
+        lib.fp8bs_layernorm.argtypes = [vp, vp, vp, vp, f32, i64, i64, vp, vp, vp, vp, vp]
+        lib.fp8bs_layernorm.restype = ctypes.c_int
+        lib.fp8bs_layernorm_backward_workspace.argtypes = [i64, i64]
+        lib.fp8bs_layernorm_backward_workspace.restype = i64
+        lib.fp8bs_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, vp, i64, vp]
+        lib.fp8bs_layernorm_backward.restype = ctypes.c_int
         lib.fp8bs_grad_norm_workspace.argtypes = [i32]
         lib.fp8bs_grad_norm_workspace.restype = i64
         lib.fp8bs_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp]
@@ -204,6 +212,24 @@ def swiglu_quantize_tg128_raw(gu_ptr, rows, d, q_ptr, s_ptr, y_ptr, stream=None)
 def swiglu_backward_quantize_tg128_raw(gu_ptr, dy_ptr, rows, d, dgu_ptr, q_ptr, s_ptr, y_ptr, stream=None) -> int:
     return load_library().fp8bs_swiglu_backward_quantize_tg128(gu_ptr, dy_ptr, rows, d, dgu_ptr, q_ptr, s_ptr, y_ptr,
                                                                stream)
+
+
+def layernorm_quantize_tg128_raw(x_ptr, res_ptr, gamma_ptr, beta_ptr, eps, rows, d, h_ptr, q_ptr, s_ptr, y_ptr,
+                                 mean_ptr, rstd_ptr, stream=None) -> int:
+    return load_library().fp8bs_layernorm_quantize_tg128(x_ptr, res_ptr, gamma_ptr, beta_ptr, eps, rows, d, h_ptr,
+                                                         q_ptr, s_ptr, y_ptr, mean_ptr, rstd_ptr, stream)
+
+
+def layernorm_raw(x_ptr, res_ptr, gamma_ptr, beta_ptr, eps, rows, d, h_ptr, y_ptr, mean_ptr, rstd_ptr,
+                  stream=None) -> int:
+    return load_library().fp8bs_layernorm(x_ptr, res_ptr, gamma_ptr, beta_ptr, eps, rows, d, h_ptr, y_ptr, mean_ptr,
+                                          rstd_ptr, stream)
+
+
+def layernorm_backward_raw(dy_ptr, h_ptr, gamma_ptr, mean_ptr, rstd_ptr, dres_ptr, rows, d, dx_ptr, dgamma_ptr,
+                           dbeta_ptr, accumulate, ws_ptr, ws_bytes, stream=None) -> int:
+    return load_library().fp8bs_layernorm_backward(dy_ptr, h_ptr, gamma_ptr, mean_ptr, rstd_ptr, dres_ptr, rows, d,
+                                                   dx_ptr, dgamma_ptr, dbeta_ptr, accumulate, ws_ptr, ws_bytes, stream)
 
 
 def grad_norm_raw(grads, counts, types, n, norm_ptr, ws_ptr, ws_bytes, stream=None) -> int:
@@ -652,6 +678,90 @@ def swiglu_backward_quantize_tg128(gu: torch.Tensor, dy: torch.Tensor, dgu: torc
 
 
 # ---- between the products of a block (include/fp8bs_layer.h) ----------------------------------
+def _norm_inputs(x, gamma, beta, residual, h, mean, rstd, want_stats):
+    """The arguments that both forms of the layer norm have, checked, and the outputs that are not given:
+    (rows, columns, device, h, mean, rstd)."""
+    _need(x, "x", _BF16, 2)
+    R, d = x.shape
+    dev = x.device
+    _need_like(gamma, "gamma", _BF16, (d,), dev)
+    if beta is not None:
+        _need_like(beta, "beta", _BF16, (d,), dev)
+    if residual is not None:
+        _need_like(residual, "residual", _BF16, (R, d), dev)
+        h = residual if h is None else _need_like(h, "h", _BF16, (R, d), dev)
+    elif h is not None:
+        raise ValueError("h needs residual")
+    if (mean is None) != (rstd is None):
+        raise ValueError("mean and rstd go together")
+    if want_stats or mean is not None:
+        mean, rstd = _output(mean, "mean", _F32, (R,), dev), _output(rstd, "rstd", _F32, (R,), dev)
+    return R, d, dev, h, mean, rstd
+
+
+def layernorm_quantize_tg128(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor | None, eps: float,
+                             residual: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                             q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                             y: torch.Tensor | None = None, mean: torch.Tensor | None = None,
+                             rstd: torch.Tensor | None = None, want_y: bool = False, want_stats: bool = False):
+    """Residual add + layer norm of bf16 x [R, d] with weight gamma [d] and bias beta [d] (or None), quantized as
+    by quantize_tg128 from its fp32 values: (q uint8 [R, d], scales fp32 [R, ceil(d/128)]).
+
+    With ``residual`` the rows are h = x + residual, written to ``h``, or in place to ``residual`` if ``h`` is not
+    given.  When ``want_y`` is true or ``y`` is given the bf16 rows follow, when ``want_stats`` is true or ``mean``
+    and ``rstd`` are given the fp32 statistics [R] that layernorm_backward takes: (q, scales[, y][, mean, rstd])."""
+    R, d, dev, h, mean, rstd = _norm_inputs(x, gamma, beta, residual, h, mean, rstd, want_stats)
+    q = _output(q, "q", E4M3_DTYPES, (R, d), dev)
+    scales = _output(scales, "scales", _F32, (R, _blocks128(d)), dev)
+    if y is not None or want_y:
+        y = _output(y, "y", _BF16, (R, d), dev)
+    _call_on(dev, "fp8bs_layernorm_quantize_tg128", x.data_ptr(), _ptr(residual), gamma.data_ptr(), _ptr(beta),
+             float(eps), R, d, _ptr(h), q.data_ptr(), scales.data_ptr(), _ptr(y), _ptr(mean), _ptr(rstd))
+    return (q, scales) + (() if y is None else (y,)) + (() if mean is None else (mean, rstd))
+
+
+def layernorm(x: torch.Tensor, gamma: torch.Tensor, beta: torch.Tensor | None, eps: float,
+              residual: torch.Tensor | None = None, h: torch.Tensor | None = None, y: torch.Tensor | None = None,
+              mean: torch.Tensor | None = None, rstd: torch.Tensor | None = None, want_stats: bool = False):
+    """As layernorm_quantize_tg128 without codes: y bf16 [R, d], or (y, mean, rstd) when ``want_stats`` is true or
+    ``mean`` and ``rstd`` are given."""
+    R, d, dev, h, mean, rstd = _norm_inputs(x, gamma, beta, residual, h, mean, rstd, want_stats)
+    y = _output(y, "y", _BF16, (R, d), dev)
+    _call_on(dev, "fp8bs_layernorm", x.data_ptr(), _ptr(residual), gamma.data_ptr(), _ptr(beta), float(eps), R, d,
+             _ptr(h), y.data_ptr(), _ptr(mean), _ptr(rstd))
+    return y if mean is None else (y, mean, rstd)
+
+
+def layernorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, mean: torch.Tensor,
+                       rstd: torch.Tensor, dresidual: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                       dgamma: torch.Tensor | None = None, dbeta: torch.Tensor | None = None,
+                       accumulate: bool = False):
+    """The gradients of the layer norm of the bf16 rows h [R, d] for bf16 dy [R, d], with the statistics that the
+    forward call gave: (dx bf16 [R, d], dgamma fp32 [d], dbeta fp32 [d]).
+
+    ``dresidual`` bf16 [R, d], the gradient that reaches h past the norm, is added to dx; with ``accumulate`` the sums
+    are added to the given ``dgamma`` and ``dbeta``."""
+    _need(dy, "dy", _BF16, 2)
+    R, d = dy.shape
+    dev = dy.device
+    _need_like(h, "h", _BF16, (R, d), dev)
+    _need_like(gamma, "gamma", _BF16, (d,), dev)
+    _need_like(mean, "mean", _F32, (R,), dev)
+    _need_like(rstd, "rstd", _F32, (R,), dev)
+    if dresidual is not None:
+        _need_like(dresidual, "dresidual", _BF16, (R, d), dev)
+    if accumulate and (dgamma is None or dbeta is None):
+        raise ValueError("accumulate needs dgamma and dbeta")
+    dx = _output(dx, "dx", _BF16, (R, d), dev)
+    dgamma, dbeta = _output(dgamma, "dgamma", _F32, (d,), dev), _output(dbeta, "dbeta", _F32, (d,), dev)
+    size = (_lib or load_library()).fp8bs_layernorm_backward_workspace(R, d)
+    ws = _workspace(size, dev)
+    _call_on(dev, "fp8bs_layernorm_backward", dy.data_ptr(), h.data_ptr(), gamma.data_ptr(), mean.data_ptr(),
+             rstd.data_ptr(), _ptr(dresidual), R, d, dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+             1 if accumulate else 0, ws.data_ptr(), size)
+    return dx, dgamma, dbeta
+
+
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 

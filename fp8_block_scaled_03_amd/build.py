@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8bs.so")
 
 SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "rmsnorm.hip", "gemm_e8m0.hip", "api_g128.cpp",
-           "quantize_g128.hip", "gemm_g128.hip", "wgrad.hip", "swiglu.hip", "api_layer.cpp", "gradnorm.hip"]
+           "quantize_g128.hip", "gemm_g128.hip", "wgrad.hip", "swiglu.hip",
+           "api_layer.cpp", "gradnorm.hip", "layernorm.hip"]
 # measurement and test support (single instructions for the tests and the
 # bench), linked into a library of its own
 PROBE_SOURCES = ["probe.hip"]

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <vector>
 
 #include "launch_layer.hpp"
@@ -18,6 +19,43 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 fp8bs_status from_launch(hipError_t e) {
   if (e == hipErrorNotSupported) return FP8BS_ESHAPE;
   return e == hipSuccess ? FP8BS_OK : FP8BS_EHIP;
+}
+
+constexpr int64_t MAX_DIM = int64_t(1) << 30;
+
+// Kernel attributes (dynamic LDS above the default), once per process and device.
+fp8bs_status ensure_attributes() {
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return FP8BS_EHIP;
+  if (dev < 0 || dev >= 64) return FP8BS_EHIP;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!done[dev]) {
+    if (fp8bs::set_layernorm_attributes() != hipSuccess) return FP8BS_EHIP;
+    done[dev] = true;
+  }
+  return FP8BS_OK;
+}
+
+fp8bs_status check_workspace(const void* workspace, int64_t have, int64_t need) {
+  if (need == 0) return FP8BS_OK;
+  if (!workspace || have < need) return FP8BS_EINVAL;
+  return aligned(workspace, 16) ? FP8BS_OK : FP8BS_EALIGN;
+}
+
+// Sizes and the arguments that both forms of the layer norm have.
+fp8bs_status check_layernorm(const void* x, const void* residual, const void* gamma, const void* beta, float eps,
+                             int64_t rows, int64_t d, const void* h, const void* y, const float* mean,
+                             const float* rstd) {
+  if (rows < 0 || d < 0 || !(eps >= 0) || std::isinf(eps) || (mean == nullptr) != (rstd == nullptr))
+    return FP8BS_EINVAL;
+  if (rows > MAX_DIM || d > fp8bs::layernorm_max_cols() || d % 16) return FP8BS_ESHAPE;
+  if (rows == 0 || d == 0) return FP8BS_OK;
+  if (!x || !gamma) return FP8BS_EINVAL;
+  for (const void* p : {x, residual, gamma, beta, h, y})
+    if (!aligned(p, 16)) return FP8BS_EALIGN;
+  return aligned(mean, 4) && aligned(rstd, 4) ? FP8BS_OK : FP8BS_EALIGN;
 }
 
 constexpr int64_t MAX_COUNT = int64_t(1) << 36;  // a launch's chunks of 32 KB stay below 2^31
@@ -77,14 +115,59 @@ fp8bs_status check_clip(const void* const* grads, void* const* outs, const int64
   return FP8BS_OK;
 }
 
-fp8bs_status check_workspace(const void* workspace, int64_t have, int64_t need) {
-  if (!workspace || have < need) return FP8BS_EINVAL;
-  return aligned(workspace, 16) ? FP8BS_OK : FP8BS_EALIGN;
-}
-
 }  // namespace
 
 extern "C" {
+
+fp8bs_status fp8bs_layernorm_quantize_tg128(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                                            const void* beta_bf16, float eps, int64_t rows, int64_t d, void* h_bf16,
+                                            void* q_e4m3, float* scales, void* y_bf16, float* mean, float* rstd,
+                                            void* stream) {
+  const fp8bs_status st =
+      check_layernorm(x_bf16, residual_bf16, gamma_bf16, beta_bf16, eps, rows, d, h_bf16, y_bf16, mean, rstd);
+  if (st != FP8BS_OK || rows == 0 || d == 0) return st;
+  if (!q_e4m3 || !scales) return FP8BS_EINVAL;
+  if (!aligned(q_e4m3, 16) || !aligned(scales, 4)) return FP8BS_EALIGN;
+  return from_launch(fp8bs::launch_layernorm(x_bf16, residual_bf16, gamma_bf16, beta_bf16, eps, rows, d, h_bf16,
+                                             q_e4m3, scales, y_bf16, mean, rstd, (hipStream_t)stream));
+}
+
+fp8bs_status fp8bs_layernorm(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                             const void* beta_bf16, float eps, int64_t rows, int64_t d, void* h_bf16, void* y_bf16,
+                             float* mean, float* rstd, void* stream) {
+  const fp8bs_status st =
+      check_layernorm(x_bf16, residual_bf16, gamma_bf16, beta_bf16, eps, rows, d, h_bf16, y_bf16, mean, rstd);
+  if (st != FP8BS_OK || rows == 0 || d == 0) return st;
+  if (!y_bf16) return FP8BS_EINVAL;
+  return from_launch(fp8bs::launch_layernorm(x_bf16, residual_bf16, gamma_bf16, beta_bf16, eps, rows, d, h_bf16,
+                                             nullptr, nullptr, y_bf16, mean, rstd, (hipStream_t)stream));
+}
+
+int64_t fp8bs_layernorm_backward_workspace(int64_t rows, int64_t d) {
+  if (rows <= 0 || d <= 0 || rows > MAX_DIM || d > fp8bs::layernorm_max_cols()) return 0;
+  return fp8bs::layernorm_backward_workspace(rows, d);
+}
+
+fp8bs_status fp8bs_layernorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16,
+                                      const float* mean, const float* rstd, const void* dresidual_bf16, int64_t rows,
+                                      int64_t d, void* dx_bf16, float* dgamma, float* dbeta, int32_t accumulate,
+                                      void* workspace, int64_t workspace_bytes, void* stream) {
+  if (rows < 0 || d < 0) return FP8BS_EINVAL;
+  if (rows > MAX_DIM || d > fp8bs::layernorm_max_cols() || d % 16) return FP8BS_ESHAPE;
+  if (d == 0) return FP8BS_OK;
+  if (rows > 0 && (!dy_bf16 || !h_bf16 || !gamma_bf16 || !mean || !rstd || !dx_bf16)) return FP8BS_EINVAL;
+  for (const void* p : {dy_bf16, h_bf16, gamma_bf16, dresidual_bf16, (const void*)dx_bf16})
+    if (!aligned(p, 16)) return FP8BS_EALIGN;
+  for (const void* p : {mean, rstd, (const float*)dgamma, (const float*)dbeta})
+    if (!aligned(p, 4)) return FP8BS_EALIGN;
+  fp8bs_status st = check_workspace(workspace, workspace_bytes, fp8bs_layernorm_backward_workspace(rows, d));
+  if (st != FP8BS_OK) return st;
+  st = ensure_attributes();
+  if (st != FP8BS_OK) return st;
+  return from_launch(fp8bs::launch_layernorm_backward(dy_bf16, h_bf16, gamma_bf16, mean, rstd, dresidual_bf16, rows,
+                                                      d, dx_bf16, dgamma, dbeta, accumulate != 0, (float*)workspace,
+                                                      (hipStream_t)stream));
+}
 
 int64_t fp8bs_grad_norm_workspace(int32_t n) { return fp8bs::grad_norm_workspace(n > 0 ? n : 0); }
 

@@ -4,6 +4,17 @@
 #include <stdint.h>
 
 namespace fp8bs {
+// q and scales, y, h, residual, beta, mean and rstd may be null
+hipError_t launch_layernorm(const void* x, const void* residual, const void* gamma, const void* beta, float eps,
+                            int64_t rows, int64_t d, void* h, void* q, float* scales, void* y, float* mean,
+                            float* rstd, hipStream_t stream);
+int layernorm_max_cols();
+int64_t layernorm_backward_workspace(int64_t rows, int64_t d);
+hipError_t launch_layernorm_backward(const void* dy, const void* h, const void* gamma, const float* mean,
+                                     const float* rstd, const void* dresidual, int64_t rows, int64_t d, void* dx,
+                                     float* dgamma, float* dbeta, bool accumulate, float* workspace,
+                                     hipStream_t stream);
+hipError_t set_layernorm_attributes();
 // The gradients of one call, on the host.
 struct Grads {
   const void* const* src;

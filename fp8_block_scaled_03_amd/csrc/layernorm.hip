@@ -1,0 +1,420 @@
+// Residual add + layer norm + the row quantizer of 128 values, and the backward pass.
+//
+//   h = bf16(x + r),  mu = sum h / d,  var = sum (h - mu)^2 / d,  rstd = 1 / sqrt(var + eps)
+//   y = (h - mu) rstd gamma + beta;  codes and scales of the fp32 y, 128 columns each
+//
+// A row stays in registers between the sums (packed bf16), so x and the residual are
+// read once.  mu is taken in two steps: m = sum h / d as fp32 gives it, then
+// delta = sum (h - m) / d, so that a row far from zero (|mu| >> sigma) keeps its
+// digits: the deviation is (h - m) - delta, var = sum (h - m)^2 / d - delta^2.
+//
+//   backward, with xh = (h - mean) rstd and g = dy gamma:
+//   dx = rstd (g - sum g / d - xh sum (g xh) / d) [+ the residual stream's gradient]
+//   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+//
+// Row mapping: WPR waves hold a row, lane l of wave k the columns
+// 512 (WPR i + k) + 8 l .. +7, i < NL <= 4: 16 lanes hold a group of 128.  Sums run
+// over a lane's columns in order, over lanes by a butterfly, over waves in order: a
+// row's results depend on that row and on d only.
+//
+// dgamma and dbeta: a workgroup walks every gridDim.x-th set of rows and keeps
+// its columns' sums in registers, joins its rows' sums in LDS and writes them once
+// to the workspace; a second launch adds the workgroups' sums in order.  The
+// grid depends on the sizes only, so results are the same bits every time.
+//
+// Bound by HBM traffic: forward 7 bytes a value (9 with y), backward 6 (8).
+#include "column_sum.hpp"
+#include "launch_layer.hpp"
+#include "quant_g128.hpp"
+
+namespace fp8bs {
+
+constexpr int LN_NL = 4, LN_MAX_WPR = 8;
+
+// Sum over the lanes of a wave, in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// Two sums over a row's WPR waves, of which this is wave wk of the workgroup's wave
+// w; `lds` is not in use by another sum since the last barrier but one.
+template <int WPR>
+__device__ __forceinline__ void row_sums(float& a, float& b, int w, float (*lds)[2]) {
+  a = wave_sum(a);
+  b = wave_sum(b);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) {
+      lds[w][0] = a;
+      lds[w][1] = b;
+    }
+    __syncthreads();
+    const int first = w & ~(WPR - 1);
+    a = lds[first][0];
+    b = lds[first][1];
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      a += lds[first + k][0];
+      b += lds[first + k][1];
+    }
+  }
+}
+
+struct LayerNorm {
+  const uint16_t *x, *res, *gamma, *beta;
+  uint16_t *h, *y;
+  uint8_t* q;
+  float *scales, *mean, *rstd;
+  int64_t rows, d;
+  float eps;
+};
+
+template <int NL, int WPR, bool LINES>
+__global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNorm p, uint32_t sets) {
+  constexpr int WAVES = WPR == 8 ? 8 : 4, RPW = WAVES / WPR;  // waves and rows of a workgroup
+  __shared__ float sums[2][WAVES][2];
+  const int lane = threadIdx.x & 63, w = wave_id_uniform(), wk = w & (WPR - 1);
+  const int d = (int)p.d, nb = (d + 127) >> 7;
+  const float inv_d = 1.0f / (float)d;
+  uint4 gv[NL], bv[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int col = (WPR * i + wk) * 512 + lane * 8;
+    gv[i] = col < d ? *reinterpret_cast<const uint4*>(p.gamma + col) : make_uint4(0, 0, 0, 0);
+    bv[i] = p.beta != nullptr && col < d ? *reinterpret_cast<const uint4*>(p.beta + col) : make_uint4(0, 0, 0, 0);
+  }
+  for (uint32_t id = blockIdx.x; id < sets; id += gridDim.x) {
+    const int64_t row = (int64_t)region_at<LINES>(id, sets) * RPW + w / WPR;
+    const bool row_ok = row < p.rows;
+    const int64_t at = (row_ok ? row : p.rows - 1) * p.d;
+    uint4 hv[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int col = (WPR * i + wk) * 512 + lane * 8;
+      hv[i] = col < d ? *reinterpret_cast<const uint4*>(p.x + at + col) : make_uint4(0, 0, 0, 0);
+    }
+    if (p.res != nullptr) {
+      uint4 rv[NL];
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int col = (WPR * i + wk) * 512 + lane * 8;
+        rv[i] = col < d ? *reinterpret_cast<const uint4*>(p.res + at + col) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        const int col = (WPR * i + wk) * 512 + lane * 8;
+        float a[8], b[8];
+        unpack8(hv[i], a);
+        unpack8(rv[i], b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += b[j];  // rounds to bf16 as the exact sum does
+        hv[i] = bf16_round8(a);
+        if (p.h != nullptr && row_ok && col < d) *reinterpret_cast<uint4*>(p.h + at + col) = hv[i];
+      }
+    }
+    float s = 0.0f, unused = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      float a[8];
+      unpack8(hv[i], a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += a[j];
+    }
+    row_sums<WPR>(s, unused, w, sums[0]);
+    const float m = s * inv_d;
+    float dev = 0.0f, sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int col = (WPR * i + wk) * 512 + lane * 8;
+      float a[8];
+      unpack8(hv[i], a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float c = col < d ? a[j] - m : 0.0f;
+        dev += c;
+        sq = __builtin_fmaf(c, c, sq);
+      }
+    }
+    row_sums<WPR>(dev, sq, w, sums[1]);
+    const float delta = dev * inv_d;
+    const float var = fmaxf(__builtin_fmaf(-delta, delta, sq * inv_d), 0.0f);
+    const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
+    if (p.mean != nullptr && row_ok && lane == 0 && wk == 0) {
+      p.mean[row] = m + delta;
+      p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int col = (WPR * i + wk) * 512 + lane * 8;
+      const bool ok = row_ok && col < d;
+      // unpacked again: the floats of the row are not kept over the sums
+      asm volatile("" : "+v"(hv[i].x), "+v"(hv[i].y), "+v"(hv[i].z), "+v"(hv[i].w));
+      asm volatile("" : "+v"(gv[i].x), "+v"(gv[i].y), "+v"(gv[i].z), "+v"(gv[i].w));
+      asm volatile("" : "+v"(bv[i].x), "+v"(bv[i].y), "+v"(bv[i].z), "+v"(bv[i].w));
+      float v[8], g[8], b[8];
+      unpack8(hv[i], v);
+      unpack8(gv[i], g);
+      unpack8(bv[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = col < d ? __builtin_fmaf(((v[j] - m) - delta) * rstd, g[j], b[j]) : 0.0f;
+      if (p.y != nullptr && ok) *reinterpret_cast<uint4*>(p.y + at + col) = bf16_round8(v);
+      if (p.q != nullptr) {
+        const Scale sc = scale_of(row16_max(amax8(v)));
+        const uint2 codes = __all(sc.r != 0.0f || !ok) ? codes8<true>(v, sc) : codes8<false>(v, sc);
+        if (ok) {
+          put_codes8<LINES>(p.q + at + col, codes);
+          if ((lane & 15) == 0) p.scales[row * nb + (col >> 7)] = sc.s;
+        }
+      }
+    }
+  }
+}
+
+// ---- backward ---------------------------------------------------------------------------
+constexpr int LNB_WAVES = 16, LNB_NL = 2;  // waves of a workgroup, pieces of a lane at most
+
+struct LayerNormBackward {
+  const uint16_t *dy, *h, *gamma, *dres;
+  const float *mean, *rstd;
+  uint16_t* dx;
+  float* partial;  // [gridDim.x, 2, d]
+  int64_t rows, d;
+};
+
+template <int NL, int WPR, bool STREAM>
+__global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(LayerNormBackward p, uint32_t sets) {
+  constexpr int RPW = LNB_WAVES / WPR;  // rows of a workgroup
+  __shared__ float sums[2][LNB_WAVES][2];
+  extern __shared__ __attribute__((aligned(16))) float joined[];  // [2][NL][8][64 WPR] if RPW > 1
+  const int lane = threadIdx.x & 63, w = wave_id_uniform(), wk = w & (WPR - 1), sub = w / WPR;
+  const int d = (int)p.d;
+  const float inv_d = 1.0f / (float)d;
+  int at_col[NL];  // columns past d read column 0 (gamma is 0 there, their sums are not stored)
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int col = (WPR * i + wk) * 512 + lane * 8;
+    at_col[i] = col < d ? col : 0;
+  }
+  // Rows past the end read the last row (not added, not stored).
+  auto row_of = [&](uint32_t id) __attribute__((always_inline)) -> int64_t {
+    const int64_t row = (int64_t)(id < sets ? id : sets - 1) * RPW + sub;
+    return row < p.rows ? row : p.rows - 1;
+  };
+  auto load = [&](uint32_t id, uint4 (&dy)[NL], uint4 (&h)[NL], float& mean, float& rstd)
+      __attribute__((always_inline)) {
+    const int64_t from = row_of(id);
+    const uint16_t *const a = p.dy + from * p.d, *const b = p.h + from * p.d;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      dy[i] = *reinterpret_cast<const uint4*>(a + at_col[i]);
+      h[i] = *reinterpret_cast<const uint4*>(b + at_col[i]);
+    }
+    mean = p.mean[from];
+    rstd = p.rstd[from];
+  };
+  uint4 gv[NL];
+  float dg[NL][8], db[NL][8];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int col = (WPR * i + wk) * 512 + lane * 8;
+    gv[i] = col < d ? *reinterpret_cast<const uint4*>(p.gamma + col) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
+  }
+  // The residual stream's gradient is needed last: it is asked for before the next
+  // set's rows, which stay in flight when it is waited for.
+  uint4 rv[STREAM ? NL : 1];
+  auto load_stream = [&](uint32_t id) __attribute__((always_inline)) {
+    if constexpr (STREAM) {
+      const uint16_t* const a = p.dres + row_of(id) * p.d;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) rv[i] = *reinterpret_cast<const uint4*>(a + at_col[i]);
+    }
+  };
+  // One set of rows; the next set's loads are in flight meanwhile.
+  auto work = [&](uint32_t id, uint4 (&dyv)[NL], uint4 (&hv)[NL], float mean, float rstd, int turn)
+      __attribute__((always_inline)) {
+    const int64_t row = (int64_t)id * RPW + sub;
+    const bool row_ok = row < p.rows;  // (the same for the whole wave)
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      if (!row_ok) break;
+      float dy[8], h[8], g[8];
+      unpack8(dyv[i], dy);
+      unpack8(hv[i], h);
+      unpack8(gv[i], g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = (h[j] - mean) * rstd, gy = dy[j] * g[j];
+        s1 += gy;
+        s2 = __builtin_fmaf(gy, xh, s2);
+        db[i][j] += dy[j];
+        dg[i][j] = __builtin_fmaf(dy[j], xh, dg[i][j]);
+      }
+    }
+    row_sums<WPR>(s1, s2, w, sums[turn]);
+    const float c1 = s1 * inv_d, c2 = s2 * inv_d;
+    uint16_t* const out = p.dx + row * p.d;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      // unpacked a second time: 24 values for each of the row's pieces are not kept over the sums
+      asm volatile("" : "+v"(dyv[i].x), "+v"(dyv[i].y), "+v"(dyv[i].z), "+v"(dyv[i].w));
+      asm volatile("" : "+v"(hv[i].x), "+v"(hv[i].y), "+v"(hv[i].z), "+v"(hv[i].w));
+      asm volatile("" : "+v"(gv[i].x), "+v"(gv[i].y), "+v"(gv[i].z), "+v"(gv[i].w));
+      const int col = (WPR * i + wk) * 512 + lane * 8;
+      float dy[8], h[8], g[8], r[8];
+      unpack8(dyv[i], dy);
+      unpack8(hv[i], h);
+      unpack8(gv[i], g);
+      if constexpr (STREAM) unpack8(rv[i], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = (h[j] - mean) * rstd;
+        const float v = __builtin_fmaf(-xh, c2, __builtin_fmaf(dy[j], g[j], -c1));
+        if constexpr (STREAM) dy[j] = __builtin_fmaf(v, rstd, r[j]);
+        else dy[j] = v * rstd;
+      }
+      if (row_ok && col < d) *reinterpret_cast<uint4*>(out + col) = bf16_round8(dy);
+    }
+  };
+  uint4 dy0[NL], h0[NL], dy1[NL], h1[NL];
+  float mean0, rstd0, mean1, rstd1;
+  const uint32_t step = gridDim.x;
+  load(blockIdx.x, dy0, h0, mean0, rstd0);
+  for (uint32_t id = blockIdx.x; id < sets; id += 2 * step) {
+    load_stream(id);
+    load(id + step, dy1, h1, mean1, rstd1);
+    work(id, dy0, h0, mean0, rstd0, 0);
+    if (id + step >= sets) break;  // (the same for the whole workgroup)
+    load_stream(id + step);
+    load(id + 2 * step, dy0, h0, mean0, rstd0);
+    work(id + step, dy1, h1, mean1, rstd1, 1);
+  }
+  if constexpr (RPW > 1) {  // the workgroup's rows, in order
+    for (int k = 1; k < RPW; ++k) {
+      __syncthreads();
+      float* const mine = joined + wk * 64 + lane;
+      if (sub == k) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            mine[(i * 8 + j) * 64 * WPR] = dg[i][j];
+            mine[(NL * 8 + i * 8 + j) * 64 * WPR] = db[i][j];
+          }
+      }
+      __syncthreads();
+      if (sub == 0) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            dg[i][j] += mine[(i * 8 + j) * 64 * WPR];
+            db[i][j] += mine[(NL * 8 + i * 8 + j) * 64 * WPR];
+          }
+      }
+    }
+  }
+  if (sub == 0) {
+    float* const out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int col = (WPR * i + wk) * 512 + lane * 8;
+      if (col < d) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          *reinterpret_cast<float4*>(out + col + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+          *reinterpret_cast<float4*>(out + d + col + j) =
+              make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+        }
+      }
+    }
+  }
+}
+
+int layernorm_max_cols() { return 512 * LN_NL * LN_MAX_WPR; }
+
+template <int NL, int WPR>
+static void launch_ln(const LayerNorm& p, hipStream_t stream) {
+  constexpr int THREADS = WPR == 8 ? 512 : 256, RPW = THREADS / 64 / WPR;
+  const int64_t sets = (p.rows + RPW - 1) / RPW;
+  const dim3 grid((unsigned)(sets < 2048 ? sets : 2048));
+  if (p.d % 128 == 0)
+    hipLaunchKernelGGL((layernorm_kernel<NL, WPR, true>), grid, dim3(THREADS), 0, stream, p, (uint32_t)sets);
+  else
+    hipLaunchKernelGGL((layernorm_kernel<NL, WPR, false>), grid, dim3(THREADS), 0, stream, p, (uint32_t)sets);
+}
+
+hipError_t launch_layernorm(const void* x, const void* residual, const void* gamma, const void* beta, float eps,
+                            int64_t rows, int64_t d, void* h, void* q, float* scales, void* y, float* mean,
+                            float* rstd, hipStream_t stream) {
+  const LayerNorm p = {(const uint16_t*)x, (const uint16_t*)residual, (const uint16_t*)gamma, (const uint16_t*)beta,
+                       (uint16_t*)h,       (uint16_t*)y,              (uint8_t*)q,            scales,
+                       mean,               rstd,                      rows,                   d, eps};
+  if (d <= 512) launch_ln<1, 1>(p, stream);
+  else if (d <= 1024) launch_ln<2, 1>(p, stream);
+  else if (d <= 2048) launch_ln<4, 1>(p, stream);
+  else if (d <= 4096) launch_ln<4, 2>(p, stream);
+  else if (d <= 8192) launch_ln<4, 4>(p, stream);
+  else launch_ln<4, 8>(p, stream);
+  return hipGetLastError();
+}
+
+// Sets of rows (what a workgroup takes at once) and workgroups of the backward pass.
+static int64_t ln_sets(int64_t rows, int64_t d) {
+  const int wpr = d <= 1024 ? 1 : d <= 2048 ? 2 : d <= 4096 ? 4 : d <= 8192 ? 8 : 16, rpw = LNB_WAVES / wpr;
+  return (rows + rpw - 1) / rpw;
+}
+static int64_t ln_backward_grid(int64_t rows, int64_t d) {
+  const int64_t sets = ln_sets(rows, d);
+  return sets < 256 ? sets : 256;
+}
+
+int64_t layernorm_backward_workspace(int64_t rows, int64_t d) { return ln_backward_grid(rows, d) * 2 * d * 4; }
+
+template <int NL, int WPR>
+constexpr int ln_backward_lds() { return WPR < LNB_WAVES ? 2 * NL * 8 * 64 * WPR * 4 : 0; }
+
+template <int NL, int WPR>
+static void launch_ln_backward(const LayerNormBackward& p, unsigned grid, uint32_t sets, hipStream_t stream) {
+  constexpr int LDS = ln_backward_lds<NL, WPR>(), THREADS = 64 * LNB_WAVES;
+  if (p.dres)
+    hipLaunchKernelGGL((layernorm_backward_kernel<NL, WPR, true>), dim3(grid), dim3(THREADS), LDS, stream, p, sets);
+  else
+    hipLaunchKernelGGL((layernorm_backward_kernel<NL, WPR, false>), dim3(grid), dim3(THREADS), LDS, stream, p, sets);
+}
+
+hipError_t set_layernorm_attributes() {
+  hipError_t e = hipSuccess;
+  auto allow = [&](const void* kernel, int lds) {
+    if (e == hipSuccess) e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  };
+  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, true>, ln_backward_lds<LNB_NL, 8>());
+  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, false>, ln_backward_lds<LNB_NL, 8>());
+  return e;
+}
+
+hipError_t launch_layernorm_backward(const void* dy, const void* h, const void* gamma, const float* mean,
+                                     const float* rstd, const void* dresidual, int64_t rows, int64_t d, void* dx,
+                                     float* dgamma, float* dbeta, bool accumulate, float* workspace,
+                                     hipStream_t stream) {
+  const LayerNormBackward p = {(const uint16_t*)dy, (const uint16_t*)h, (const uint16_t*)gamma,
+                               (const uint16_t*)dresidual, mean, rstd, (uint16_t*)dx, workspace, rows, d};
+  const uint32_t sets = (uint32_t)ln_sets(rows, d);
+  const unsigned grid = (unsigned)ln_backward_grid(rows, d);
+  if (grid > 0) {
+    if (d <= 512) launch_ln_backward<1, 1>(p, grid, sets, stream);
+    else if (d <= 1024) launch_ln_backward<LNB_NL, 1>(p, grid, sets, stream);
+    else if (d <= 2048) launch_ln_backward<LNB_NL, 2>(p, grid, sets, stream);
+    else if (d <= 4096) launch_ln_backward<LNB_NL, 4>(p, grid, sets, stream);
+    else if (d <= 8192) launch_ln_backward<LNB_NL, 8>(p, grid, sets, stream);
+    else launch_ln_backward<LNB_NL, 16>(p, grid, sets, stream);
+  }
+  launch_column_sum(workspace, grid, 2 * d, d, dgamma, dbeta, accumulate, stream);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

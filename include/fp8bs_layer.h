@@ -1,6 +1,7 @@
 /*
  * fp8bs_layer.h - the entry points of libfp8bs.so that stand between the products
- * of a transformer block: gradient norms and clipping.
+ * of a transformer block: layer norm with its backward pass, gradient norms and
+ * clipping.
  * Status codes, pointer ownership, streams and errors are those of fp8bs.h; the
  * E4M3 format and the quantizer's rule for 128 values are those of fp8bs_g128.h.
  *
@@ -21,6 +22,55 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/*
+ * fp8bs_layernorm_quantize_tg128 - residual add + layer norm + the row quantizer of
+ *   128 values, in one pass over each row:
+ *     residual != NULL:  h = bf16(x + residual) (nearest even), written to h if given
+ *     residual == NULL:  h = x (and the argument h is not used)
+ *     mean = sum(h) / d,  var = sum((h - mean)^2) / d,  rstd = 1 / sqrt(var + eps)  (fp32)
+ *     y_i = (h_i - mean) * rstd * gamma_i + beta_i                                (fp32)
+ *     q, scales = the quantizer's rule of fp8bs_g128.h on the fp32 y (128 columns each)
+ *   x [rows, d] bf16, residual [rows, d] bf16 or NULL, gamma [d] bf16,
+ *   beta [d] bf16 or NULL (no bias)
+ *   h [rows, d] bf16 out or NULL; may be residual or x themselves (in place)
+ *   q [rows, d] E4M3 out, scales [rows, ceil128(d)] fp32 out
+ *   y [rows, d] bf16 out (rounded to nearest) or NULL
+ *   mean, rstd [rows] fp32 out for the backward pass, or both NULL
+ *   eps finite and >= 0 (else FP8BS_EINVAL); with eps == 0 a row of equal values has
+ *   no defined result.  d % 16 == 0, d <= 16384, rows <= 2^30 (else FP8BS_ESHAPE);
+ *   rows == 0 or d == 0: no-op.  Matrices, gamma and beta are 16-byte aligned, scales
+ *   and statistics 4-byte (else FP8BS_EALIGN).  A row's results depend on that row
+ *   only.  Outputs other than h overlap no input.
+ */
+fp8bs_status fp8bs_layernorm_quantize_tg128(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                                            const void* beta_bf16, float eps, int64_t rows, int64_t d, void* h_bf16,
+                                            void* q_e4m3, float* scales, void* y_bf16, float* mean, float* rstd,
+                                            void* stream);
+
+/* fp8bs_layernorm - the same without codes; y is required. */
+fp8bs_status fp8bs_layernorm(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
+                             const void* beta_bf16, float eps, int64_t rows, int64_t d, void* h_bf16, void* y_bf16,
+                             float* mean, float* rstd, void* stream);
+
+/*
+ * fp8bs_layernorm_backward - the gradients of y = (h - mean) rstd gamma + beta, with
+ *   xh = (h - mean) * rstd and g = dy * gamma, all in fp32:
+ *     dx     = rstd * (g - sum(g)/d - xh * sum(g xh)/d) (+ dresidual), rounded to bf16
+ *     dgamma = sum over the rows of dy * xh,  dbeta = sum over the rows of dy
+ *   dy, h [rows, d] bf16, gamma [d] bf16, mean, rstd [rows] fp32 (the forward call's)
+ *   dresidual [rows, d] bf16 or NULL: the gradient that reaches h past the norm
+ *   dx [rows, d] bf16 out
+ *   dgamma, dbeta [d] fp32 out, each or NULL; if accumulate != 0 the sums are added
+ *      to what they hold.  rows == 0: zeros (or nothing is added).
+ *   workspace of fp8bs_layernorm_backward_workspace(rows, d) bytes (else FP8BS_EINVAL).
+ *   Sizes and alignment as above; outputs overlap no input.
+ */
+int64_t fp8bs_layernorm_backward_workspace(int64_t rows, int64_t d);
+fp8bs_status fp8bs_layernorm_backward(const void* dy_bf16, const void* h_bf16, const void* gamma_bf16,
+                                      const float* mean, const float* rstd, const void* dresidual_bf16, int64_t rows,
+                                      int64_t d, void* dx_bf16, float* dgamma, float* dbeta, int32_t accumulate,
+                                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Types of a gradient. */
 #define FP8BS_F32 0

@@ -29,6 +29,60 @@ def test_library_exports_every_declared_symbol():
             assert hasattr(fp8bs, n[len("fp8bs_"):]), n
 
 
+def test_layernorm_refusals():
+    f = binding.layernorm_quantize_tg128_raw
+    ok = [A16, A16, A16, A16, 1e-5, 4, 64, A16, A16, A4, A16, A4, A4]
+
+    def with_(**at):
+        p = list(ok)
+        for i, v in at.items():
+            p[int(i[1:])] = v
+        return f(*p)
+
+    assert with_(_5=0) == OK and with_(_6=0) == OK and with_(_5=0, _0=None, _2=None, _8=None, _9=None) == OK
+    assert with_(_5=-1) == EINVAL and with_(_6=-16) == EINVAL
+    for eps in (-1e-9, float("nan"), float("inf")):
+        assert with_(_4=eps) == EINVAL
+    assert with_(_6=40) == ESHAPE and with_(_6=16400) == ESHAPE and with_(_5=BIG + 1) == ESHAPE
+    for i in (0, 2, 8, 9, 11, 12):
+        assert with_(**{f"_{i}": None}) == EINVAL
+    for i in (0, 1, 2, 3, 7, 8, 10):
+        assert with_(**{f"_{i}": A16 + 8}) == EALIGN
+    for i in (9, 11, 12):
+        assert with_(**{f"_{i}": A4 + 2}) == EALIGN
+    g = binding.layernorm_raw
+    assert g(A16, None, A16, None, 1e-5, 0, 64, None, A16, None, None) == OK
+    assert g(A16, None, A16, None, 1e-5, 4, 64, None, None, None, None) == EINVAL
+    assert g(A16, None, A16, None, 1e-5, 4, 64, None, A16, A4, None) == EINVAL
+    assert g(A16, None, A16, None, 1e-5, 4, 65, None, A16, None, None) == ESHAPE
+
+
+def test_layernorm_backward_refusals():
+    lib = binding.load_library()
+    size = lib.fp8bs_layernorm_backward_workspace(4, 64)
+    assert size > 0 and lib.fp8bs_layernorm_backward_workspace(0, 64) == 0
+    assert lib.fp8bs_layernorm_backward_workspace(-1, 64) == 0
+    assert lib.fp8bs_layernorm_backward_workspace(4, 16400) == 0
+    ok = [A16, A16, A16, A4, A4, A16, 4, 64, A16, A4, A4, 0, A16, size]
+
+    def with_(**at):
+        p = list(ok)
+        for i, v in at.items():
+            p[int(i[1:])] = v
+        return binding.layernorm_backward_raw(*p)
+
+    assert with_(_7=0) == OK
+    assert with_(_6=-1) == EINVAL and with_(_7=-16) == EINVAL
+    assert with_(_7=24) == ESHAPE and with_(_7=16400) == ESHAPE and with_(_6=BIG + 1) == ESHAPE
+    for i in (0, 1, 2, 3, 4, 8, 12):
+        assert with_(**{f"_{i}": None}) == EINVAL
+    assert with_(_13=size - 1) == EINVAL
+    for i in (0, 1, 2, 5, 8, 12):
+        assert with_(**{f"_{i}": A16 + 8}) == EALIGN
+    for i in (3, 4, 9, 10):
+        assert with_(**{f"_{i}": A4 + 2}) == EALIGN
+
+
 # ---- gradients ---------------------------------------------------------------------------
 def _arrays(pointers, counts, types):
     n = len(pointers)

@@ -17,6 +17,8 @@ _BINDING_NAMES = ("Fp8bsError", "quantize", "gemm", "grouped_gemm", "gemm_nt", "
                   "swiglu_quantize_tg128_raw", "swiglu_backward_quantize_tg128_raw",
                   "layernorm_quantize_tg128", "layernorm", "layernorm_backward", "layernorm_quantize_tg128_raw",
                   "layernorm_raw", "layernorm_backward_raw",
+                  "ACTIVATIONS", "gemm_tg128_nt_epilogue", "epilogue_backward_quantize_tg128",
+                  "gemm_tg128_nt_epilogue_raw", "epilogue_backward_quantize_tg128_raw",
                   "grad_norm", "clip_grads", "clip_grad_norm", "grad_norm_raw", "clip_grads_raw", "clip_grad_norm_raw")
 
 __all__ = list(_BINDING_NAMES)

@@ -89,6 +89,12 @@ def load_library() -> ctypes.CDLL:
         lib.fp8bs_layernorm_backward_workspace.restype = i64
         lib.fp8bs_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, i32, vp, i64, vp]
         lib.fp8bs_layernorm_backward.restype = ctypes.c_int
+        lib.fp8bs_gemm_tg128_nt_epilogue.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, i64, i64, i64, vp]
+        lib.fp8bs_gemm_tg128_nt_epilogue.restype = ctypes.c_int
+        lib.fp8bs_epilogue_backward_workspace.argtypes = [i64, i64]
+        lib.fp8bs_epilogue_backward_workspace.restype = i64
+        lib.fp8bs_epilogue_backward_quantize_tg128.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp]
+        lib.fp8bs_epilogue_backward_quantize_tg128.restype = ctypes.c_int
         lib.fp8bs_grad_norm_workspace.argtypes = [i32]
         lib.fp8bs_grad_norm_workspace.restype = i64
         lib.fp8bs_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp]
@@ -230,6 +236,19 @@ def layernorm_backward_raw(dy_ptr, h_ptr, gamma_ptr, mean_ptr, rstd_ptr, dres_pt
                            dbeta_ptr, accumulate, ws_ptr, ws_bytes, stream=None) -> int:
     return load_library().fp8bs_layernorm_backward(dy_ptr, h_ptr, gamma_ptr, mean_ptr, rstd_ptr, dres_ptr, rows, d,
                                                    dx_ptr, dgamma_ptr, dbeta_ptr, accumulate, ws_ptr, ws_bytes, stream)
+
+
+def gemm_tg128_nt_epilogue_raw(a_ptr, sa_ptr, bt_ptr, sbt_ptr, bias_ptr, activation, res_ptr, c_ptr, pre_ptr, M, N, K,
+                               stream=None) -> int:
+    return load_library().fp8bs_gemm_tg128_nt_epilogue(a_ptr, sa_ptr, bt_ptr, sbt_ptr, bias_ptr, activation, res_ptr,
+                                                       c_ptr, pre_ptr, M, N, K, stream)
+
+
+def epilogue_backward_quantize_tg128_raw(dout_ptr, pre_ptr, activation, rows, n, dz_ptr, q_ptr, s_ptr, dbias_ptr,
+                                         accumulate, ws_ptr, ws_bytes, stream=None) -> int:
+    return load_library().fp8bs_epilogue_backward_quantize_tg128(dout_ptr, pre_ptr, activation, rows, n, dz_ptr, q_ptr,
+                                                                 s_ptr, dbias_ptr, accumulate, ws_ptr, ws_bytes,
+                                                                 stream)
 
 
 def grad_norm_raw(grads, counts, types, n, norm_ptr, ws_ptr, ws_bytes, stream=None) -> int:
@@ -760,6 +779,72 @@ def layernorm_backward(dy: torch.Tensor, h: torch.Tensor, gamma: torch.Tensor, m
              rstd.data_ptr(), _ptr(dresidual), R, d, dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
              1 if accumulate else 0, ws.data_ptr(), size)
     return dx, dgamma, dbeta
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(name: str) -> int:
+    code = ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation {name!r} is none of {tuple(ACTIVATIONS)}")
+    return code
+
+
+def gemm_tg128_nt_epilogue(a: torch.Tensor, sa: torch.Tensor, bt: torch.Tensor, sbt: torch.Tensor,
+                           bias: torch.Tensor | None = None, activation: str = "none",
+                           residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                           pre: torch.Tensor | None = None, want_pre: bool = False):
+    """act(a bt' + bias) + residual for operands as gemm_tg128_nt's, bias bf16 [N], residual bf16 [M, N] (``out`` may
+    be it) and an activation of ACTIVATIONS, all in fp32 and rounded once to bf16 [M, N]; when ``want_pre`` is true
+    or ``pre`` is given, (out, pre) with a bt' + bias in bf16 for epilogue_backward_quantize_tg128."""
+    _need(a, "a", E4M3_DTYPES, 2)
+    _need(bt, "bt", E4M3_DTYPES, 2)
+    code = _activation(activation)
+    M, K = a.shape
+    N, KB, dev = bt.shape[0], _blocks128(K), a.device
+    _need_size(bt, "bt", 1, K, dev)
+    _need_like(sa, "sa", _F32, (M, KB), dev)
+    _need_like(sbt, "sbt", _F32, (_blocks128(N), KB), dev)
+    if bias is not None:
+        _need_like(bias, "bias", _BF16, (N,), dev)
+    if residual is not None:
+        _need_like(residual, "residual", _BF16, (M, N), dev)
+    out = _output(out, "out", _BF16, (M, N), dev)
+    if pre is not None or want_pre:
+        pre = _output(pre, "pre", _BF16, (M, N), dev)
+    _call_on(dev, "fp8bs_gemm_tg128_nt_epilogue", a.data_ptr(), sa.data_ptr(), bt.data_ptr(), sbt.data_ptr(),
+             _ptr(bias), code, _ptr(residual), out.data_ptr(), _ptr(pre), M, N, K)
+    return out if pre is None else (out, pre)
+
+
+def epilogue_backward_quantize_tg128(dout: torch.Tensor, pre: torch.Tensor | None, activation: str = "none",
+                                     dz: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                                     scales: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                                     accumulate: bool = False):
+    """The gradient of act(z) + residual with respect to z for bf16 dout [R, N] and the forward call's ``pre`` (which
+    "none" does not need): (dz bf16 [R, N], its codes uint8 [R, N] and scales fp32 [R, ceil(N/128)] as by
+    quantize_tg128 from the fp32 values, dbias fp32 [N], the sums of dz over the rows).  With ``accumulate`` they are
+    added to the given ``dbias``."""
+    _need(dout, "dout", _BF16, 2)
+    code = _activation(activation)
+    R, N = dout.shape
+    dev = dout.device
+    if pre is not None:
+        _need_like(pre, "pre", _BF16, (R, N), dev)
+    elif code:
+        raise ValueError(f"activation {activation!r} needs pre")
+    if accumulate and dbias is None:
+        raise ValueError("accumulate needs dbias")
+    dz = _output(dz, "dz", _BF16, (R, N), dev)
+    q = _output(q, "q", E4M3_DTYPES, (R, N), dev)
+    scales = _output(scales, "scales", _F32, (R, _blocks128(N)), dev)
+    dbias = _output(dbias, "dbias", _F32, (N,), dev)
+    size = (_lib or load_library()).fp8bs_epilogue_backward_workspace(R, N)
+    ws = _workspace(size, dev)
+    _call_on(dev, "fp8bs_epilogue_backward_quantize_tg128", dout.data_ptr(), _ptr(pre), code, R, N, dz.data_ptr(),
+             q.data_ptr(), scales.data_ptr(), dbias.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), size)
+    return dz, q, scales, dbias
 
 
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}

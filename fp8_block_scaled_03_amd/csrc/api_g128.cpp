@@ -1,12 +1,15 @@
-// C ABI of the 128-value forms (see include/fp8bs_g128.h).
+// C ABI of the 128-value forms (see include/fp8bs_g128.h) and of their product with an
+// epilogue (include/fp8bs_layer.h).
 // Host-side argument checks, then one launch on the caller's stream.
 #include "fp8bs_g128.h"
+#include "fp8bs_layer.h"
 
 #include <hip/hip_runtime.h>
 
 #include <mutex>
 
 #include "launch_g128.hpp"
+#include "launch_layer.hpp"
 
 namespace {
 
@@ -88,6 +91,21 @@ fp8bs_status fp8bs_gemm_tg128_nt(const void* a, const float* sa, const void* bt,
   st = ensure_attributes();
   if (st != FP8BS_OK) return st;
   return from_launch(fp8bs::launch_gemm_g128(a, sa, bt, sbt, nullptr, 1, c_bf16, M, N, K, (hipStream_t)stream));
+}
+
+fp8bs_status fp8bs_gemm_tg128_nt_epilogue(const void* a, const float* sa, const void* bt, const float* sbt,
+                                          const void* bias_bf16, int32_t activation, const void* residual_bf16,
+                                          void* c_bf16, void* pre_bf16, int64_t M, int64_t N, int64_t K,
+                                          void* stream) {
+  if (activation < FP8BS_ACT_NONE || activation > FP8BS_ACT_SILU) return FP8BS_EINVAL;
+  fp8bs_status st = check_gemm(a, sa, bt, sbt, c_bf16, M, N, K);
+  if (st != FP8BS_OK || M == 0 || N == 0) return st;
+  if (!aligned(bias_bf16, 16) || !aligned(residual_bf16, 16) || !aligned(pre_bf16, 16)) return FP8BS_EALIGN;
+  st = ensure_attributes();
+  if (st != FP8BS_OK) return st;
+  const fp8bs::Epilogue e = {(const uint16_t*)bias_bf16, (const uint16_t*)residual_bf16, (uint16_t*)pre_bf16,
+                             activation};
+  return from_launch(fp8bs::launch_gemm_g128_epilogue(a, sa, bt, sbt, e, c_bf16, M, N, K, (hipStream_t)stream));
 }
 
 fp8bs_status fp8bs_grouped_gemm_tg128_nt(const void* a, const float* sa, const void* bt, const float* sbt,

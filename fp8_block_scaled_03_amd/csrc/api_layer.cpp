@@ -169,6 +169,31 @@ fp8bs_status fp8bs_layernorm_backward(const void* dy_bf16, const void* h_bf16, c
                                                       (hipStream_t)stream));
 }
 
+int64_t fp8bs_epilogue_backward_workspace(int64_t rows, int64_t n) {
+  if (rows <= 0 || n <= 0 || rows > MAX_DIM || n > MAX_DIM) return 0;
+  return fp8bs::epilogue_backward_workspace(rows, n);
+}
+
+fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const void* pre_bf16, int32_t activation,
+                                                    int64_t rows, int64_t n, void* dz_bf16, void* q_e4m3,
+                                                    float* scales, float* dbias, int32_t accumulate, void* workspace,
+                                                    int64_t workspace_bytes, void* stream) {
+  if (rows < 0 || n < 0 || activation < FP8BS_ACT_NONE || activation > FP8BS_ACT_SILU) return FP8BS_EINVAL;
+  if (rows > MAX_DIM || n > MAX_DIM || n % 16) return FP8BS_ESHAPE;
+  if (n == 0) return FP8BS_OK;
+  if (rows > 0 && (!dout_bf16 || (!pre_bf16 && activation != FP8BS_ACT_NONE) || !q_e4m3 || !scales))
+    return FP8BS_EINVAL;
+  for (const void* p : {dout_bf16, pre_bf16, (const void*)dz_bf16, (const void*)q_e4m3})
+    if (!aligned(p, 16)) return FP8BS_EALIGN;
+  if (!aligned(scales, 4) || !aligned(dbias, 4)) return FP8BS_EALIGN;
+  const fp8bs_status st =
+      check_workspace(workspace, workspace_bytes, dbias ? fp8bs_epilogue_backward_workspace(rows, n) : 0);
+  if (st != FP8BS_OK) return st;
+  return from_launch(fp8bs::launch_epilogue_backward(dout_bf16, pre_bf16, activation, rows, n, dz_bf16, q_e4m3,
+                                                     scales, dbias, accumulate != 0, (float*)workspace,
+                                                     (hipStream_t)stream));
+}
+
 int64_t fp8bs_grad_norm_workspace(int32_t n) { return fp8bs::grad_norm_workspace(n > 0 ? n : 0); }
 
 fp8bs_status fp8bs_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* types, int32_t n,

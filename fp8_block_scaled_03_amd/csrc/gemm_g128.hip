@@ -26,8 +26,10 @@
 // (l & 15) of the 16-row operand, bytes 0-15 = K [16g, 16g+16) and bytes
 // 16-31 = K [64+16g, 64+16g+16).  The first operand is the weight, so a lane's
 // four results are four columns of one row of C.
+#include "activation.hpp"
 #include "common.hpp"
 #include "launch_g128.hpp"
+#include "launch_layer.hpp"
 #include "ragged.hpp"
 
 #include <algorithm>
@@ -140,6 +142,157 @@ __device__ __forceinline__ void store_wave_rows(uint16_t* c, int64_t N, const v4
   }
 }
 
+// ---- epilogue: z = acc + bias, C = act(z) + residual, pre = z (include/fp8bs_layer.h), in
+// the accumulators' layout: lane l holds row lo, columns 16j + 4g .. +3 of a row
+// sub-tile.  The residual is read, and results are written, as C is without an
+// epilogue (16 bytes a lane, whole lines where there are); the exchanges between
+// lanes that lead there are their own inverse.
+struct NoEpilogue {};
+
+enum ActivationCode { CODE_CLAMP, CODE_GATED, CODE_GELU };  // what the loops over a tile are compiled for
+
+// What does not depend on the element: none and relu are max(z, low) with low = -inf and 0
+// (a NaN stays), gelu_tanh and silu z sigma(z (c0 + c1 z^2)).
+template <int CODE>
+struct Activate {
+  float low, c0, c1;
+  __device__ __forceinline__ explicit Activate(int act)
+      : low(act == ACT_RELU ? 0.0f : -__builtin_inff()),
+        c0(act == ACT_SILU ? 1.0f : GT_C0),
+        c1(act == ACT_SILU ? 0.0f : GT_C1) {}
+  __device__ __forceinline__ float operator()(float z) const {
+    if constexpr (CODE == CODE_CLAMP) return z < low ? low : z;
+    // (an infinite square times silu's c1 = 0 would be a NaN)
+    if constexpr (CODE == CODE_GATED) return gated(z, z * __builtin_fmaf(c1, fminf(z * z, 0x1p100f), c0));
+    return gelu(z);
+  }
+};
+
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F&& f) {
+  if (act == ACT_GELU) f(Activate<CODE_GELU>(act));
+  else if (act == ACT_GELU_TANH || act == ACT_SILU) f(Activate<CODE_GATED>(act));
+  else f(Activate<CODE_CLAMP>(act));
+}
+
+__device__ __forceinline__ v4f add_bf16x4(v4f v, uint32_t lo, uint32_t hi) {
+  return v4f{v[0] + bf16_lo(lo), v[1] + bf16_hi(lo), v[2] + bf16_lo(hi), v[3] + bf16_hi(hi)};
+}
+// The inverse of bf16_octet's exchange, added to both accumulators.
+__device__ __forceinline__ void add_octet(v4f& x, v4f& y, uint4 v) {
+  const auto lo = __builtin_amdgcn_permlane16_swap(v.x, v.z, false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(v.y, v.w, false, false);
+  x = add_bf16x4(x, lo[0], hi[0]);
+  y = add_bf16x4(y, lo[1], hi[1]);
+}
+
+// Row sub-tile at row `r0`, column `c0` of the tile at offset `at` of C, the residual and pre.
+// ROWS: as store_wave_rows (NJ = 4), else as store_wave.
+template <int NJ, bool ROWS>
+struct EpilogueRow {
+  uint4 res[NJ / 2 > 0 ? NJ / 2 : 1];
+
+  __device__ __forceinline__ static int64_t place(int part, int64_t N, int r0, int c0, int& r, int& col) {
+    const int ln = fresh_lane(), g = ln >> 4, lo = ln & 15;
+    if constexpr (ROWS) {
+      r = r0 + (lo & 7) + 8 * part;
+      col = c0 + 16 * (g & 1) + 4 * (g & 2) + (lo < 8 ? 0 : 32);
+    } else if constexpr (NJ % 2 == 0) {
+      r = r0 + lo;
+      col = c0 + 16 * (2 * part + (g & 1)) + 4 * (g & 2);
+    } else {
+      r = r0 + lo;
+      col = c0 + 4 * g;
+    }
+    return r * N + col;
+  }
+  static constexpr int PARTS = NJ % 2 == 0 ? NJ / 2 : 1;
+
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t N, int r0, int c0, int m_valid, int n_valid) {
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) {
+      int r, col;
+      const int64_t off = place(k, N, r0, c0, r, col);
+      res[k] = make_uint4(0, 0, 0, 0);
+      if (r < m_valid && col < n_valid) {
+        if constexpr (NJ % 2 == 0) {
+          res[k] = *reinterpret_cast<const uint4*>(p + off);
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(p + off);
+          res[k].x = v.x;
+          res[k].y = v.y;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ static uint32_t ror8(uint32_t x) {
+    return __builtin_amdgcn_update_dpp(0, x, 0x128, 0xF, 0xF, true);
+  }
+  __device__ __forceinline__ void add(v4f (&acc)[NJ]) const {
+    if constexpr (ROWS) {
+      const bool low = (fresh_lane() & 15) < 8;
+      auto side = [&](uint32_t a, uint32_t b) __attribute__((always_inline)) { return ror8(low ? b : a); };
+      const uint4 a = res[0], b = res[1];
+      const uint4 x = make_uint4(side(a.x, b.x), side(a.y, b.y), side(a.z, b.z), side(a.w, b.w));
+      add_octet(acc[0], acc[1], low ? a : x);
+      add_octet(acc[2], acc[3], low ? x : b);
+    } else if constexpr (NJ % 2 == 0) {
+#pragma unroll
+      for (int j = 0; j < NJ; j += 2) add_octet(acc[j], acc[j + 1], res[j / 2]);
+    } else {
+      acc[0] = add_bf16x4(acc[0], res[0].x, res[0].y);
+    }
+  }
+};
+
+template <int MI, int NJ>
+__device__ __forceinline__ void epilogue_wave(const Epilogue& e, uint16_t* c, int64_t at, int64_t N,
+                                              v4f (&acc)[MI][NJ], int64_t col0, int r0, int c0, int m_valid,
+                                              int n_valid) {
+  constexpr bool ROWS = NJ == 4;
+  const bool lines = ROWS && whole_lines(c, N);
+  static_assert(NJ == 1 || NJ % 2 == 0, "pairs of sub-tiles");
+  if (e.bias != nullptr) {
+    const int g = fresh_lane() >> 4;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int col = c0 + 16 * j + 4 * g;
+      uint2 b = make_uint2(0, 0);
+      if (col < n_valid) b = *reinterpret_cast<const uint2*>(e.bias + col0 + col);
+#pragma unroll
+      for (int i = 0; i < MI; ++i) acc[i][j] = add_bf16x4(acc[i][j], b.x, b.y);
+    }
+  }
+  auto store = [&](uint16_t* p, const v4f (&v)[1][NJ], int r) __attribute__((always_inline)) {
+    if constexpr (ROWS) {
+      if (lines) store_wave_rows<true, 1>(p, N, v, r, c0, m_valid, n_valid);
+      else store_wave_rows<false, 1>(p, N, v, r, c0, m_valid, n_valid);
+    } else {
+      store_wave<1, NJ>(p, N, v, r, c0, m_valid, n_valid);
+    }
+  };
+  with_activation(e.act, [&](auto activate) __attribute__((always_inline)) {
+    EpilogueRow<NJ, ROWS> next;
+    if (e.residual != nullptr) next.load(e.residual + at, N, r0, c0, m_valid, n_valid);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const EpilogueRow<NJ, ROWS> now = next;
+      if (e.residual != nullptr && i + 1 < MI) next.load(e.residual + at, N, r0 + 16 * (i + 1), c0, m_valid, n_valid);
+      v4f v[1][NJ];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) v[0][j] = acc[i][j];
+      if (e.pre != nullptr) store(e.pre + at, v, r0 + 16 * i);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[0][j][k] = activate(v[0][j][k]);
+      if (e.residual != nullptr) now.add(v[0]);
+      store(c + at, v, r0 + 16 * i);
+      __builtin_amdgcn_sched_barrier(0);  // one row sub-tile's values at a time
+    }
+  });
+}
+
 // ---- small and middle tiles: BM = 16*MI*WM rows by BN = 16*NJ*WN columns per
 // workgroup of WM x WN waves; wave (wm, wn) owns MI x NJ sub-tiles of 16x16.
 //
@@ -151,11 +304,11 @@ __device__ __forceinline__ void store_wave_rows(uint16_t* c, int64_t N, const v4
 // one value per wave and step, held by lane l for step 64c + l.  A wave's MFMAs,
 // promotions and fragment reads are in the large tile's order (below); left to the
 // compiler's order 512 x 8192 x 8192 took 7% longer.
-template <int MI, int NJ, int WM, int WN, int S, bool GROUPED>
+template <int MI, int NJ, int WM, int WN, int S, bool GROUPED, typename E>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
     const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
-    int64_t N, int64_t K, uint32_t tiles_n) {
+    int64_t N, int64_t K, uint32_t tiles_n, E epilogue) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN, WAVES = WM * WN;
   constexpr int STAGE = (BM + BN) * GK;
   constexpr int PIECES = (BM + BN) / 8 / WAVES;            // 1 KB loads per wave and step
@@ -378,6 +531,12 @@ __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
   }
 
   if (!wave_live) return;
+  if constexpr (!std::is_same_v<E, NoEpilogue>) {
+    const int64_t at = row0 * N + col0;
+    const int r0 = wm * 16 * MI, c0 = wn * 16 * NJ;
+    epilogue_wave(epilogue, c, at, N, acc, col0, r0, c0, m_valid, n_valid);
+    return;
+  }
   uint16_t* const ct = c + row0 * N + col0;
   if constexpr (NJ == 4) {
     if (whole_lines(c, N)) {
@@ -420,11 +579,11 @@ constexpr int X_SLOT = XBM * GK;
 constexpr int X_SSUB = 768, X_SBUF = XBM / 16 * X_SSUB;
 constexpr int X_LDS = X_S + 2 * X_SBUF;
 
-template <bool GROUPED>
+template <bool GROUPED, typename E>
 __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
     const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
-    int64_t N, int64_t K, uint32_t tiles_n, uint32_t tiles) {
+    int64_t N, int64_t K, uint32_t tiles_n, uint32_t tiles, E epilogue) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
   typedef __attribute__((address_space(3))) const v4i lds_v4i;
@@ -608,7 +767,8 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
   if (KB > 0) first_loads();
 #pragma unroll 1
   for (;;) {
-    uint16_t* const ct = c + t.row0 * N + (int64_t)t.tn * XBN;
+    const int64_t at_here = t.row0 * N + (int64_t)t.tn * XBN, col0_here = (int64_t)t.tn * XBN;
+    uint16_t* const ct = c + at_here;
     const int m_here = m_valid, n_here = n_valid;
     const bool wave_live = wm * 128 < m_here && wn * 64 < n_here;
     id += gridDim.x;
@@ -712,7 +872,9 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     } else if (more) {
       begin_tile();
     }
-    if (wave_live) {
+    if constexpr (!std::is_same_v<E, NoEpilogue>) {
+      if (wave_live) epilogue_wave(epilogue, c, at_here, N, acc, col0_here, wm * 128, wn * 64, m_here, n_here);
+    } else if (wave_live) {
       if (lines) store_wave_rows<true>(ct, N, acc, wm * 128, wn * 64, m_here, n_here);
       else store_wave_rows<false>(ct, N, acc, wm * 128, wn * 64, m_here, n_here);
     }
@@ -721,7 +883,7 @@ __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
 }
 
 static hipError_t launch_big(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
-                             int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+                             int G, void* c, int64_t M, int64_t N, int64_t K, const Epilogue* e, hipStream_t stream) {
   const int64_t tiles_n = (N + XBN - 1) / XBN;
   // each range adds at most one partial tile
   const int64_t tiles_m = offsets ? (M + XBM - 1) / XBM + (G < M ? G : M) : (M + XBM - 1) / XBM;
@@ -729,12 +891,13 @@ static hipError_t launch_big(const void* a, const float* sa, const void* bt, con
   if (tiles > 0x7FFFFFFF) return hipErrorNotSupported;
   // one workgroup per CU (their LDS allows no second one)
   const dim3 grid((unsigned)(tiles < 256 ? tiles : 256));
-  if (offsets)
-    hipLaunchKernelGGL(gemm_g128_big_kernel<true>, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa,
-                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n, (uint32_t)tiles);
-  else
-    hipLaunchKernelGGL(gemm_g128_big_kernel<false>, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa,
-                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n, (uint32_t)tiles);
+  auto launch = [&](auto kernel, auto epilogue) {
+    hipLaunchKernelGGL(kernel, grid, dim3(XTHREADS), X_LDS, stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt,
+                       offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n, (uint32_t)tiles, epilogue);
+  };
+  if (e) launch(gemm_g128_big_kernel<false, Epilogue>, *e);
+  else if (offsets) launch(gemm_g128_big_kernel<true, NoEpilogue>, NoEpilogue());
+  else launch(gemm_g128_big_kernel<false, NoEpilogue>, NoEpilogue());
   return hipGetLastError();
 }
 
@@ -743,33 +906,36 @@ constexpr int tile_lds() {
   return S * (16 * MI * WM + 16 * NJ * WN) * GK + 2 * MI * WM * 576;
 }
 
+static hipError_t allow_lds(const void* kernel, int bytes) {
+  return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <int MI, int NJ, int WM, int WN, int S>
 static hipError_t set_tile_attributes() {
-  hipError_t e = hipFuncSetAttribute((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds<MI, NJ, WM, WN, S>());
-  if (e != hipSuccess) return e;
-  return hipFuncSetAttribute((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, true>,
-                             hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds<MI, NJ, WM, WN, S>());
+  constexpr int LDS = tile_lds<MI, NJ, WM, WN, S>();
+  hipError_t e = allow_lds((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false, NoEpilogue>, LDS);
+  if (e == hipSuccess) e = allow_lds((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, true, NoEpilogue>, LDS);
+  if (e == hipSuccess) e = allow_lds((const void*)gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false, Epilogue>, LDS);
+  return e;
 }
 
 template <int MI, int NJ, int WM, int WN, int S>
 static hipError_t launch_tile(const void* a, const float* sa, const void* bt, const float* sbt,
                               const int32_t* offsets, int G, void* c, int64_t M, int64_t N, int64_t K,
-                              hipStream_t stream) {
+                              const Epilogue* e, hipStream_t stream) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN, THREADS = 64 * WM * WN;
   const int64_t tiles_n = (N + BN - 1) / BN;
   // each range adds at most one partial tile
   const int64_t tiles_m = offsets ? (M + BM - 1) / BM + (G < M ? G : M) : (M + BM - 1) / BM;
   if (tiles_m * tiles_n > (int64_t)0xFFFFFFFF / THREADS) return hipErrorNotSupported;
   const dim3 grid((unsigned)(tiles_m * tiles_n));
-  if (offsets)
-    hipLaunchKernelGGL((gemm_g128_tile_kernel<MI, NJ, WM, WN, S, true>), grid, dim3(THREADS),
-                       (tile_lds<MI, NJ, WM, WN, S>()), stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt,
-                       offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
-  else
-    hipLaunchKernelGGL((gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false>), grid, dim3(THREADS),
-                       (tile_lds<MI, NJ, WM, WN, S>()), stream, (const uint8_t*)a, sa, (const uint8_t*)bt, sbt,
-                       offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n);
+  auto launch = [&](auto kernel, auto epilogue) {
+    hipLaunchKernelGGL(kernel, grid, dim3(THREADS), (tile_lds<MI, NJ, WM, WN, S>()), stream, (const uint8_t*)a, sa,
+                       (const uint8_t*)bt, sbt, offsets, G, (uint16_t*)c, M, N, K, (uint32_t)tiles_n, epilogue);
+  };
+  if (e) launch(gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false, Epilogue>, *e);
+  else if (offsets) launch(gemm_g128_tile_kernel<MI, NJ, WM, WN, S, true, NoEpilogue>, NoEpilogue());
+  else launch(gemm_g128_tile_kernel<MI, NJ, WM, WN, S, false, NoEpilogue>, NoEpilogue());
   return hipGetLastError();
 }
 
@@ -785,12 +951,13 @@ static hipError_t launch_tile(const void* a, const float* sa, const void* bt, co
 // loads are issued before the round's products are formed.
 constexpr int RU = 2, RKC = 4 * RU;  // K-blocks of a wave and of a round
 
+template <typename E>
 __global__ void __launch_bounds__(256) gemm_g128_rows_kernel(const uint8_t* __restrict__ a,
                                                              const float* __restrict__ sa,
                                                              const uint8_t* __restrict__ bt,
                                                              const float* __restrict__ sbt,
                                                              uint16_t* __restrict__ c, int64_t M, int64_t N,
-                                                             int64_t K) {
+                                                             int64_t K, E epilogue) {
   __shared__ __attribute__((aligned(16))) float part[2][RKC][256];
   __shared__ float sprod[2][RKC][16];
   const int lane = threadIdx.x & 63;
@@ -883,15 +1050,22 @@ __global__ void __launch_bounds__(256) gemm_g128_rows_kernel(const uint8_t* __re
       chain(r + 1);
     }
   }
-  if (row < M) c[row * N + n0 + col] = (uint16_t)bf16_pair(acc, 0.0f);
+  if (row >= M) return;
+  const int64_t at = row * N + n0 + col;
+  if constexpr (!std::is_same_v<E, NoEpilogue>) {
+    auto value = [](const uint16_t* p) __attribute__((always_inline)) { return bf16_lo(*p); };
+    if (epilogue.bias != nullptr) acc += value(epilogue.bias + n0 + col);
+    if (epilogue.pre != nullptr) epilogue.pre[at] = (uint16_t)bf16_pair(acc, 0.0f);
+    with_activation(epilogue.act, [&](auto activate) __attribute__((always_inline)) { acc = activate(acc); });
+    if (epilogue.residual != nullptr) acc += value(epilogue.residual + at);
+  }
+  c[at] = (uint16_t)bf16_pair(acc, 0.0f);
 }
 
 hipError_t set_gemm_g128_attributes() {
-  hipError_t e = hipFuncSetAttribute((const void*)gemm_g128_big_kernel<false>,
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, X_LDS);
-  if (e == hipSuccess)
-    e = hipFuncSetAttribute((const void*)gemm_g128_big_kernel<true>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                            X_LDS);
+  hipError_t e = allow_lds((const void*)gemm_g128_big_kernel<false, NoEpilogue>, X_LDS);
+  if (e == hipSuccess) e = allow_lds((const void*)gemm_g128_big_kernel<true, NoEpilogue>, X_LDS);
+  if (e == hipSuccess) e = allow_lds((const void*)gemm_g128_big_kernel<false, Epilogue>, X_LDS);
   if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 4, 3>();
   if (e == hipSuccess) e = set_tile_attributes<4, 4, 2, 2, 2>();
   if (e == hipSuccess) e = set_tile_attributes<2, 4, 4, 2, 3>();
@@ -933,8 +1107,8 @@ hipError_t set_gemm_g128_attributes() {
 // rows the choice is 1.5% and 3% slower than the best of these tiles on average; what
 // none of them reaches this does not see (32 x 576 x 7168 is 18 workgroups of 56
 // K-blocks one after another: 13.7 us).
-hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
-                            int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+static hipError_t launch(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
+                         int G, void* c, int64_t M, int64_t N, int64_t K, const Epilogue* e, hipStream_t stream) {
   const int64_t live = G < M ? G : M;           // ranges that can have rows
   const int64_t avg = (M + live - 1) / live;    // rows of one
   auto tiles = [&](int64_t bm, int64_t bn) {
@@ -942,30 +1116,45 @@ hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, cons
     return rows * ((N + bn - 1) / bn);
   };
   if (!offsets && K > 0 && M <= 16 && tiles(32, 32) < 200) {
-    hipLaunchKernelGGL(gemm_g128_rows_kernel, dim3((unsigned)(N / 16)), dim3(256), 0, stream, (const uint8_t*)a, sa,
-                       (const uint8_t*)bt, sbt, (uint16_t*)c, M, N, K);
+    auto rows = [&](auto kernel, auto epilogue) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(N / 16)), dim3(256), 0, stream, (const uint8_t*)a, sa,
+                         (const uint8_t*)bt, sbt, (uint16_t*)c, M, N, K, epilogue);
+    };
+    if (e) rows(gemm_g128_rows_kernel<Epilogue>, *e);
+    else rows(gemm_g128_rows_kernel<NoEpilogue>, NoEpilogue());
     return hipGetLastError();
   }
   const int64_t big = tiles(256, 256), wide = tiles(128, 256), square = tiles(128, 128), low = tiles(64, 128);
   const int64_t small = tiles(64, 64);
   if (avg >= (offsets ? 112 : 160) && big >= 160)
-    return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_big(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (avg >= (offsets ? 48 : 65) && wide >= 150 && wide <= 256)
-    return launch_tile<4, 4, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<4, 4, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (avg > 64 && square >= 200 && square <= 256)
-    return launch_tile<2, 4, 4, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<2, 4, 4, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (avg >= 128 && square > 256)
-    return launch_tile<4, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<4, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (!offsets && M <= 64 && small > 256)
-    return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (avg >= 20 && low > 256)
-    return launch_tile<2, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<2, 4, 2, 2, 2>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (avg >= 20 && low > 128)
-    return launch_tile<2, 2, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<2, 2, 2, 4, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
   if (avg > 32 && small > 128 && small <= 256)
-    return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  if (tiles(32, 64) >= 150) return launch_tile<1, 2, 2, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
-  return launch_tile<1, 1, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, stream);
+    return launch_tile<2, 2, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
+  if (tiles(32, 64) >= 150) return launch_tile<1, 2, 2, 2, 3>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
+  return launch_tile<1, 1, 2, 2, 4>(a, sa, bt, sbt, offsets, G, c, M, N, K, e, stream);
+}
+
+hipError_t launch_gemm_g128(const void* a, const float* sa, const void* bt, const float* sbt, const int32_t* offsets,
+                            int G, void* c, int64_t M, int64_t N, int64_t K, hipStream_t stream) {
+  return launch(a, sa, bt, sbt, offsets, G, c, M, N, K, nullptr, stream);
+}
+
+hipError_t launch_gemm_g128_epilogue(const void* a, const float* sa, const void* bt, const float* sbt,
+                                     const Epilogue& e, void* c, int64_t M, int64_t N, int64_t K,
+                                     hipStream_t stream) {
+  return launch(a, sa, bt, sbt, nullptr, 1, c, M, N, K, &e, stream);
 }
 
 }  // namespace fp8bs

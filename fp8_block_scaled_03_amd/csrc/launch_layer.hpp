@@ -4,6 +4,21 @@
 #include <stdint.h>
 
 namespace fp8bs {
+// What a product's epilogue does: z = acc + bias, C = act(z) + residual, pre = z; any of the
+// pointers may be null.
+struct Epilogue {
+  const uint16_t *bias, *residual;
+  uint16_t* pre;
+  int act;  // an Activation
+};
+hipError_t launch_gemm_g128_epilogue(const void* a, const float* sa, const void* bt, const float* sbt,
+                                     const Epilogue& e, void* c, int64_t M, int64_t N, int64_t K,
+                                     hipStream_t stream);
+int64_t epilogue_backward_workspace(int64_t rows, int64_t n);
+// z may be null with ACT_NONE; dz and dbias (and then workspace) may be null
+hipError_t launch_epilogue_backward(const void* dout, const void* z, int act, int64_t rows, int64_t n, void* dz,
+                                    void* q, float* scales, float* dbias, bool accumulate, float* workspace,
+                                    hipStream_t stream);
 // q and scales, y, h, residual, beta, mean and rstd may be null
 hipError_t launch_layernorm(const void* x, const void* residual, const void* gamma, const void* beta, float eps,
                             int64_t rows, int64_t d, void* h, void* q, float* scales, void* y, float* mean,

@@ -3,47 +3,19 @@
 //   sigma = 1 / (1 + exp(-g)),  y = g sigma u
 //   dg = dy u sigma (1 + g (1 - sigma)) = dy u (sigma + g sigma (1 - sigma)),
 //   du = dy g sigma
-// in fp32 from bf16 inputs; the codes are taken from the fp32 values.  With
-// e = exp(-|g|) <= 1 the two sigmoids sigma(|g|) = 1 / (1 + e) and sigma(-|g|) =
-// e / (1 + e) never overflow and 1 - sigma loses nothing.  The exponent is split
-// into a whole number and a rest of at most 1/2, whose exp2 the hardware takes (a
-// rest taken from the rounded exponent costs a far gate more bits the farther it
-// lies: 46 x 2^-24 at -60); the reciprocal is the hardware's with one Newton step.
-// With one ulp for exp2 sigma(-|g|) is within 2.9 ulp for every gate (where its fp32
-// value is not subnormal), and y / 448 was within 3.9 x 2^-24 for every bf16 gate
+// in fp32 from bf16 inputs; the codes are taken from the fp32 values.  sigma is
+// activation.hpp's, and y / 448 was within 3.9 x 2^-24 for every bf16 gate
 // of [2^-7, 80] and either sign: an error there moves the scale of a whole group
 // and the codes next to a border.
 //
 // Bound by HBM traffic: 5 bytes per value forward, 12 backward (14 with y).
 // Mapping as in quantize_g128.hip: 16 lanes hold a group's 128 columns of one
 // row, eight each.
+#include "activation.hpp"
 #include "launch_g128.hpp"
 #include "quant_g128.hpp"
 
 namespace fp8bs {
-
-struct Sigmoid {
-  float s, c;  // sigma(g) and 1 - sigma(g) = sigma(-g)
-};
-
-__device__ __forceinline__ Sigmoid sigmoid(float g) {
-  constexpr float L_HI = 1.44269502162933349609375f;   // log2(e) rounded to fp32
-  constexpr float L_LO = 1.92596299112661746887e-8f;   // the rest
-  constexpr float ROUND = 0x1.8p23f;                   // adding it rounds to a whole number, which the low bits hold
-  const float a = fminf(__builtin_fabsf(g), 128.0f);   // exp(-128) is below every fp32 value
-  const float t = __builtin_fmaf(a, L_HI, ROUND);
-  const float n = t - ROUND;
-  // n - a log2(e): the first product and sum lose nothing of a far gate
-  const float rest = __builtin_fmaf(-a, L_LO, __builtin_fmaf(-a, L_HI, n));
-  // 2^24 e, the factor so that a subnormal e keeps its bits until sigma is rounded
-  const int up = 24 + __builtin_bit_cast(int, ROUND) - __builtin_bit_cast(int, t);
-  const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), up);
-  const float b = __builtin_fmaf(e, 0x1p-24f, 1.0f);  // in [1, 2]
-  const float r = __builtin_amdgcn_rcpf(b);
-  const float large = __builtin_fmaf(__builtin_fmaf(-b, r, 1.0f), r, r);
-  const float small = e * large * 0x1p-24f;
-  return g >= 0.0f ? Sigmoid{large, small} : Sigmoid{small, large};
-}
 
 // A region is 4 rows x 512 columns of y; a wave takes 128 columns (a group) of the
 // four rows.  (Two or four such loads per lane are slower: 8192 x 2048 forward

@@ -1,7 +1,8 @@
 /*
  * fp8bs_layer.h - the entry points of libfp8bs.so that stand between the products
- * of a transformer block: layer norm with its backward pass, gradient norms and
- * clipping.
+ * of a transformer block: layer norm with its backward pass, products with bias,
+ * activation and residual in their epilogue and its backward pass, gradient norms
+ * and clipping.
  * Status codes, pointer ownership, streams and errors are those of fp8bs.h; the
  * E4M3 format and the quantizer's rule for 128 values are those of fp8bs_g128.h.
  *
@@ -71,6 +72,52 @@ fp8bs_status fp8bs_layernorm_backward(const void* dy_bf16, const void* h_bf16, c
                                       const float* mean, const float* rstd, const void* dresidual_bf16, int64_t rows,
                                       int64_t d, void* dx_bf16, float* dgamma, float* dbeta, int32_t accumulate,
                                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Activations of an epilogue. */
+#define FP8BS_ACT_NONE 0
+#define FP8BS_ACT_RELU 1
+#define FP8BS_ACT_GELU 2      /* z Phi(z), Phi the normal distribution's function  */
+#define FP8BS_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2   */
+#define FP8BS_ACT_SILU 4      /* z / (1 + exp(-z))                                 */
+
+/*
+ * fp8bs_gemm_tg128_nt_epilogue - fp8bs_gemm_tg128_nt with an epilogue on its fp32
+ *   accumulators, before the one rounding of the result:
+ *     z = A Bt' + bias,  c = bf16(act(z) + residual),  pre = bf16(z)
+ *   a, sa, bt, sbt, M, N, K as for fp8bs_gemm_tg128_nt; K == 0: the product is 0
+ *   bias [N] bf16 or NULL, activation one of FP8BS_ACT_* (else FP8BS_EINVAL)
+ *   residual [M, N] bf16 or NULL; may be c itself (in place)
+ *   c [M, N] bf16 out; pre [M, N] bf16 out or NULL, apart from the other arguments
+ *   The activation is fp32 arithmetic, off by at most 2^-15 of its result, whose
+ *   magnitudes below 2^-118 may come out as 0; an exact zero is stored as +0.
+ *   Results are batch invariant as fp8bs_gemm_tg128_nt's.
+ */
+fp8bs_status fp8bs_gemm_tg128_nt_epilogue(const void* a, const float* sa, const void* bt, const float* sbt,
+                                          const void* bias_bf16, int32_t activation, const void* residual_bf16,
+                                          void* c_bf16, void* pre_bf16, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * fp8bs_epilogue_backward_quantize_tg128 - the gradient of act(z) + residual with
+ *   respect to z (the residual's is dout itself), with the quantizer that the input
+ *   gradient's product needs and the gradient of the bias:
+ *     dz     = dout * act'(pre)  (fp32), rounded to bf16 (for the weight gradient)
+ *     q, scales = the row quantizer's rule of fp8bs_g128.h on the fp32 dz
+ *     dbias  = sum over the rows of the fp32 dz
+ *   relu's derivative at 0 is 0.
+ *   dout [rows, n] bf16, pre [rows, n] bf16 (the forward call's; with FP8BS_ACT_NONE
+ *   it is not read and may be NULL), dz [rows, n] bf16 out or NULL, q [rows, n] E4M3
+ *   out, scales [rows, ceil128(n)] fp32 out
+ *   dbias [n] fp32 out or NULL; if accumulate != 0 the sums are added to what it holds.
+ *      rows == 0: zeros (or nothing is added).
+ *   workspace of fp8bs_epilogue_backward_workspace(rows, n) bytes (else
+ *   FP8BS_EINVAL); not used without dbias.
+ *   n % 16 == 0, rows and n at most 2^30 (else FP8BS_ESHAPE); n == 0: no-op.
+ */
+int64_t fp8bs_epilogue_backward_workspace(int64_t rows, int64_t n);
+fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const void* pre_bf16, int32_t activation,
+                                                    int64_t rows, int64_t n, void* dz_bf16, void* q_e4m3,
+                                                    float* scales, float* dbias, int32_t accumulate, void* workspace,
+                                                    int64_t workspace_bytes, void* stream);
 
 /* Types of a gradient. */
 #define FP8BS_F32 0

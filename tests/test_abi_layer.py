@@ -83,6 +83,48 @@ def test_layernorm_backward_refusals():
         assert with_(**{f"_{i}": A4 + 2}) == EALIGN
 
 
+def _changed(call, ok):
+    def with_(**at):
+        p = list(ok)
+        for i, v in at.items():
+            p[int(i[1:])] = v
+        return call(*p)
+    return with_
+
+
+def test_epilogue_refusals():
+    with_ = _changed(binding.gemm_tg128_nt_epilogue_raw, [A16, A4, A16, A4, A16, 2, A16, A16, A16, 4, 64, 64])
+    assert with_(_9=0) == OK and with_(_10=0) == OK and with_(_9=0, _0=None, _7=None) == OK
+    assert with_(_5=-1) == EINVAL and with_(_5=5) == EINVAL
+    assert with_(_9=-1) == EINVAL and with_(_10=40) == ESHAPE and with_(_11=40) == ESHAPE
+    assert with_(_9=BIG + 1) == ESHAPE and with_(_11=(1 << 22) + 16) == ESHAPE
+    for i in (0, 1, 2, 3, 7):
+        assert with_(**{f"_{i}": None}) == EINVAL
+    for i in (0, 2, 4, 6, 7, 8):
+        assert with_(**{f"_{i}": A16 + 8}) == EALIGN
+    for i in (1, 3):
+        assert with_(**{f"_{i}": A4 + 2}) == EALIGN
+
+
+def test_epilogue_backward_refusals():
+    lib = binding.load_library()
+    size = lib.fp8bs_epilogue_backward_workspace(4, 64)
+    assert size >= 256 and lib.fp8bs_epilogue_backward_workspace(0, 64) == 0
+    assert lib.fp8bs_epilogue_backward_workspace(4, -16) == 0
+    with_ = _changed(binding.epilogue_backward_quantize_tg128_raw,
+                     [A16, A16, 2, 4, 64, A16, A16, A4, A4, 0, A16, size])
+    assert with_(_4=0) == OK
+    assert with_(_2=-1) == EINVAL and with_(_2=5) == EINVAL and with_(_3=-1) == EINVAL and with_(_4=-16) == EINVAL
+    assert with_(_4=24) == ESHAPE and with_(_3=BIG + 1) == ESHAPE and with_(_4=BIG + 16) == ESHAPE
+    for i in (0, 1, 6, 7, 10):
+        assert with_(**{f"_{i}": None}) == EINVAL
+    assert with_(_11=size - 1) == EINVAL
+    for i in (0, 1, 5, 6, 10):
+        assert with_(**{f"_{i}": A16 + 8}) == EALIGN
+    for i in (7, 8):
+        assert with_(**{f"_{i}": A4 + 2}) == EALIGN
+
+
 # ---- gradients ---------------------------------------------------------------------------
 def _arrays(pointers, counts, types):
     n = len(pointers)

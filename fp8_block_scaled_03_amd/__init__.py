@@ -19,6 +19,7 @@ _BINDING_NAMES = ("Fp8bsError", "quantize", "gemm", "grouped_gemm", "gemm_nt", "
                   "layernorm_raw", "layernorm_backward_raw",
                   "ACTIVATIONS", "gemm_tg128_nt_epilogue", "epilogue_backward_quantize_tg128",
                   "gemm_tg128_nt_epilogue_raw", "epilogue_backward_quantize_tg128_raw",
+                  "moe_decode_b128", "moe_decode_b128_raw",
                   "grad_norm", "clip_grads", "clip_grad_norm", "grad_norm_raw", "clip_grads_raw", "clip_grad_norm_raw")
 
 __all__ = list(_BINDING_NAMES)

@@ -95,6 +95,10 @@ def load_library() -> ctypes.CDLL:
         lib.fp8bs_epilogue_backward_workspace.restype = i64
         lib.fp8bs_epilogue_backward_quantize_tg128.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp]
         lib.fp8bs_epilogue_backward_quantize_tg128.restype = ctypes.c_int
+        lib.fp8bs_moe_decode_b128_workspace.argtypes = [i64, i64, i64, i64]
+        lib.fp8bs_moe_decode_b128_workspace.restype = i64
+        lib.fp8bs_moe_decode_b128.argtypes = [vp] * 9 + [i64] * 5 + [vp, i64, vp]
+        lib.fp8bs_moe_decode_b128.restype = ctypes.c_int
         lib.fp8bs_grad_norm_workspace.argtypes = [i32]
         lib.fp8bs_grad_norm_workspace.restype = i64
         lib.fp8bs_grad_norm.argtypes = [vp, vp, vp, i32, vp, vp, i64, vp]
@@ -249,6 +253,12 @@ def epilogue_backward_quantize_tg128_raw(dout_ptr, pre_ptr, activation, rows, n,
     return load_library().fp8bs_epilogue_backward_quantize_tg128(dout_ptr, pre_ptr, activation, rows, n, dz_ptr, q_ptr,
                                                                  s_ptr, dbias_ptr, accumulate, ws_ptr, ws_bytes,
                                                                  stream)
+
+
+def moe_decode_b128_raw(x_ptr, ids_ptr, weights_ptr, w1_ptr, s1_ptr, w2_ptr, s2_ptr, res_ptr, out_ptr, tokens, top,
+                        experts, hidden, inner, ws_ptr, ws_bytes, stream=None) -> int:
+    return load_library().fp8bs_moe_decode_b128(x_ptr, ids_ptr, weights_ptr, w1_ptr, s1_ptr, w2_ptr, s2_ptr, res_ptr,
+                                                out_ptr, tokens, top, experts, hidden, inner, ws_ptr, ws_bytes, stream)
 
 
 def grad_norm_raw(grads, counts, types, n, norm_ptr, ws_ptr, ws_bytes, stream=None) -> int:
@@ -845,6 +855,39 @@ def epilogue_backward_quantize_tg128(dout: torch.Tensor, pre: torch.Tensor | Non
     _call_on(dev, "fp8bs_epilogue_backward_quantize_tg128", dout.data_ptr(), _ptr(pre), code, R, N, dz.data_ptr(),
              q.data_ptr(), scales.data_ptr(), dbias.data_ptr(), 1 if accumulate else 0, ws.data_ptr(), size)
     return dz, q, scales, dbias
+
+
+def moe_decode_b128(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1: torch.Tensor, s1: torch.Tensor,
+                    w2: torch.Tensor, s2: torch.Tensor, residual: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None):
+    """A whole mixture-of-experts layer for a few tokens (tokens * choices <= 512): bf16 x [T, H], int32 ids [T, k],
+    fp32 weights [T, k], E4M3 w1 [E, 2I, H] (gates, then ups) and w2 [E, H, I] with the fp32 scales of their 128x128
+    blocks (quantize_b128) -> bf16 [T, H], the weighted sum over the choices of w2 (silu(gate) * up), plus
+    ``residual`` bf16 [T, H] if given (``out`` may be it).  Choices with an id outside [0, E) add nothing."""
+    _need(x, "x", _BF16, 2)
+    _need(w1, "w1", E4M3_DTYPES, 3)
+    _need(ids, "ids", _I32, 2)
+    T, H = x.shape
+    E, I2, _ = w1.shape
+    k, dev = ids.shape[1], x.device
+    if I2 % 2:
+        raise ValueError("w1 needs an even number of rows")
+    inner = I2 // 2
+    _need_size(w1, "w1", 2, H, dev)
+    _need_size(ids, "ids", 0, T, dev)
+    _need_like(weights, "weights", _F32, (T, k), dev)
+    _need_like(w2, "w2", E4M3_DTYPES, (E, H, inner), dev)
+    _need_like(s1, "s1", _F32, (E, _blocks128(I2), _blocks128(H)), dev)
+    _need_like(s2, "s2", _F32, (E, _blocks128(H), _blocks128(inner)), dev)
+    if residual is not None:
+        _need_like(residual, "residual", _BF16, (T, H), dev)
+    out = _output(out, "out", _BF16, (T, H), dev)
+    size = (_lib or load_library()).fp8bs_moe_decode_b128_workspace(T, k, E, inner)
+    ws = _workspace(size, dev)
+    _call_on(dev, "fp8bs_moe_decode_b128", x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w1.data_ptr(),
+             s1.data_ptr(), w2.data_ptr(), s2.data_ptr(), _ptr(residual), out.data_ptr(), T, k, E, H, inner,
+             ws.data_ptr(), size)
+    return out
 
 
 _GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}

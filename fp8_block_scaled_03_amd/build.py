@@ -24,7 +24,8 @@ LIB = os.path.join(PKG, "libfp8bs.so")
 
 SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "rmsnorm.hip", "gemm_e8m0.hip", "api_g128.cpp",
            "quantize_g128.hip", "gemm_g128.hip", "wgrad.hip", "swiglu.hip",
-           "api_layer.cpp", "gradnorm.hip", "layernorm.hip", "epilogue_backward.hip"]
+           "api_layer.cpp", "gradnorm.hip", "layernorm.hip", "epilogue_backward.hip",
+           "moe_decode.hip"]
 # measurement and test support (single instructions for the tests and the
 # bench), linked into a library of its own
 PROBE_SOURCES = ["probe.hip"]

@@ -33,6 +33,7 @@ fp8bs_status ensure_attributes() {
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
     if (fp8bs::set_layernorm_attributes() != hipSuccess) return FP8BS_EHIP;
+    if (fp8bs::set_moe_attributes() != hipSuccess) return FP8BS_EHIP;
     done[dev] = true;
   }
   return FP8BS_OK;
@@ -56,6 +57,17 @@ fp8bs_status check_layernorm(const void* x, const void* residual, const void* ga
   for (const void* p : {x, residual, gamma, beta, h, y})
     if (!aligned(p, 16)) return FP8BS_EALIGN;
   return aligned(mean, 4) && aligned(rstd, 4) ? FP8BS_OK : FP8BS_EALIGN;
+}
+
+constexpr int64_t MAX_MOE_DIM = 65536;
+
+fp8bs_status check_moe_sizes(int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inner) {
+  if (tokens < 0 || top < 1 || experts < 1 || experts > FP8BS_MAX_GROUPS || hidden < 0 || inner < 0)
+    return FP8BS_EINVAL;
+  if (top > FP8BS_MAX_MOE_CHOICES || tokens > FP8BS_MAX_MOE_CHOICES || tokens * top > FP8BS_MAX_MOE_CHOICES)
+    return FP8BS_ESHAPE;
+  if (hidden % 16 || hidden > MAX_MOE_DIM || inner % 16 || inner < 16 || inner > MAX_MOE_DIM) return FP8BS_ESHAPE;
+  return FP8BS_OK;
 }
 
 constexpr int64_t MAX_COUNT = int64_t(1) << 36;  // a launch's chunks of 32 KB stay below 2^31
@@ -192,6 +204,31 @@ fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const
   return from_launch(fp8bs::launch_epilogue_backward(dout_bf16, pre_bf16, activation, rows, n, dz_bf16, q_e4m3,
                                                      scales, dbias, accumulate != 0, (float*)workspace,
                                                      (hipStream_t)stream));
+}
+
+int64_t fp8bs_moe_decode_b128_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t inner) {
+  if (check_moe_sizes(tokens, top, experts, 0, inner) != FP8BS_OK || tokens == 0) return 0;
+  return fp8bs::moe_decode_workspace((int)tokens, (int)top, (int)experts, inner);
+}
+
+fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, const float* weights, const void* w1,
+                                   const float* s1, const void* w2, const float* s2, const void* residual_bf16,
+                                   void* out_bf16, int64_t tokens, int64_t top, int64_t experts, int64_t hidden,
+                                   int64_t inner, void* workspace, int64_t workspace_bytes, void* stream) {
+  fp8bs_status st = check_moe_sizes(tokens, top, experts, hidden, inner);
+  if (st != FP8BS_OK || tokens == 0 || hidden == 0) return st;
+  if (!x_bf16 || !ids_dev || !weights || !w1 || !s1 || !w2 || !s2 || !out_bf16) return FP8BS_EINVAL;
+  for (const void* p : {x_bf16, w1, w2, residual_bf16, (const void*)out_bf16})
+    if (!aligned(p, 16)) return FP8BS_EALIGN;
+  for (const void* p : {(const void*)ids_dev, (const void*)weights, (const void*)s1, (const void*)s2})
+    if (!aligned(p, 4)) return FP8BS_EALIGN;
+  st = check_workspace(workspace, workspace_bytes, fp8bs_moe_decode_b128_workspace(tokens, top, experts, inner));
+  if (st != FP8BS_OK) return st;
+  st = ensure_attributes();
+  if (st != FP8BS_OK) return st;
+  return from_launch(fp8bs::launch_moe_decode(x_bf16, ids_dev, weights, w1, s1, w2, s2, residual_bf16, out_bf16,
+                                              (int)tokens, (int)top, (int)experts, hidden, inner, workspace,
+                                              (hipStream_t)stream));
 }
 
 int64_t fp8bs_grad_norm_workspace(int32_t n) { return fp8bs::grad_norm_workspace(n > 0 ? n : 0); }

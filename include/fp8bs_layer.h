@@ -1,8 +1,8 @@
 /*
  * fp8bs_layer.h - the entry points of libfp8bs.so that stand between the products
  * of a transformer block: layer norm with its backward pass, products with bias,
- * activation and residual in their epilogue and its backward pass, gradient norms
- * and clipping.
+ * activation and residual in their epilogue and its backward pass, a whole
+ * mixture-of-experts layer for a few tokens, gradient norms and clipping.
  * Status codes, pointer ownership, streams and errors are those of fp8bs.h; the
  * E4M3 format and the quantizer's rule for 128 values are those of fp8bs_g128.h.
  *
@@ -118,6 +118,41 @@ fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const
                                                     int64_t rows, int64_t n, void* dz_bf16, void* q_e4m3,
                                                     float* scales, float* dbias, int32_t accumulate, void* workspace,
                                                     int64_t workspace_bytes, void* stream);
+
+/* Most choices (tokens * top) of fp8bs_moe_decode_b128. */
+#define FP8BS_MAX_MOE_CHOICES 512
+
+/*
+ * fp8bs_moe_decode_b128 - a whole mixture-of-experts layer for a few tokens: per
+ *   token t, with e = ids[t,j] for its choices j = 0 .. top-1,
+ *     [g | u] = W1[e] x[t],  y = silu(g) * u,
+ *     out[t]  = bf16(sum_j weights[t,j] * W2[e] y (+ residual[t]))
+ *   The weights are E4M3 codes with a scale per 128x128 block (fp8bs_quantize_b128);
+ *   x is bf16 and is not quantized, [g | u] is fp32 and y is held to 2^-17 of itself.
+ *   Products are exact, sums fp32; the choices are added in order.
+ *   x [tokens, hidden] bf16
+ *   ids [tokens, top] int32 on the device, read when the kernels run, so a captured graph
+ *      follows them.  A choice whose id is outside [0, experts) adds nothing
+ *      (an expert that another process holds, a token that pads a batch).  A
+ *      token may name an expert more than once.
+ *   weights [tokens, top] fp32; those of skipped choices are not used
+ *   w1 [experts, 2 inner, hidden] E4M3 (inner gates, then inner ups),
+ *   s1 [experts, ceil128(2 inner), ceil128(hidden)] fp32
+ *   w2 [experts, hidden, inner] E4M3, s2 [experts, ceil128(hidden), ceil128(inner)] fp32
+ *   residual [tokens, hidden] bf16 or NULL; may be out itself (in place)
+ *   out [tokens, hidden] bf16 out
+ *   1 <= top and 1 <= experts <= FP8BS_MAX_GROUPS (else FP8BS_EINVAL);
+ *   tokens * top <= FP8BS_MAX_MOE_CHOICES, hidden and inner multiples of 16, hidden <=
+ *   65536, 16 <= inner <= 65536 (else FP8BS_ESHAPE); tokens == 0 or hidden == 0: no-op.
+ *   workspace of fp8bs_moe_decode_b128_workspace(tokens, top, experts, inner) bytes
+ *   (else FP8BS_EINVAL).
+ *   Results are batch invariant: a token's depend on that token only.
+ */
+int64_t fp8bs_moe_decode_b128_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t inner);
+fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, const float* weights, const void* w1,
+                                   const float* s1, const void* w2, const float* s2, const void* residual_bf16,
+                                   void* out_bf16, int64_t tokens, int64_t top, int64_t experts, int64_t hidden,
+                                   int64_t inner, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Types of a gradient. */
 #define FP8BS_F32 0

@@ -1,5 +1,5 @@
 """The operators between the products (test oracle only), plain numpy in fp64: activations of an epilogue and their
-derivatives, layer norm and its gradients."""
+derivatives, layer norm and its gradients, an expert layer."""
 
 from __future__ import annotations
 
@@ -51,3 +51,23 @@ def layernorm_grad(dy, h, gamma, mean, rstd):
     g = dy * gamma
     dx = rstd * (g - g.mean(1, keepdims=True) - xh * (g * xh).mean(1, keepdims=True))
     return dx, dy * xh, dy
+
+
+def moe_layer(x, ids, weights, w1, w2):
+    """(out [T, H], bound-making magnitudes [T, H]) of sum_j weights[t,j] w2[e] (silu(g) u), [g | u] = w1[e] x[t];
+    w1 [E, 2I, H] and w2 [E, H, I] are the dequantized weights.  The second result is
+    sum_j |weights| |w2| (|y| + what y moves by for a relative error of 1 of every sum's magnitudes)."""
+    x = np.asarray(x, np.float64)
+    out, size = np.zeros_like(x), np.zeros_like(x)
+    for t in range(ids.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if not 0 <= e < w1.shape[0]:
+                continue
+            g, u = np.split(w1[e] @ x[t], 2)
+            ga, ua = np.split(np.abs(w1[e]) @ np.abs(x[t]), 2)
+            silu, slope, _ = activation_parts(g, "silu")
+            moved = np.abs(slope * u) * ga + np.abs(silu) * ua
+            out[t] += weights[t, j] * (w2[e] @ (silu * u))
+            size[t] += abs(weights[t, j]) * (np.abs(w2[e]) @ (np.abs(silu * u) + moved))
+    return out, size

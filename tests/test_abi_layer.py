@@ -125,6 +125,30 @@ def test_epilogue_backward_refusals():
         assert with_(**{f"_{i}": A4 + 2}) == EALIGN
 
 
+def test_moe_refusals():
+    lib = binding.load_library()
+    size = lib.fp8bs_moe_decode_b128_workspace(3, 2, 4, 64)
+    assert size > 0
+    for bad in ((-1, 2, 4, 64), (3, 0, 4, 64), (3, 2, 0, 64), (3, 2, 1025, 64), (3, 2, 4, 0), (3, 2, 4, 24),
+                (257, 2, 4, 64), (1 << 40, 1 << 40, 4, 64), (0, 2, 4, 64)):
+        assert lib.fp8bs_moe_decode_b128_workspace(*bad) == 0
+    ok = [A16, A4, A4, A16, A4, A16, A4, A16, A16, 3, 2, 4, 64, 64, A16, size]
+    with_ = _changed(binding.moe_decode_b128_raw, ok)
+    assert with_(_9=0) == OK and with_(_12=0) == OK
+    assert with_(_9=-1) == EINVAL and with_(_10=0) == EINVAL and with_(_11=0) == EINVAL and with_(_11=1025) == EINVAL
+    assert with_(_12=-16) == EINVAL and with_(_13=-16) == EINVAL
+    assert with_(_9=257) == ESHAPE and with_(_10=513) == ESHAPE and with_(_9=1 << 40, _10=1 << 40) == ESHAPE
+    assert with_(_12=40) == ESHAPE and with_(_13=40) == ESHAPE and with_(_13=0) == ESHAPE
+    assert with_(_12=65552) == ESHAPE and with_(_13=65552) == ESHAPE
+    for i in (0, 1, 2, 3, 4, 5, 6, 8, 14):
+        assert with_(**{f"_{i}": None}) == EINVAL
+    assert with_(_15=size - 1) == EINVAL
+    for i in (0, 3, 5, 7, 8, 14):
+        assert with_(**{f"_{i}": A16 + 8}) == EALIGN
+    for i in (1, 2, 4, 6):
+        assert with_(**{f"_{i}": A4 + 2}) == EALIGN
+
+
 # ---- gradients ---------------------------------------------------------------------------
 def _arrays(pointers, counts, types):
     n = len(pointers)

@@ -59,7 +59,7 @@ fp8bs_status check_layernorm(const void* x, const void* residual, const void* ga
   return aligned(mean, 4) && aligned(rstd, 4) ? FP8BS_OK : FP8BS_EALIGN;
 }
 
-constexpr int64_t MAX_MOE_DIM = 65536;
+constexpr int64_t MAX_MOE_DIM = 32768;
 
 fp8bs_status check_moe_sizes(int64_t tokens, int64_t top, int64_t experts, int64_t hidden, int64_t inner) {
   if (tokens < 0 || top < 1 || experts < 1 || experts > FP8BS_MAX_GROUPS || hidden < 0 || inner < 0)

@@ -33,6 +33,12 @@ constexpr int MOE_SLOTS = 512;     // most choices of a call
 constexpr int MOE_WAVES1 = 4, MOE_WAVES2 = 16;
 constexpr int MOE_CHUNKS = 4;      // most chunks of K in the second kernel
 
+// An expert with choices, as the first kernel leaves it for the second.
+struct Live {
+  int32_t expert, count, start;  // count 0: the candidate stands for none; its slots are list[start ..]
+  int32_t unused;
+};
+
 struct Moe {
   const uint16_t* x;
   const int32_t* ids;
@@ -46,10 +52,9 @@ struct Moe {
   int tokens, top, experts, hidden, inner;
   int slots, candidates;
   // workspace
-  int32_t* count;    // [candidates] slots of its expert, 0: it stands for none
-  int32_t* expert;   // [candidates]
-  uint16_t* list;    // [candidates, slots]
-  uint16_t *y_hi, *y_lo;  // [slots, inner]
+  Live* live;       // [candidates]
+  uint16_t* list;   // [slots], by expert
+  uint16_t* y;      // [2, slots, inner]: y rounded, and the rest rounded
 };
 
 __device__ __forceinline__ v4f mfma_bf16(v8bf w, v8bf x, v4f acc) {
@@ -57,7 +62,10 @@ __device__ __forceinline__ v4f mfma_bf16(v8bf w, v8bf x, v4f acc) {
 }
 
 // A lane's pieces of one K-block: 16 codes each of a weight row from 16g and 64 + 16g, and
-// for its column the values at the same K.
+// for its column the values at the same K.  Loads have no conditions, so that the
+// compiler can count them: pieces past K read the row's last whole one (values are then
+// replaced by zeros, in the last K-block only), columns without a slot read the
+// first one's and are not stored.
 struct Codes {
   v4i c[2];
 };
@@ -65,28 +73,31 @@ struct Values {
   v4i v[4];
 };
 
-__device__ __forceinline__ Codes load_codes(const uint8_t* row, int kb, int g, int last) {
+__device__ __forceinline__ Codes load_codes(const uint8_t* row, int kb, int g, int k) {
   int o0 = kb * 128 + 16 * g, o1 = o0 + 64;
-  o0 = o0 < last ? o0 : last;  // pieces past K read the last whole one; their values are zeros
-  o1 = o1 < last ? o1 : last;
+  o0 = o0 < k ? o0 : k - 16;
+  o1 = o1 < k ? o1 : k - 16;
   return {{*reinterpret_cast<const v4i*>(row + o0), *reinterpret_cast<const v4i*>(row + o1)}};
 }
-__device__ __forceinline__ Values load_values(const uint16_t* row, int kb, int g, int k, bool live) {
-  const v4i z = {0, 0, 0, 0};
-  const int o0 = kb * 128 + 16 * g, o1 = o0 + 64;
-  Values r = {{z, z, z, z}};
-  if (live && o0 < k) {
-    r.v[0] = *reinterpret_cast<const v4i*>(row + o0);
-    r.v[1] = *reinterpret_cast<const v4i*>(row + o0 + 8);
-  }
-  if (live && o1 < k) {
-    r.v[2] = *reinterpret_cast<const v4i*>(row + o1);
-    r.v[3] = *reinterpret_cast<const v4i*>(row + o1 + 8);
-  }
-  return r;
+__device__ __forceinline__ Values load_values(const uint16_t* row, int kb, int g, int k) {
+  int o0 = kb * 128 + 16 * g, o1 = o0 + 64;
+  o0 = o0 < k ? o0 : k - 16;
+  o1 = o1 < k ? o1 : k - 16;
+  const v4i *const a = reinterpret_cast<const v4i*>(row + o0), *const b = reinterpret_cast<const v4i*>(row + o1);
+  return {{a[0], a[1], b[0], b[1]}};
 }
-// P of one K-block for 16 weight rows x 16 columns.
-__device__ __forceinline__ v4f block_product(const Codes& c, const Values& x, v4f p) {
+__device__ __forceinline__ void clear_past(Values& x, int kb, int g, int k) {
+  if (kb * 128 + 128 <= k) return;
+  const v4i z = {0, 0, 0, 0};
+  const bool in0 = kb * 128 + 16 * g < k, in1 = kb * 128 + 64 + 16 * g < k;
+  x.v[0] = in0 ? x.v[0] : z;
+  x.v[1] = in0 ? x.v[1] : z;
+  x.v[2] = in1 ? x.v[2] : z;
+  x.v[3] = in1 ? x.v[3] : z;
+}
+// P of one K-block for 16 weight rows x 16 columns, for N sets of rows or of columns.
+__device__ __forceinline__ v4f block_product(const Codes& c, const Values& x) {
+  v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const v8bf lo = e4m3x8_to_bf16x8(v2i{c.c[h][0], c.c[h][1]}), hi = e4m3x8_to_bf16x8(v2i{c.c[h][2], c.c[h][3]});
@@ -95,79 +106,80 @@ __device__ __forceinline__ v4f block_product(const Codes& c, const Values& x, v4
   }
   return p;
 }
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
 
-// The expert that candidate `y` stands for, or -1, and its slots in order: their
-// number, and list[0 ..] for this wave.
-__device__ __forceinline__ int slots_of(const Moe& m, int y, int& count, uint16_t* list) {
+// What candidate `y` stands for; its slots in order at list[0 ..] for this wave.
+__device__ __forceinline__ Live slots_of(const Moe& m, int y, uint16_t* list) {
   const int lane = threadIdx.x & 63;
   const bool by_slot = m.slots < m.experts;
   const int e = by_slot ? m.ids[y] : y;
-  count = 0;
-  if (e < 0 || e >= m.experts) return -1;
+  Live r = {e, 0, 0, 0};
+  if (e < 0 || e >= m.experts) return r;
+  int id[MOE_SLOTS / 64];
+#pragma unroll
+  for (int i = 0; i < MOE_SLOTS / 64; ++i)
+    if (i * 64 < m.slots) id[i] = m.ids[i * 64 + lane < m.slots ? i * 64 + lane : m.slots - 1];
   int first = -1;
-  for (int base = 0; base < m.slots; base += 64) {
-    const int i = base + lane;
-    const uint64_t same = __ballot(i < m.slots && m.ids[i < m.slots ? i : 0] == e);
+#pragma unroll
+  for (int i = 0; i < MOE_SLOTS / 64; ++i) {
+    if (i * 64 >= m.slots) break;
+    const bool in = i * 64 + lane < m.slots;
+    const uint64_t same = __ballot(in && id[i] == e);
+    r.start += __popcll(__ballot(in && id[i] >= 0 && id[i] < e));
     if (same == 0) continue;
-    if (first < 0) first = base + __ffsll((unsigned long long)same) - 1;
-    const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
-    if ((same >> lane) & 1) list[count + before] = (uint16_t)i;
-    count += __popcll(same);
+    if (first < 0) first = i * 64 + __ffsll((unsigned long long)same) - 1;
+    if ((same >> lane) & 1)
+      list[r.count + __popcll(same & ((uint64_t(1) << lane) - 1))] = (uint16_t)(i * 64 + lane);
+    r.count += __popcll(same);
   }
   __builtin_amdgcn_wave_barrier();  // the lanes' entries are there for every lane
-  if (by_slot && first != y) count = 0;
-  return count > 0 ? e : -1;
+  if (by_slot && first != y) r.count = 0;
+  return r;
 }
 
 __global__ void __launch_bounds__(64 * MOE_WAVES1) moe_up_kernel(Moe m) {
+  constexpr int D = 3;  // K-blocks that a wave loads at a time
   __shared__ uint16_t lists[MOE_WAVES1][MOE_SLOTS];
   __shared__ __attribute__((aligned(16))) float part[MOE_WAVES1][2][64][4];
   const int lane = threadIdx.x & 63, w = wave_id_uniform(), g = lane >> 4, lo = lane & 15;
   const int tile = blockIdx.x, y = blockIdx.y;
-  int count;
-  const int e = slots_of(m, y, count, lists[w]);
+  const Live v = slots_of(m, y, lists[w]);
   if (tile == 0 && w == 0) {
-    if (lane == 0) {
-      m.count[y] = e < 0 ? 0 : count;
-      m.expert[y] = e;
-    }
-    for (int i = lane; e >= 0 && i < count; i += 64) m.list[(int64_t)y * m.slots + i] = lists[w][i];
+    if (lane == 0) m.live[y] = v;
+    for (int i = lane; i < v.count; i += 64) m.list[v.start + i] = lists[w][i];
   }
-  if (e < 0) return;
+  if (v.count == 0) return;
   const int H = m.hidden, I = m.inner, KB = (H + 127) >> 7;
   const int per = (KB + MOE_WAVES1 - 1) / MOE_WAVES1, kb0 = w * per, kb1 = kb0 + per < KB ? kb0 + per : KB;
-  const int64_t gate = (int64_t)e * 2 * I + tile * 16, up = gate + I;  // first rows
+  const int64_t gate = (int64_t)v.expert * 2 * I + tile * 16, up = gate + I;  // first rows
   const uint8_t *const wg = m.w1 + (gate + lo) * H, *const wu = m.w1 + (up + lo) * H;
-  const int nb = (2 * I + 127) >> 7;
-  const float* const sg = m.s1 + ((int64_t)e * nb + (tile * 16 >> 7)) * KB;
-  const float* const su = m.s1 + ((int64_t)e * nb + ((I + tile * 16) >> 7)) * KB;
-  for (int c0 = 0; c0 < count; c0 += 16) {
-    const bool live = c0 + lo < count;
-    const int slot = live ? lists[w][c0 + lo] : 0;
+  // the wave's scales, one for each K-block (at most 64), in the lanes
+  const int nb = (2 * I + 127) >> 7, mine = kb0 + lane < KB ? kb0 + lane : KB - 1;
+  const float sg = m.s1[((int64_t)v.expert * nb + (tile * 16 >> 7)) * KB + mine];
+  const float su = m.s1[((int64_t)v.expert * nb + ((I + tile * 16) >> 7)) * KB + mine];
+  for (int c0 = 0; c0 < v.count; c0 += 16) {
+    const int slot = lists[w][c0 + lo < v.count ? c0 + lo : c0];
     const uint16_t* const x = m.x + (int64_t)(slot / m.top) * H;
     v4f ag = {0.0f, 0.0f, 0.0f, 0.0f}, au = ag;
-    const v4f zero = ag;
-    struct Set {
-      Codes g, u;
-      Values x;
-    };
-    auto load = [&](Set& s, int kb) __attribute__((always_inline)) {
-      kb = kb < kb1 ? kb : kb1 - 1;
-      s.g = load_codes(wg, kb, g, H - 16);
-      s.u = load_codes(wu, kb, g, H - 16);
-      s.x = load_values(x, kb, g, H, live);
-    };
-    auto multiply = [&](const Set& s, int kb) __attribute__((always_inline)) {
-      promote(ag, block_product(s.g, s.x, zero), sg[kb]);
-      promote(au, block_product(s.u, s.x, zero), su[kb]);
-    };
-    Set a, b;
-    load(a, kb0);
-    for (int kb = kb0; kb < kb1; kb += 2) {
-      load(b, kb + 1);
-      multiply(a, kb);
-      load(a, kb + 2);
-      if (kb + 1 < kb1) multiply(b, kb + 1);
+    for (int kb = kb0; kb < kb1; kb += D) {
+      Codes cg[D], cu[D];
+      Values xv[D];
+#pragma unroll
+      for (int i = 0; i < D; ++i) {
+        const int at = kb + i < kb1 ? kb + i : kb1 - 1;
+        cg[i] = load_codes(wg, at, g, H);
+        cu[i] = load_codes(wu, at, g, H);
+        xv[i] = load_values(x, at, g, H);
+      }
+#pragma unroll
+      for (int i = 0; i < D; ++i) {
+        if (kb + i >= kb1) break;
+        clear_past(xv[i], kb + i, g, H);
+        promote(ag, block_product(cg[i], xv[i]), lane_value(sg, kb + i - kb0));
+        promote(au, block_product(cu[i], xv[i]), lane_value(su, kb + i - kb0));
+      }
     }
     __syncthreads();  // the last pass' sums have been read
     *reinterpret_cast<v4f*>(part[w][0][lane]) = ag;
@@ -175,63 +187,109 @@ __global__ void __launch_bounds__(64 * MOE_WAVES1) moe_up_kernel(Moe m) {
     __syncthreads();
     // thread 4l + i: result i of lane l, that is row 4 (l >> 4) + i of the tile, column l & 15
     const int l = threadIdx.x >> 2, i = threadIdx.x & 3;
-    if (c0 + (l & 15) < count) {
+    if (c0 + (l & 15) < v.count) {
       float hg = part[0][0][l][i], hu = part[0][1][l][i];
 #pragma unroll
       for (int k = 1; k < MOE_WAVES1; ++k) {
         hg += part[k][0][l][i];
         hu += part[k][1][l][i];
       }
-      const float v = hg * sigmoid(hg).s * hu;
-      const uint32_t hi = bf16_round_pair(v, 0.0f);
-      const float rest = v - bf16_lo(hi);
+      const float val = hg * sigmoid(hg).s * hu;
+      const uint32_t hi = bf16_round_pair(val, 0.0f);
+      const float rest = val - bf16_lo(hi);
       const int64_t at = (int64_t)lists[w][c0 + (l & 15)] * I + tile * 16 + (l >> 4) * 4 + i;
-      m.y_hi[at] = (uint16_t)hi;
-      m.y_lo[at] = (uint16_t)bf16_round_pair(rest - rest == 0.0f ? rest : 0.0f, 0.0f);  // (none of an infinity)
+      m.y[at] = (uint16_t)hi;
+      // (no rest of an infinity)
+      m.y[(int64_t)m.slots * I + at] = (uint16_t)bf16_round_pair(rest - rest == 0.0f ? rest : 0.0f, 0.0f);
     }
+  }
+}
+
+// One expert's slots c0 .. c0 + 8 NT - 1, K-blocks kb0 .. kb1 - 1: columns 0-7 of an MFMA are
+// the slots' rounded y, columns 8-15 the rests, whose sums join in the end.
+template <int NT, int D>
+__device__ __forceinline__ void moe_down_part(const Moe& m, const uint8_t* row, float scales, int kb0, int kb1, int g,
+                                              int lo, const uint16_t* list, int count, float* sums) {
+  const uint16_t* y[NT];
+  v4f acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int c = 8 * t + (lo & 7);
+    const int slot = list[c < count ? c : 0];
+    y[t] = m.y + ((int64_t)(lo >> 3) * m.slots + slot) * m.inner;
+    acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  for (int kb = kb0; kb < kb1; kb += D) {
+    Codes c[D];
+    Values v[D][NT];
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      const int at = kb + i < kb1 ? kb + i : kb1 - 1;
+      c[i] = load_codes(row, at, g, m.inner);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) v[i][t] = load_values(y[t], at, g, m.inner);
+    }
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      if (kb + i >= kb1) break;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        clear_past(v[i][t], kb + i, g, m.inner);
+        promote(acc[t], block_product(c[i], v[i][t]), lane_value(scales, kb + i - kb0));
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float own = acc[t][i];
+      const int other = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, own), 0x128, 0xF, 0xF, true);  // lane ^ 8
+      acc[t][i] = own + __builtin_bit_cast(float, other);
+    }
+    const int c = 8 * t + lo;
+    if (lo < 8 && c < count) *reinterpret_cast<v4f*>(sums + list[c] * 16 + 4 * g) = acc[t];
   }
 }
 
 __global__ void __launch_bounds__(64 * MOE_WAVES2) moe_down_kernel(Moe m, int chunks) {
   extern __shared__ __attribute__((aligned(16))) float sums[];  // [chunks][slots][16]
+  __shared__ Live live[MOE_SLOTS];
+  __shared__ uint16_t list[MOE_SLOTS];
+  __shared__ int found[MOE_SLOTS / 64];
   const int lane = threadIdx.x & 63, w = wave_id_uniform(), g = lane >> 4, lo = lane & 15;
-  const int I = m.inner, KB = (I + 127) >> 7, per = (KB + chunks - 1) / chunks;
   const int n0 = blockIdx.x * 16;
-  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int item = w; item < m.candidates * chunks; item += MOE_WAVES2) {
-    const int y = item / chunks, chunk = item - y * chunks;
-    const int count = m.count[y], e = m.expert[y];
-    if (count == 0) continue;
+  // the experts with choices, without gaps
+  Live v = {0, 0, 0, 0};
+  if ((int)threadIdx.x < m.candidates) v = m.live[threadIdx.x];
+  if ((int)threadIdx.x < m.slots) list[threadIdx.x] = m.list[threadIdx.x];
+  const uint64_t there = __ballot(v.count > 0);
+  if (w < MOE_SLOTS / 64 && lane == 0) found[w] = __popcll(there);
+  __syncthreads();
+  int total = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < MOE_SLOTS / 64; ++i) {
+    before += i < w ? found[i] : 0;
+    total += found[i];
+  }
+  if (v.count > 0) live[before + __popcll(there & ((uint64_t(1) << lane) - 1))] = v;
+  __syncthreads();
+
+  const int I = m.inner, KB = (I + 127) >> 7, per = (KB + chunks - 1) / chunks;
+  const int items = __builtin_amdgcn_readfirstlane(total) * chunks;
+  for (int item = w; item < items; item += MOE_WAVES2) {
+    const int at = item / chunks, chunk = item - at * chunks;
+    const int e = __builtin_amdgcn_readfirstlane(live[at].expert);
+    const int count = __builtin_amdgcn_readfirstlane(live[at].count);
+    const int start = __builtin_amdgcn_readfirstlane(live[at].start);
     const int kb0 = chunk * per, kb1 = kb0 + per < KB ? kb0 + per : KB;
     const uint8_t* const row = m.w2 + ((int64_t)e * m.hidden + n0 + lo) * I;
-    const float* const s = m.s2 + ((int64_t)e * ((m.hidden + 127) >> 7) + (n0 >> 7)) * KB;
+    const int mine = kb0 + lane < KB ? kb0 + lane : KB - 1;
+    const float scales = m.s2[((int64_t)e * ((m.hidden + 127) >> 7) + (n0 >> 7)) * KB + mine];
+    float* const to = sums + (int64_t)chunk * m.slots * 16;
     for (int c0 = 0; c0 < count; c0 += 16) {
-      const bool live = c0 + lo < count;
-      const int slot = live ? m.list[(int64_t)y * m.slots + c0 + lo] : 0;
-      const uint16_t *const hi = m.y_hi + (int64_t)slot * I, *const low = m.y_lo + (int64_t)slot * I;
-      v4f acc = zero;
-      struct Set {
-        Codes c;
-        Values hi, lo;
-      };
-      auto load = [&](Set& t, int kb) __attribute__((always_inline)) {
-        kb = kb < kb1 ? kb : kb1 - 1;
-        t.c = load_codes(row, kb, g, I - 16);
-        t.hi = load_values(hi, kb, g, I, live);
-        t.lo = load_values(low, kb, g, I, live);
-      };
-      auto multiply = [&](const Set& t, int kb) __attribute__((always_inline)) {
-        promote(acc, block_product(t.c, t.hi, block_product(t.c, t.lo, zero)), s[kb]);
-      };
-      Set a, b;
-      load(a, kb0);
-      for (int kb = kb0; kb < kb1; kb += 2) {
-        load(b, kb + 1);
-        multiply(a, kb);
-        load(a, kb + 2);
-        if (kb + 1 < kb1) multiply(b, kb + 1);
-      }
-      if (live) *reinterpret_cast<v4f*>(sums + ((int64_t)chunk * m.slots + slot) * 16 + 4 * g) = acc;
+      if (count - c0 <= 8) moe_down_part<1, 4>(m, row, scales, kb0, kb1, g, lo, list + start + c0, count - c0, to);
+      else moe_down_part<2, 2>(m, row, scales, kb0, kb1, g, lo, list + start + c0, count - c0, to);
     }
   }
   __syncthreads();
@@ -241,9 +299,9 @@ __global__ void __launch_bounds__(64 * MOE_WAVES2) moe_down_kernel(Moe m, int ch
     for (int j = 0; j < m.top; ++j) {
       const int slot = t * m.top + j, e = m.ids[slot];
       if (e < 0 || e >= m.experts) continue;
-      float v = sums[slot * 16 + n];
-      for (int c = 1; c < chunks; ++c) v += sums[(c * m.slots + slot) * 16 + n];
-      acc = __builtin_fmaf(m.weights[slot], v, acc);
+      float s = sums[slot * 16 + n];
+      for (int c = 1; c < chunks; ++c) s += sums[(c * m.slots + slot) * 16 + n];
+      acc = __builtin_fmaf(m.weights[slot], s, acc);
     }
     const int64_t at = (int64_t)t * m.hidden + n0 + n;
     if (m.residual != nullptr) acc += bf16_lo(m.residual[at]);
@@ -262,7 +320,7 @@ int moe_max_slots() { return MOE_SLOTS; }
 int64_t moe_decode_workspace(int tokens, int top, int experts, int64_t inner) {
   const int64_t slots = (int64_t)tokens * top, candidates = moe_candidates((int)slots, experts);
   auto pad = [](int64_t n) { return (n + 15) / 16 * 16; };
-  return 2 * pad(4 * candidates) + pad(2 * candidates * slots) + 2 * pad(2 * slots * inner);
+  return (int64_t)sizeof(Live) * candidates + pad(2 * slots) + pad(4 * slots * inner);
 }
 
 hipError_t set_moe_attributes() {
@@ -276,22 +334,19 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
                              hipStream_t stream) {
   Moe m = {(const uint16_t*)x, ids, weights, (const uint8_t*)w1, s1, (const uint8_t*)w2, s2,
            (const uint16_t*)residual, (uint16_t*)out, tokens, top, experts, (int)hidden, (int)inner,
-           tokens * top, moe_candidates(tokens * top, experts), nullptr, nullptr, nullptr, nullptr, nullptr};
+           tokens * top, moe_candidates(tokens * top, experts), nullptr, nullptr, nullptr};
   uint8_t* at = (uint8_t*)workspace;
   auto take = [&](int64_t bytes) {
     uint8_t* const p = at;
     at += (bytes + 15) / 16 * 16;
     return p;
   };
-  m.count = (int32_t*)take(4 * m.candidates);
-  m.expert = (int32_t*)take(4 * m.candidates);
-  m.list = (uint16_t*)take(2 * (int64_t)m.candidates * m.slots);
-  m.y_hi = (uint16_t*)take(2 * (int64_t)m.slots * inner);
-  m.y_lo = (uint16_t*)take(2 * (int64_t)m.slots * inner);
+  m.live = (Live*)take((int64_t)sizeof(Live) * m.candidates);
+  m.list = (uint16_t*)take(2 * (int64_t)m.slots);
+  m.y = (uint16_t*)take(4 * (int64_t)m.slots * inner);
   const int chunks = moe_chunks((int)inner);
-  if (m.slots > 0 && inner > 0)
-    hipLaunchKernelGGL(moe_up_kernel, dim3((unsigned)(inner / 16), (unsigned)m.candidates), dim3(64 * MOE_WAVES1), 0,
-                       stream, m);
+  hipLaunchKernelGGL(moe_up_kernel, dim3((unsigned)(inner / 16), (unsigned)m.candidates), dim3(64 * MOE_WAVES1), 0,
+                     stream, m);
   hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(hidden / 16)), dim3(64 * MOE_WAVES2),
                      chunks * m.slots * 64, stream, m, chunks);
   return hipGetLastError();

@@ -143,7 +143,7 @@ fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const
  *   out [tokens, hidden] bf16 out
  *   1 <= top and 1 <= experts <= FP8BS_MAX_GROUPS (else FP8BS_EINVAL);
  *   tokens * top <= FP8BS_MAX_MOE_CHOICES, hidden and inner multiples of 16, hidden <=
- *   65536, 16 <= inner <= 65536 (else FP8BS_ESHAPE); tokens == 0 or hidden == 0: no-op.
+ *   32768, 16 <= inner <= 32768 (else FP8BS_ESHAPE); tokens == 0 or hidden == 0: no-op.
  *   workspace of fp8bs_moe_decode_b128_workspace(tokens, top, experts, inner) bytes
  *   (else FP8BS_EINVAL).
  *   Results are batch invariant: a token's depend on that token only.

@@ -95,7 +95,7 @@ def load_library() -> ctypes.CDLL:
         lib.fp8bs_epilogue_backward_workspace.restype = i64
         lib.fp8bs_epilogue_backward_quantize_tg128.argtypes = [vp, vp, i32, i64, i64, vp, vp, vp, vp, i32, vp, i64, vp]
         lib.fp8bs_epilogue_backward_quantize_tg128.restype = ctypes.c_int
-        lib.fp8bs_moe_decode_b128_workspace.argtypes = [i64, i64, i64, i64]
+        lib.fp8bs_moe_decode_b128_workspace.argtypes = [i64, i64, i64, i64, i64]
         lib.fp8bs_moe_decode_b128_workspace.restype = i64
         lib.fp8bs_moe_decode_b128.argtypes = [vp] * 9 + [i64] * 5 + [vp, i64, vp]
         lib.fp8bs_moe_decode_b128.restype = ctypes.c_int
@@ -882,7 +882,7 @@ def moe_decode_b128(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w
     if residual is not None:
         _need_like(residual, "residual", _BF16, (T, H), dev)
     out = _output(out, "out", _BF16, (T, H), dev)
-    size = (_lib or load_library()).fp8bs_moe_decode_b128_workspace(T, k, E, inner)
+    size = (_lib or load_library()).fp8bs_moe_decode_b128_workspace(T, k, E, H, inner)
     ws = _workspace(size, dev)
     _call_on(dev, "fp8bs_moe_decode_b128", x.data_ptr(), ids.data_ptr(), weights.data_ptr(), w1.data_ptr(),
              s1.data_ptr(), w2.data_ptr(), s2.data_ptr(), _ptr(residual), out.data_ptr(), T, k, E, H, inner,

@@ -33,7 +33,6 @@ fp8bs_status ensure_attributes() {
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
     if (fp8bs::set_layernorm_attributes() != hipSuccess) return FP8BS_EHIP;
-    if (fp8bs::set_moe_attributes() != hipSuccess) return FP8BS_EHIP;
     done[dev] = true;
   }
   return FP8BS_OK;
@@ -206,9 +205,10 @@ fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const
                                                      (hipStream_t)stream));
 }
 
-int64_t fp8bs_moe_decode_b128_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t inner) {
-  if (check_moe_sizes(tokens, top, experts, 0, inner) != FP8BS_OK || tokens == 0) return 0;
-  return fp8bs::moe_decode_workspace((int)tokens, (int)top, (int)experts, inner);
+int64_t fp8bs_moe_decode_b128_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t hidden,
+                                        int64_t inner) {
+  if (check_moe_sizes(tokens, top, experts, hidden, inner) != FP8BS_OK || tokens == 0) return 0;
+  return fp8bs::moe_decode_workspace((int)tokens, (int)top, (int)experts, hidden, inner);
 }
 
 fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, const float* weights, const void* w1,
@@ -222,9 +222,8 @@ fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, c
     if (!aligned(p, 16)) return FP8BS_EALIGN;
   for (const void* p : {(const void*)ids_dev, (const void*)weights, (const void*)s1, (const void*)s2})
     if (!aligned(p, 4)) return FP8BS_EALIGN;
-  st = check_workspace(workspace, workspace_bytes, fp8bs_moe_decode_b128_workspace(tokens, top, experts, inner));
-  if (st != FP8BS_OK) return st;
-  st = ensure_attributes();
+  st = check_workspace(workspace, workspace_bytes, 
+                       fp8bs_moe_decode_b128_workspace(tokens, top, experts, hidden, inner));
   if (st != FP8BS_OK) return st;
   return from_launch(fp8bs::launch_moe_decode(x_bf16, ids_dev, weights, w1, s1, w2, s2, residual_bf16, out_bf16,
                                               (int)tokens, (int)top, (int)experts, hidden, inner, workspace,

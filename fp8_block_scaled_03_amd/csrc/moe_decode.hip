@@ -1,4 +1,4 @@
-// A whole mixture-of-experts layer for a few tokens, in two kernels:
+// A whole mixture-of-experts layer for a few tokens:
 //
 //   out[t] = sum_j weights[t,j] W2[e] (silu(g) u) (+ residual[t]),  [g | u] = W1[e] x[t],  e = ids[t,j]
 //
@@ -8,20 +8,26 @@
 // parts (y rounded, and the rest rounded: 2^-17 of it is lost).  A K-block of 128 is
 // four MFMAs into one sum P, then acc = fma(P, scale, acc).
 //
-// A slot is one choice (t, j) of an expert.  A candidate y of the first kernel is an expert,
+// A slot is one choice (t, j) of an expert.  A candidate is an expert,
 // or, if there are fewer slots than experts, a slot: it stands for its expert if no
 // earlier slot has the same.  What a candidate stands for every wave finds by
 // comparing all ids, one ballot for 64 of them.  MFMA columns are a candidate's slots,
 // 16 at a time; rows are 16 rows of the weight.
 //
-//   kernel 1: a workgroup of four waves takes 16 gates and the 16 ups that belong to them;
-//     the waves share K and are joined in order in LDS; y goes to the workspace.
-//     The first workgroup of a candidate also leaves its expert and slots there.
-//   kernel 2: a workgroup of 16 waves takes 16 columns of out; a wave takes an expert and a
-//     chunk of K at a time and leaves each slot's 16 sums in LDS; in the end every token
-//     adds its slots' sums, chunks and choices in order.
+//   up: a workgroup of four waves takes 16 or 32 gates and the ups that belong to them; y goes to the
+//     workspace.  The first workgroup of a candidate also leaves its expert and slots there.
+//   down: a workgroup takes 32 or 64 columns of out for one candidate; its slots' sums go to the workspace.
+//   join: every token adds its slots' sums, choices in order.
+// In the first two the waves share K (always a quarter each) and are joined in order in LDS.
 //
-// Neither order depends on the other tokens: results are batch invariant.
+// What bounds it is the weights' stream, and beside it what every workgroup reads of x
+// and y through its L2: that costs as much a byte (61 tokens, 64 experts of 4096 x 2048, top 8,
+// 16 gates to a workgroup: up 250 us, 190 without x; 16 columns: down 210 us, 88 without y).  So
+// with two slots and more to an expert a wave has 64 weight rows to a K-block of
+// values; fewer slots read little, and smaller tiles give more workgroups.  Waves that share rows of
+// y instead of K did not help (down 190): their reads do not meet in the L1.
+//
+// No order depends on the other tokens: results are batch invariant.
 #include "activation.hpp"
 #include "common.hpp"
 #include "launch_layer.hpp"
@@ -30,12 +36,11 @@
 namespace fp8bs {
 
 constexpr int MOE_SLOTS = 512;     // most choices of a call
-constexpr int MOE_WAVES1 = 4, MOE_WAVES2 = 16;
-constexpr int MOE_CHUNKS = 4;      // most chunks of K in the second kernel
+constexpr int MOE_WAVES = 4;       // of a workgroup; they share K
 
-// An expert with choices, as the first kernel leaves it for the second.
+// What a candidate stands for, as the first kernel leaves it for the second.
 struct Live {
-  int32_t expert, count, start;  // count 0: the candidate stands for none; its slots are list[start ..]
+  int32_t expert, count, start;  // count 0: it stands for none; its slots are list[start ..]
   int32_t unused;
 };
 
@@ -55,6 +60,7 @@ struct Moe {
   Live* live;       // [candidates]
   uint16_t* list;   // [slots], by expert
   uint16_t* y;      // [2, slots, inner]: y rounded, and the rest rounded
+  float* z;         // [slots, hidden]: the experts' results
 };
 
 __device__ __forceinline__ v4f mfma_bf16(v8bf w, v8bf x, v4f acc) {
@@ -62,10 +68,10 @@ __device__ __forceinline__ v4f mfma_bf16(v8bf w, v8bf x, v4f acc) {
 }
 
 // A lane's pieces of one K-block: 16 codes each of a weight row from 16g and 64 + 16g, and
-// for its column the values at the same K.  Loads have no conditions, so that the
-// compiler can count them: pieces past K read the row's last whole one (values are then
-// replaced by zeros, in the last K-block only), columns without a slot read the
-// first one's and are not stored.
+// for its column the values at the same K, from a uniform base.  Loads have no
+// conditions, so that the compiler can count them: pieces past K read the row's last
+// whole one (values are then replaced by zeros, in the last K-block only), columns
+// without a slot read another one's and are not stored.
 struct Codes {
   v4i c[2];
 };
@@ -73,18 +79,21 @@ struct Values {
   v4i v[4];
 };
 
-__device__ __forceinline__ Codes load_codes(const uint8_t* row, int kb, int g, int k) {
-  int o0 = kb * 128 + 16 * g, o1 = o0 + 64;
-  o0 = o0 < k ? o0 : k - 16;
-  o1 = o1 < k ? o1 : k - 16;
-  return {{*reinterpret_cast<const v4i*>(row + o0), *reinterpret_cast<const v4i*>(row + o1)}};
+struct Pieces {
+  uint32_t o0, o1;  // first K of the two pieces
+  __device__ __forceinline__ Pieces(int kb, int g, int k) {
+    const int a = kb * 128 + 16 * g, b = a + 64;
+    o0 = a < k ? a : k - 16;
+    o1 = b < k ? b : k - 16;
+  }
+};
+__device__ __forceinline__ Codes load_codes(const uint8_t* base, uint32_t row, Pieces p) {
+  return {{*reinterpret_cast<const v4i*>(base + (row + p.o0)), *reinterpret_cast<const v4i*>(base + (row + p.o1))}};
 }
-__device__ __forceinline__ Values load_values(const uint16_t* row, int kb, int g, int k) {
-  int o0 = kb * 128 + 16 * g, o1 = o0 + 64;
-  o0 = o0 < k ? o0 : k - 16;
-  o1 = o1 < k ? o1 : k - 16;
-  const v4i *const a = reinterpret_cast<const v4i*>(row + o0), *const b = reinterpret_cast<const v4i*>(row + o1);
-  return {{a[0], a[1], b[0], b[1]}};
+__device__ __forceinline__ Values load_values(const uint8_t* base, uint32_t row, Pieces p) {
+  const uint32_t a = row + 2 * p.o0, b = row + 2 * p.o1;  // (bytes)
+  return {{*reinterpret_cast<const v4i*>(base + a), *reinterpret_cast<const v4i*>(base + (a + 16)),
+           *reinterpret_cast<const v4i*>(base + b), *reinterpret_cast<const v4i*>(base + (b + 16))}};
 }
 __device__ __forceinline__ void clear_past(Values& x, int kb, int g, int k) {
   if (kb * 128 + 128 <= k) return;
@@ -95,19 +104,60 @@ __device__ __forceinline__ void clear_past(Values& x, int kb, int g, int k) {
   x.v[2] = in1 ? x.v[2] : z;
   x.v[3] = in1 ? x.v[3] : z;
 }
-// P of one K-block for 16 weight rows x 16 columns, for N sets of rows or of columns.
-__device__ __forceinline__ v4f block_product(const Codes& c, const Values& x) {
-  v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const v8bf lo = e4m3x8_to_bf16x8(v2i{c.c[h][0], c.c[h][1]}), hi = e4m3x8_to_bf16x8(v2i{c.c[h][2], c.c[h][3]});
-    p = mfma_bf16(lo, __builtin_bit_cast(v8bf, x.v[2 * h]), p);
-    p = mfma_bf16(hi, __builtin_bit_cast(v8bf, x.v[2 * h + 1]), p);
-  }
-  return p;
-}
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// RT row tiles x NT column tiles over K-blocks kb0 .. kb1 - 1 (at most 64): acc += sum of scale * P.
+// rows: the tiles' first rows; scales: a tile's, K-block kb0 + l in lane l; column t's values
+// begin at base + col[t].
+template <int RT, int NT, int D>
+__device__ __forceinline__ void products(const uint8_t* const (&rows)[RT], const float (&scales)[RT],
+                                         const uint8_t* base, const uint32_t (&col)[NT], int kb0, int kb1, int k,
+                                         v4f (&acc)[RT][NT]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4;
+  const uint32_t row = (uint32_t)(lane & 15) * (uint32_t)k;
+  struct Set {
+    Codes c[RT];
+    Values v[NT];
+  };
+  auto load = [&](Set& s, int kb) __attribute__((always_inline)) {
+    const Pieces p(kb < kb1 ? kb : kb1 - 1, g, k);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s.c[r] = load_codes(rows[r], row, p);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s.v[t] = load_values(base, col[t], p);
+  };
+  auto multiply = [&](Set& s, int kb) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) clear_past(s.v[t], kb, g, k);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const float scale = lane_value(scales[r], kb - kb0);
+      v8bf w[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const v4i q = s.c[r].c[h >> 1];
+        w[h] = e4m3x8_to_bf16x8(v2i{q[2 * (h & 1)], q[2 * (h & 1) + 1]});
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) p = mfma_bf16(w[h], __builtin_bit_cast(v8bf, s.v[t].v[h]), p);
+        promote(acc[r][t], p, scale);
+      }
+    }
+  };
+#pragma unroll 1
+  for (int kb = kb0; kb < kb1; kb += D) {
+    Set s[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) load(s[i], kb + i);
+#pragma unroll
+    for (int i = 0; i < D; ++i)
+      if (kb + i < kb1) multiply(s[i], kb + i);
+  }
 }
 
 // What candidate `y` stands for; its slots in order at list[0 ..] for this wave.
@@ -139,193 +189,193 @@ __device__ __forceinline__ Live slots_of(const Moe& m, int y, uint16_t* list) {
   return r;
 }
 
-__global__ void __launch_bounds__(64 * MOE_WAVES1) moe_up_kernel(Moe m) {
-  constexpr int D = 3;  // K-blocks that a wave loads at a time
-  __shared__ uint16_t lists[MOE_WAVES1][MOE_SLOTS];
-  __shared__ __attribute__((aligned(16))) float part[MOE_WAVES1][2][64][4];
-  const int lane = threadIdx.x & 63, w = wave_id_uniform(), g = lane >> 4, lo = lane & 15;
+__device__ __forceinline__ Live uniform(const Live& v) {
+  return {__builtin_amdgcn_readfirstlane(v.expert), __builtin_amdgcn_readfirstlane(v.count),
+          __builtin_amdgcn_readfirstlane(v.start), 0};
+}
+
+// The waves' shares of K, and their sums in LDS: part[wave][row tile][lane][row].
+struct Share {
+  int kb0, kb1, mine;  // K-blocks, and the one whose scales this lane holds
+  __device__ __forceinline__ Share(int w, int KB) {
+    const int per = (KB + MOE_WAVES - 1) / MOE_WAVES;
+    kb0 = w * per;
+    kb1 = kb0 + per < KB ? kb0 + per : KB;
+    mine = kb0 + (int)(threadIdx.x & 63);
+    mine = mine < KB ? mine : KB - 1;
+  }
+};
+template <int RT>
+using Part = float[MOE_WAVES][RT][64][4];
+
+template <int RT, int NT>
+__device__ __forceinline__ void leave(Part<RT>& part, int w, const v4f (&acc)[RT][NT], int t) {
+  __syncthreads();  // the sums before these have been read
+#pragma unroll
+  for (int r = 0; r < RT; ++r) *reinterpret_cast<v4f*>(part[w][r][threadIdx.x & 63]) = acc[r][t];
+  __syncthreads();
+}
+
+// RT / 2 tiles of 16 gates and their ups, NT column tiles of 16 slots at a time; D K-blocks are
+// loaded at a time, WAVES of them share a SIMD.
+template <int RT, int NT, int D, int WAVES>
+__global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
+  constexpr int G = RT / 2, ROWS = 16 * G;  // row tiles, and rows, of gates
+  __shared__ uint16_t lists[MOE_WAVES][MOE_SLOTS];
+  __shared__ __attribute__((aligned(16))) Part<RT> part;
+  const int lane = threadIdx.x & 63, w = wave_id_uniform(), lo = lane & 15;
   const int tile = blockIdx.x, y = blockIdx.y;
-  const Live v = slots_of(m, y, lists[w]);
+  const Live v = uniform(slots_of(m, y, lists[w]));
   if (tile == 0 && w == 0) {
     if (lane == 0) m.live[y] = v;
     for (int i = lane; i < v.count; i += 64) m.list[v.start + i] = lists[w][i];
   }
   if (v.count == 0) return;
-  const int H = m.hidden, I = m.inner, KB = (H + 127) >> 7;
-  const int per = (KB + MOE_WAVES1 - 1) / MOE_WAVES1, kb0 = w * per, kb1 = kb0 + per < KB ? kb0 + per : KB;
-  const int64_t gate = (int64_t)v.expert * 2 * I + tile * 16, up = gate + I;  // first rows
-  const uint8_t *const wg = m.w1 + (gate + lo) * H, *const wu = m.w1 + (up + lo) * H;
-  // the wave's scales, one for each K-block (at most 64), in the lanes
-  const int nb = (2 * I + 127) >> 7, mine = kb0 + lane < KB ? kb0 + lane : KB - 1;
-  const float sg = m.s1[((int64_t)v.expert * nb + (tile * 16 >> 7)) * KB + mine];
-  const float su = m.s1[((int64_t)v.expert * nb + ((I + tile * 16) >> 7)) * KB + mine];
-  for (int c0 = 0; c0 < v.count; c0 += 16) {
-    const int slot = lists[w][c0 + lo < v.count ? c0 + lo : c0];
-    const uint16_t* const x = m.x + (int64_t)(slot / m.top) * H;
-    v4f ag = {0.0f, 0.0f, 0.0f, 0.0f}, au = ag;
-    for (int kb = kb0; kb < kb1; kb += D) {
-      Codes cg[D], cu[D];
-      Values xv[D];
+  const int H = m.hidden, I = m.inner, KB = (H + 127) >> 7, nb = (2 * I + 127) >> 7;
+  const Share share(w, KB);
+  // the first half of the row tiles are gates from tile * ROWS, the second their ups; behind
+  // inner the first tile again
+  const uint8_t* rows[RT];
+  float scales[RT];
 #pragma unroll
-      for (int i = 0; i < D; ++i) {
-        const int at = kb + i < kb1 ? kb + i : kb1 - 1;
-        cg[i] = load_codes(wg, at, g, H);
-        cu[i] = load_codes(wu, at, g, H);
-        xv[i] = load_values(x, at, g, H);
-      }
+  for (int r = 0; r < RT; ++r) {
+    const int n = tile * ROWS + (r % G) * 16, row = (r / G) * I + (n < I ? n : tile * ROWS);
+    rows[r] = uniform_ptr(m.w1 + ((int64_t)v.expert * 2 * I + row) * H);
+    scales[r] = m.s1[((int64_t)v.expert * nb + (row >> 7)) * KB + share.mine];
+  }
+  for (int c0 = 0; c0 < v.count; c0 += 16 * NT) {
+    uint32_t col[NT];
+    v4f acc[RT][NT];
 #pragma unroll
-      for (int i = 0; i < D; ++i) {
-        if (kb + i >= kb1) break;
-        clear_past(xv[i], kb + i, g, H);
-        promote(ag, block_product(cg[i], xv[i]), lane_value(sg, kb + i - kb0));
-        promote(au, block_product(cu[i], xv[i]), lane_value(su, kb + i - kb0));
-      }
+    for (int t = 0; t < NT; ++t) {
+      const int c = c0 + 16 * t + lo;
+      const int slot = lists[w][c < v.count ? c : c0];
+      col[t] = (uint32_t)(slot / m.top) * (uint32_t)H * 2;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    __syncthreads();  // the last pass' sums have been read
-    *reinterpret_cast<v4f*>(part[w][0][lane]) = ag;
-    *reinterpret_cast<v4f*>(part[w][1][lane]) = au;
-    __syncthreads();
-    // thread 4l + i: result i of lane l, that is row 4 (l >> 4) + i of the tile, column l & 15
-    const int l = threadIdx.x >> 2, i = threadIdx.x & 3;
-    if (c0 + (l & 15) < v.count) {
-      float hg = part[0][0][l][i], hu = part[0][1][l][i];
+    products<RT, NT, D>(rows, scales, (const uint8_t*)m.x, col, share.kb0, share.kb1, H, acc);
 #pragma unroll
-      for (int k = 1; k < MOE_WAVES1; ++k) {
-        hg += part[k][0][l][i];
-        hu += part[k][1][l][i];
+    for (int t = 0; t < NT; ++t) {
+      if (c0 + 16 * t >= v.count) break;
+      leave<RT, NT>(part, w, acc, t);
+      // a thread has a slot and two gates of a row tile
+      for (int i = threadIdx.x; i < G * 128; i += 64 * MOE_WAVES) {
+        const int c = c0 + 16 * t + (i & 15), l = i & 63, pair = (i >> 6) & 1, r = i >> 7;
+        const int n = tile * ROWS + r * 16 + (l >> 4) * 4 + 2 * pair;
+        if (c >= v.count || n >= I) continue;
+        uint32_t hi[2], rest[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float g = part[0][r][l][2 * pair + e], u = part[0][r + G][l][2 * pair + e];
+#pragma unroll
+          for (int k = 1; k < MOE_WAVES; ++k) {
+            g += part[k][r][l][2 * pair + e];
+            u += part[k][r + G][l][2 * pair + e];
+          }
+          const float val = g * sigmoid(g).s * u;
+          hi[e] = bf16_round_pair(val, 0.0f);
+          const float left = val - bf16_lo(hi[e]);
+          rest[e] = bf16_round_pair(left - left == 0.0f ? left : 0.0f, 0.0f);  // (none of an infinity)
+        }
+        uint16_t* const to = m.y + (int64_t)lists[w][c] * I + n;
+        *reinterpret_cast<uint32_t*>(to) = hi[0] | (hi[1] << 16);
+        *reinterpret_cast<uint32_t*>(to + (int64_t)m.slots * I) = rest[0] | (rest[1] << 16);
       }
-      const float val = hg * sigmoid(hg).s * hu;
-      const uint32_t hi = bf16_round_pair(val, 0.0f);
-      const float rest = val - bf16_lo(hi);
-      const int64_t at = (int64_t)lists[w][c0 + (l & 15)] * I + tile * 16 + (l >> 4) * 4 + i;
-      m.y[at] = (uint16_t)hi;
-      // (no rest of an infinity)
-      m.y[(int64_t)m.slots * I + at] = (uint16_t)bf16_round_pair(rest - rest == 0.0f ? rest : 0.0f, 0.0f);
     }
   }
 }
 
-// One expert's slots c0 .. c0 + 8 NT - 1, K-blocks kb0 .. kb1 - 1: columns 0-7 of an MFMA are
-// the slots' rounded y, columns 8-15 the rests, whose sums join in the end.
-template <int NT, int D>
-__device__ __forceinline__ void moe_down_part(const Moe& m, const uint8_t* row, float scales, int kb0, int kb1, int g,
-                                              int lo, const uint16_t* list, int count, float* sums) {
-  const uint16_t* y[NT];
-  v4f acc[NT];
+// RT tiles of 16 columns of out, NT column tiles of 8 slots at a time: MFMA columns 0-7 are the slots' rounded y, columns 8-15 the
+// rests, whose sums join in the end.
+template <int RT, int NT, int D, int WAVES>
+__global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) {
+  __shared__ __attribute__((aligned(16))) Part<RT> part;
+  const int lane = threadIdx.x & 63, w = wave_id_uniform(), lo = lane & 15;
+  const Live v = uniform(m.live[blockIdx.y]);
+  if (v.count == 0) return;
+  const int I = m.inner, KB = (I + 127) >> 7, nb = (m.hidden + 127) >> 7, n0 = blockIdx.x * 16 * RT;
+  const Share share(w, KB);
+  const uint8_t* rows[RT];
+  float scales[RT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = 8 * t + (lo & 7);
-    const int slot = list[c < count ? c : 0];
-    y[t] = m.y + ((int64_t)(lo >> 3) * m.slots + slot) * m.inner;
-    acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < RT; ++r) {  // behind hidden: the first tile again
+    const int row = n0 + (n0 + 16 * r < m.hidden ? 16 * r : 0);
+    rows[r] = uniform_ptr(m.w2 + ((int64_t)v.expert * m.hidden + row) * I);
+    scales[r] = m.s2[((int64_t)v.expert * nb + (row >> 7)) * KB + share.mine];
   }
-  for (int kb = kb0; kb < kb1; kb += D) {
-    Codes c[D];
-    Values v[D][NT];
+  const uint16_t* const list = m.list + v.start;
+  for (int c0 = 0; c0 < v.count; c0 += 8 * NT) {
+    uint32_t col[NT];
+    v4f acc[RT][NT];
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-      const int at = kb + i < kb1 ? kb + i : kb1 - 1;
-      c[i] = load_codes(row, at, g, m.inner);
+    for (int t = 0; t < NT; ++t) {
+      const int c = c0 + 8 * t + (lo & 7);
+      const int slot = list[c < v.count ? c : c0];
+      col[t] = (uint32_t)((lo >> 3) * m.slots + slot) * (uint32_t)I * 2;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) v[i][t] = load_values(y[t], at, g, m.inner);
+      for (int r = 0; r < RT; ++r) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    products<RT, NT, D>(rows, scales, (const uint8_t*)m.y, col, share.kb0, share.kb1, I, acc);
 #pragma unroll
-    for (int i = 0; i < D; ++i) {
-      if (kb + i >= kb1) break;
+    for (int t = 0; t < NT; ++t) {
+      if (c0 + 8 * t >= v.count) break;
+      leave<RT, NT>(part, w, acc, t);
+      // a thread has a slot and four rows of a row tile
+      for (int i = threadIdx.x; i < RT * 32; i += 64 * MOE_WAVES) {
+        const int c = c0 + 8 * t + (i & 7), q = (i >> 3) & 3, r = i >> 5, at = 16 * q + (i & 7);
+        if (c >= v.count || n0 + 16 * r >= m.hidden) continue;
+        v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        clear_past(v[i][t], kb + i, g, m.inner);
-        promote(acc[t], block_product(c[i], v[i][t]), lane_value(scales, kb + i - kb0));
+        for (int k = 0; k < MOE_WAVES; ++k) {
+          const v4f one = *reinterpret_cast<const v4f*>(part[k][r][at]) +
+                          *reinterpret_cast<const v4f*>(part[k][r][at + 8]);
+          sum = k == 0 ? one : sum + one;
+        }
+        *reinterpret_cast<v4f*>(m.z + (int64_t)list[c] * m.hidden + n0 + 16 * r + 4 * q) = sum;
       }
     }
   }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float own = acc[t][i];
-      const int other = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, own), 0x128, 0xF, 0xF, true);  // lane ^ 8
-      acc[t][i] = own + __builtin_bit_cast(float, other);
-    }
-    const int c = 8 * t + lo;
-    if (lo < 8 && c < count) *reinterpret_cast<v4f*>(sums + list[c] * 16 + 4 * g) = acc[t];
-  }
 }
 
-__global__ void __launch_bounds__(64 * MOE_WAVES2) moe_down_kernel(Moe m, int chunks) {
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // [chunks][slots][16]
-  __shared__ Live live[MOE_SLOTS];
-  __shared__ uint16_t list[MOE_SLOTS];
-  __shared__ int found[MOE_SLOTS / 64];
-  const int lane = threadIdx.x & 63, w = wave_id_uniform(), g = lane >> 4, lo = lane & 15;
-  const int n0 = blockIdx.x * 16;
-  // the experts with choices, without gaps
-  Live v = {0, 0, 0, 0};
-  if ((int)threadIdx.x < m.candidates) v = m.live[threadIdx.x];
-  if ((int)threadIdx.x < m.slots) list[threadIdx.x] = m.list[threadIdx.x];
-  const uint64_t there = __ballot(v.count > 0);
-  if (w < MOE_SLOTS / 64 && lane == 0) found[w] = __popcll(there);
-  __syncthreads();
-  int total = 0, before = 0;
-#pragma unroll
-  for (int i = 0; i < MOE_SLOTS / 64; ++i) {
-    before += i < w ? found[i] : 0;
-    total += found[i];
-  }
-  if (v.count > 0) live[before + __popcll(there & ((uint64_t(1) << lane) - 1))] = v;
-  __syncthreads();
 
-  const int I = m.inner, KB = (I + 127) >> 7, per = (KB + chunks - 1) / chunks;
-  const int items = __builtin_amdgcn_readfirstlane(total) * chunks;
-  for (int item = w; item < items; item += MOE_WAVES2) {
-    const int at = item / chunks, chunk = item - at * chunks;
-    const int e = __builtin_amdgcn_readfirstlane(live[at].expert);
-    const int count = __builtin_amdgcn_readfirstlane(live[at].count);
-    const int start = __builtin_amdgcn_readfirstlane(live[at].start);
-    const int kb0 = chunk * per, kb1 = kb0 + per < KB ? kb0 + per : KB;
-    const uint8_t* const row = m.w2 + ((int64_t)e * m.hidden + n0 + lo) * I;
-    const int mine = kb0 + lane < KB ? kb0 + lane : KB - 1;
-    const float scales = m.s2[((int64_t)e * ((m.hidden + 127) >> 7) + (n0 >> 7)) * KB + mine];
-    float* const to = sums + (int64_t)chunk * m.slots * 16;
-    for (int c0 = 0; c0 < count; c0 += 16) {
-      if (count - c0 <= 8) moe_down_part<1, 4>(m, row, scales, kb0, kb1, g, lo, list + start + c0, count - c0, to);
-      else moe_down_part<2, 2>(m, row, scales, kb0, kb1, g, lo, list + start + c0, count - c0, to);
+// Four columns of a token to a thread.
+__global__ void __launch_bounds__(256) moe_join_kernel(Moe m) {
+  const int quads = m.hidden / 4, q = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+  if (q >= quads) return;
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int J = 8;  // choices that are loaded at a time; a skipped one reads its own z, which is not used
+  for (int j0 = 0; j0 < m.top; j0 += J) {
+    int id[J];
+    float w[J];
+    v4f z[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int slot = t * m.top + (j0 + j < m.top ? j0 + j : m.top - 1);
+      id[j] = m.ids[slot];
+      w[j] = m.weights[slot];
+      z[j] = *reinterpret_cast<const v4f*>(m.z + (int64_t)slot * m.hidden + 4 * q);
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (j0 + j < m.top && id[j] >= 0 && id[j] < m.experts) promote(acc, z[j], w[j]);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < m.tokens * 16; i += 64 * MOE_WAVES2) {
-    const int t = i >> 4, n = i & 15;
-    float acc = 0.0f;
-    for (int j = 0; j < m.top; ++j) {
-      const int slot = t * m.top + j, e = m.ids[slot];
-      if (e < 0 || e >= m.experts) continue;
-      float s = sums[slot * 16 + n];
-      for (int c = 1; c < chunks; ++c) s += sums[(c * m.slots + slot) * 16 + n];
-      acc = __builtin_fmaf(m.weights[slot], s, acc);
-    }
-    const int64_t at = (int64_t)t * m.hidden + n0 + n;
-    if (m.residual != nullptr) acc += bf16_lo(m.residual[at]);
-    m.out[at] = (uint16_t)bf16_round_pair(acc + 0.0f, 0.0f);
+  const int64_t at = (int64_t)t * m.hidden + 4 * q;
+  if (m.residual != nullptr) {
+    const uint2 r = *reinterpret_cast<const uint2*>(m.residual + at);
+    acc = acc + v4f{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
   }
+  *reinterpret_cast<uint2*>(m.out + at) =
+      make_uint2(bf16_round_pair(acc[0] + 0.0f, acc[1] + 0.0f), bf16_round_pair(acc[2] + 0.0f, acc[3] + 0.0f));
 }
 
 static int moe_candidates(int slots, int experts) { return slots < experts ? slots : experts; }
-static int moe_chunks(int inner) {
-  const int wanted = (inner + 511) / 512;  // (a function of inner alone: sums of a token are the same in every batch)
-  return wanted < MOE_CHUNKS ? (wanted > 0 ? wanted : 1) : MOE_CHUNKS;
-}
-
 int moe_max_slots() { return MOE_SLOTS; }
 
-int64_t moe_decode_workspace(int tokens, int top, int experts, int64_t inner) {
+int64_t moe_decode_workspace(int tokens, int top, int experts, int64_t hidden, int64_t inner) {
   const int64_t slots = (int64_t)tokens * top, candidates = moe_candidates((int)slots, experts);
   auto pad = [](int64_t n) { return (n + 15) / 16 * 16; };
-  return (int64_t)sizeof(Live) * candidates + pad(2 * slots) + pad(4 * slots * inner);
-}
-
-hipError_t set_moe_attributes() {
-  return hipFuncSetAttribute((const void*)moe_down_kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
-                             MOE_CHUNKS * MOE_SLOTS * 64);
+  return (int64_t)sizeof(Live) * candidates + pad(2 * slots) + pad(4 * slots * inner) + pad(4 * slots * hidden);
 }
 
 hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* weights, const void* w1,
@@ -334,7 +384,7 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
                              hipStream_t stream) {
   Moe m = {(const uint16_t*)x, ids, weights, (const uint8_t*)w1, s1, (const uint8_t*)w2, s2,
            (const uint16_t*)residual, (uint16_t*)out, tokens, top, experts, (int)hidden, (int)inner,
-           tokens * top, moe_candidates(tokens * top, experts), nullptr, nullptr, nullptr};
+           tokens * top, moe_candidates(tokens * top, experts), nullptr, nullptr, nullptr, nullptr};
   uint8_t* at = (uint8_t*)workspace;
   auto take = [&](int64_t bytes) {
     uint8_t* const p = at;
@@ -344,11 +394,26 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   m.live = (Live*)take((int64_t)sizeof(Live) * m.candidates);
   m.list = (uint16_t*)take(2 * (int64_t)m.slots);
   m.y = (uint16_t*)take(4 * (int64_t)m.slots * inner);
-  const int chunks = moe_chunks((int)inner);
-  hipLaunchKernelGGL(moe_up_kernel, dim3((unsigned)(inner / 16), (unsigned)m.candidates), dim3(64 * MOE_WAVES1), 0,
-                     stream, m);
-  hipLaunchKernelGGL(moe_down_kernel, dim3((unsigned)(hidden / 16)), dim3(64 * MOE_WAVES2),
-                     chunks * m.slots * 64, stream, m, chunks);
+  m.z = (float*)take(4 * (int64_t)m.slots * hidden);
+  const dim3 threads(64 * MOE_WAVES);
+  auto up = [&](auto kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((inner + rows - 1) / rows), (unsigned)m.candidates), threads, 0, stream, m);
+  };
+  auto down = [&](auto kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((hidden + rows - 1) / rows), (unsigned)m.candidates), threads, 0, stream, m);
+  };
+  // Slots of an expert, on average if every one is taken (us a call, two small and two large tiles, 64
+  // experts of 4096 x 2048, top 8, by tokens: 1 48.9 and 52.2, 2 69.6 and 82, 4 113 and 117, 8 140 and 149, 16 194 and
+  // 190, 32 296 and 277, 61 417 and 332; 61 tokens, top 1: 121 and 124; 8 experts, top 2, 61 tokens: 96 and 84)
+  if (m.slots < 2 * m.candidates) {
+    up(moe_up_kernel<2, 1, 2, 4>, 16);
+    down(moe_down_kernel<2, 1, 2, 4>, 32);
+  } else {
+    up(moe_up_kernel<4, 2, 1, 3>, 32);
+    down(moe_down_kernel<4, 2, 1, 3>, 64);
+  }
+  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((hidden / 4 + 255) / 256), (unsigned)tokens), dim3(256), 0, stream,
+                     m);
   return hipGetLastError();
 }
 

@@ -144,11 +144,11 @@ fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const
  *   1 <= top and 1 <= experts <= FP8BS_MAX_GROUPS (else FP8BS_EINVAL);
  *   tokens * top <= FP8BS_MAX_MOE_CHOICES, hidden and inner multiples of 16, hidden <=
  *   32768, 16 <= inner <= 32768 (else FP8BS_ESHAPE); tokens == 0 or hidden == 0: no-op.
- *   workspace of fp8bs_moe_decode_b128_workspace(tokens, top, experts, inner) bytes
- *   (else FP8BS_EINVAL).
+ *   workspace of fp8bs_moe_decode_b128_workspace(...) bytes (else FP8BS_EINVAL).
  *   Results are batch invariant: a token's depend on that token only.
  */
-int64_t fp8bs_moe_decode_b128_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t inner);
+int64_t fp8bs_moe_decode_b128_workspace(int64_t tokens, int64_t top, int64_t experts, int64_t hidden,
+                                        int64_t inner);
 fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, const float* weights, const void* w1,
                                    const float* s1, const void* w2, const float* s2, const void* residual_bf16,
                                    void* out_bf16, int64_t tokens, int64_t top, int64_t experts, int64_t hidden,

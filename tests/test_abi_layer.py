@@ -127,10 +127,11 @@ def test_epilogue_backward_refusals():
 
 def test_moe_refusals():
     lib = binding.load_library()
-    size = lib.fp8bs_moe_decode_b128_workspace(3, 2, 4, 64)
+    size = lib.fp8bs_moe_decode_b128_workspace(3, 2, 4, 64, 64)
     assert size > 0
-    for bad in ((-1, 2, 4, 64), (3, 0, 4, 64), (3, 2, 0, 64), (3, 2, 1025, 64), (3, 2, 4, 0), (3, 2, 4, 24),
-                (257, 2, 4, 64), (1 << 40, 1 << 40, 4, 64), (0, 2, 4, 64)):
+    for bad in ((-1, 2, 4, 64, 64), (3, 0, 4, 64, 64), (3, 2, 0, 64, 64), (3, 2, 1025, 64, 64), (3, 2, 4, 64, 0),
+                (3, 2, 4, 64, 24), (3, 2, 4, 24, 64), (257, 2, 4, 64, 64), (1 << 40, 1 << 40, 4, 64, 64),
+                (0, 2, 4, 64, 64)):
         assert lib.fp8bs_moe_decode_b128_workspace(*bad) == 0
     ok = [A16, A4, A4, A16, A4, A16, A4, A16, A16, 3, 2, 4, 64, 64, A16, size]
     with_ = _changed(binding.moe_decode_b128_raw, ok)

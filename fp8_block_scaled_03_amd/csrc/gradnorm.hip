@@ -19,7 +19,7 @@ namespace fp8bs {
 
 constexpr int TABLE = 96;
 constexpr int64_t CHUNK = 32768;
-constexpr int GRAD_GRID = 2048;
+constexpr int GRAD_GRID = 1024;
 constexpr int64_t JOIN_MAX = 4096;  // partial sums that every workgroup of the clipping kernel adds up by itself
 
 struct GradTable {
@@ -30,7 +30,24 @@ struct GradTable {
   uint8_t bf16[TABLE];
 };
 
+// Gradients beyond what the caches keep are read past them.  Of 256 MB of Infinity Cache a
+// norm that fits leaves the clipping its gradients; above that, lines that are
+// not kept cost nothing to replace (403 M values: norm 285 us through the caches, 209 past
+// them; clipping 531 and 519; but 32 M values, 112 MB, 66 us in place through the caches and 73).
+constexpr int64_t NORM_PAST = int64_t(512) << 20, CLIP_PAST = int64_t(192) << 20;  // bytes of all gradients
+
 typedef uint4 piece_t;
+template <bool PAST>
+__device__ __forceinline__ piece_t load_piece(const piece_t* p) {
+  typedef unsigned v4u __attribute__((ext_vector_type(4)));
+  if constexpr (!PAST) return *p;
+  const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_piece(uint8_t* p, piece_t v) {  // (it is read in another step of the program)
+  typedef unsigned v4u __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
+}
 struct __attribute__((packed, aligned(2))) loose_piece_t {
   uint32_t v[4];
 };
@@ -68,6 +85,7 @@ __device__ __forceinline__ void add_squares(piece_t v, bool bf16, double (&acc)[
   }
 }
 
+template <bool PAST>
 __global__ void __launch_bounds__(256) grad_sumsq_kernel(GradTable t, uint32_t chunks, double* __restrict__ partial) {
   __shared__ double lds[4];
   double acc[2] = {0.0, 0.0};
@@ -82,7 +100,7 @@ __global__ void __launch_bounds__(256) grad_sumsq_kernel(GradTable t, uint32_t c
     if (at >= lead && at + CHUNK <= end) {
       piece_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const piece_t*>(q)[i * 256 + threadIdx.x];
+      for (int i = 0; i < 8; ++i) v[i] = load_piece<PAST>(reinterpret_cast<const piece_t*>(q) + i * 256 + threadIdx.x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) add_squares(v[i], bf16, acc);
     } else {
@@ -140,6 +158,7 @@ __device__ __forceinline__ piece_t scaled(piece_t v, bool bf16, float f) {
 }
 
 // n partial sums, or (partial null) the norm at norm_in.
+template <bool PAST>
 __global__ void __launch_bounds__(256) clip_kernel(GradTable t, uint32_t chunks, const double* __restrict__ partial,
                                                    int n, const float* __restrict__ norm_in, double max_norm,
                                                    double eps, float* __restrict__ norm_out) {
@@ -164,12 +183,12 @@ __global__ void __launch_bounds__(256) clip_kernel(GradTable t, uint32_t chunks,
     if (at >= lead && at + CHUNK <= end) {
       piece_t v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = reinterpret_cast<const piece_t*>(q)[j * 256 + threadIdx.x];
+      for (int j = 0; j < 8; ++j) v[j] = load_piece<PAST>(reinterpret_cast<const piece_t*>(q) + j * 256 + threadIdx.x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const piece_t r = scaled(v[j], bf16, f);
         const int64_t off = (j * 256 + threadIdx.x) * 16;
-        if (even) *reinterpret_cast<piece_t*>(o + off) = r;
+        if (even) store_piece(o + off, r);
         else *reinterpret_cast<loose_piece_t*>(o + off) = loose_piece_t{{r.x, r.y, r.z, r.w}};
       }
     } else {
@@ -215,15 +234,22 @@ static uint32_t fill_table(const Grads& g, int first, GradTable& t) {
 
 static unsigned grad_grid(uint32_t chunks) { return chunks < GRAD_GRID ? chunks : GRAD_GRID; }
 
+static int64_t grad_bytes(const Grads& g) {
+  int64_t bytes = 0;
+  for (int i = 0; i < g.n; ++i) bytes += g.counts[i] * (g.types[i] == 1 ? 2 : 4);
+  return bytes;
+}
+
 // Partial sums of all tensors at workspace + 2; their number.
 static int64_t launch_sumsq(const Grads& g, double* workspace, hipStream_t stream) {
+  const auto kernel = grad_bytes(g) > NORM_PAST ? grad_sumsq_kernel<true> : grad_sumsq_kernel<false>;
   int64_t used = 0;
   for (int first = 0; first < g.n; first += TABLE) {
     GradTable t;
     const uint32_t chunks = fill_table(g, first, t);
     if (chunks == 0) continue;
     const unsigned grid = grad_grid(chunks);
-    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(grid), dim3(256), 0, stream, t, chunks, workspace + 2 + used);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, t, chunks, workspace + 2 + used);
     used += grid;
   }
   return used;
@@ -251,11 +277,12 @@ hipError_t launch_clip_grads(const Grads& g, double max_norm, double eps, float*
       norm_out = nullptr;
     }
   }
+  const auto kernel = grad_bytes(g) > CLIP_PAST ? clip_kernel<true> : clip_kernel<false>;
   for (int first = (g.n - 1) / TABLE * TABLE; first >= 0 && g.n > 0; first -= TABLE) {
     GradTable t;
     const uint32_t chunks = fill_table(g, first, t);
     if (chunks == 0) continue;
-    hipLaunchKernelGGL(clip_kernel, dim3(grad_grid(chunks)), dim3(256), 0, stream, t, chunks, partial, (int)used,
+    hipLaunchKernelGGL(kernel, dim3(grad_grid(chunks)), dim3(256), 0, stream, t, chunks, partial, (int)used,
                        (const float*)norm, max_norm, eps, norm_out);
     norm_out = nullptr;
   }

@@ -67,11 +67,14 @@ __device__ __forceinline__ v4f mfma_bf16(v8bf w, v8bf x, v4f acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, acc, 0, 0, 0);
 }
 
-// A lane's pieces of one K-block: 16 codes each of a weight row from 16g and 64 + 16g, and
-// for its column the values at the same K, from a uniform base.  Loads have no
-// conditions, so that the compiler can count them: pieces past K read the row's last
-// whole one (values are then replaced by zeros, in the last K-block only), columns
-// without a slot read another one's and are not stored.
+// A K-block's loads.  A load of codes covers eight rows' 128 bytes, whole lines (a line read in
+// halves past the caches comes twice: up 290 us, not 250): lane (g, lo) loads row lo & 7, or 8
+// + that, from 32g + 2 (lo & 8).  Lanes lo and lo ^ 8 then exchange one of their two pieces, and
+// lane (g, lo) has row lo from 32g and from 32g + 16, as the MFMA takes it; and for its
+// column the values at the same K.  Loads have no conditions, so that the compiler
+// can count them: pieces past K read the row's last whole one (values are then
+// replaced by zeros, in the last K-block only), columns without a slot read another
+// one's and are not stored.
 struct Codes {
   v4i c[2];
 };
@@ -80,15 +83,22 @@ struct Values {
 };
 
 struct Pieces {
-  uint32_t o0, o1;  // first K of the two pieces
-  __device__ __forceinline__ Pieces(int kb, int g, int k) {
-    const int a = kb * 128 + 16 * g, b = a + 64;
+  uint32_t code, o0, o1;  // first K of this lane's load of codes, and of its two pieces of values
+  __device__ __forceinline__ Pieces(int kb, int g, int lo, int k) {
+    const int a = kb * 128 + 32 * g, b = a + 16, c = a + 2 * (lo & 8);
     o0 = a < k ? a : k - 16;
     o1 = b < k ? b : k - 16;
+    code = c < k ? c : k - 16;
   }
 };
-__device__ __forceinline__ Codes load_codes(const uint8_t* base, uint32_t row, Pieces p) {
-  return {{*reinterpret_cast<const v4i*>(base + (row + p.o0)), *reinterpret_cast<const v4i*>(base + (row + p.o1))}};
+// The weights are read once: past the caches, which x and y share (a call of 1 to 32 tokens 4 to 9%
+// less).
+__device__ __forceinline__ v4i stream(const uint8_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));
+}
+// row: of the tile's first eight rows
+__device__ __forceinline__ Codes load_codes(const uint8_t* base, uint32_t row, uint32_t eight, Pieces p) {
+  return {{stream(base + (row + p.code)), stream(base + (row + eight + p.code))}};
 }
 __device__ __forceinline__ Values load_values(const uint8_t* base, uint32_t row, Pieces p) {
   const uint32_t a = row + 2 * p.o0, b = row + 2 * p.o1;  // (bytes)
@@ -98,7 +108,7 @@ __device__ __forceinline__ Values load_values(const uint8_t* base, uint32_t row,
 __device__ __forceinline__ void clear_past(Values& x, int kb, int g, int k) {
   if (kb * 128 + 128 <= k) return;
   const v4i z = {0, 0, 0, 0};
-  const bool in0 = kb * 128 + 16 * g < k, in1 = kb * 128 + 64 + 16 * g < k;
+  const bool in0 = kb * 128 + 32 * g < k, in1 = kb * 128 + 32 * g + 16 < k;
   x.v[0] = in0 ? x.v[0] : z;
   x.v[1] = in0 ? x.v[1] : z;
   x.v[2] = in1 ? x.v[2] : z;
@@ -116,15 +126,16 @@ __device__ __forceinline__ void products(const uint8_t* const (&rows)[RT], const
                                          const uint8_t* base, const uint32_t (&col)[NT], int kb0, int kb1, int k,
                                          v4f (&acc)[RT][NT]) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
-  const uint32_t row = (uint32_t)(lane & 15) * (uint32_t)k;
+  const uint32_t row = (uint32_t)(lane & 7) * (uint32_t)k, eight = 8 * (uint32_t)k;
+  const bool low = (lane & 8) == 0;
   struct Set {
     Codes c[RT];
     Values v[NT];
   };
   auto load = [&](Set& s, int kb) __attribute__((always_inline)) {
-    const Pieces p(kb < kb1 ? kb : kb1 - 1, g, k);
+    const Pieces p(kb < kb1 ? kb : kb1 - 1, g, lane & 15, k);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) s.c[r] = load_codes(rows[r], row, p);
+    for (int r = 0; r < RT; ++r) s.c[r] = load_codes(rows[r], row, eight, p);
 #pragma unroll
     for (int t = 0; t < NT; ++t) s.v[t] = load_values(base, col[t], p);
   };
@@ -135,9 +146,17 @@ __device__ __forceinline__ void products(const uint8_t* const (&rows)[RT], const
     for (int r = 0; r < RT; ++r) {
       const float scale = lane_value(scales[r], kb - kb0);
       v8bf w[4];
+      v4i both[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int a = s.c[r].c[0][i], b = s.c[r].c[1][i], send = low ? b : a;
+        const int got = __builtin_amdgcn_update_dpp(0, send, 0x128, 0xF, 0xF, true);  // from lane ^ 8
+        both[0][i] = low ? a : got;
+        both[1][i] = low ? got : b;
+      }
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const v4i q = s.c[r].c[h >> 1];
+        const v4i q = both[h >> 1];
         w[h] = e4m3x8_to_bf16x8(v2i{q[2 * (h & 1)], q[2 * (h & 1) + 1]});
       }
 #pragma unroll
@@ -402,15 +421,19 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   auto down = [&](auto kernel, int rows) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)((hidden + rows - 1) / rows), (unsigned)m.candidates), threads, 0, stream, m);
   };
-  // Slots of an expert, on average if every one is taken (us a call, two small and two large tiles, 64
-  // experts of 4096 x 2048, top 8, by tokens: 1 48.9 and 52.2, 2 69.6 and 82, 4 113 and 117, 8 140 and 149, 16 194 and
-  // 190, 32 296 and 277, 61 417 and 332; 61 tokens, top 1: 121 and 124; 8 experts, top 2, 61 tokens: 96 and 84)
+  // By the slots of an expert, on average if every one is taken (us a call, small, middle and large
+  // tiles, by tokens, top and experts of 4096 x 2048: 1, 8, 64 46.6, 52, -; 4, 8, 64 102, 117, -; 8, 8, 64 133, 149, -;
+  // 16, 8, 64 194, 186, -; 32, 8, 64 296, 270, -; 61, 8, 64 406, 340, 378; 61, 1, 64 111, 124, -; 61, 2, 8 92, 95, 87;
+  // 61, 4, 8 138, 130, 104)
   if (m.slots < 2 * m.candidates) {
     up(moe_up_kernel<2, 1, 2, 4>, 16);
     down(moe_down_kernel<2, 1, 2, 4>, 32);
-  } else {
+  } else if (m.slots < 12 * m.candidates) {
     up(moe_up_kernel<4, 2, 1, 3>, 32);
     down(moe_down_kernel<4, 2, 1, 3>, 64);
+  } else {
+    up(moe_up_kernel<4, 4, 1, 2>, 32);
+    down(moe_down_kernel<4, 4, 1, 2>, 64);
   }
   hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((hidden / 4 + 255) / 256), (unsigned)tokens), dim3(256), 0, stream,
                      m);

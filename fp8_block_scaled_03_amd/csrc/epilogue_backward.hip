@@ -17,9 +17,11 @@
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
 
+#include <type_traits>
+
 namespace fp8bs {
 
-template <int ACT, bool LINES>
+template <int ACT, bool LINES, bool PAST>
 __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* __restrict__ dout,
                                                                 const uint16_t* __restrict__ z, int64_t rows,
                                                                 int64_t n, uint16_t* __restrict__ dz,
@@ -35,8 +37,8 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* 
   const int64_t from = in ? col : 0;  // lanes past n read column 0 and count as zeros
   auto load = [&](int64_t set, uint4& d, uint4& x) __attribute__((always_inline)) {
     const int64_t row = set * 4 + rsub < rows ? set * 4 + rsub : rows - 1;
-    d = *reinterpret_cast<const uint4*>(dout + row * n + from);
-    if constexpr (ACT != ACT_NONE) x = *reinterpret_cast<const uint4*>(z + row * n + from);
+    d = load_once<PAST>(dout + row * n + from);
+    if constexpr (ACT != ACT_NONE) x = load_once<PAST>(z + row * n + from);
   };
   const int64_t sets = (rows + 3) >> 2;
   float sums[8] = {};
@@ -97,23 +99,20 @@ hipError_t launch_epilogue_backward(const void* dout, const void* z, int act, in
                          (const uint16_t*)z, rows, n, (uint16_t*)dz, (uint8_t*)q, scales,
                          dbias ? workspace : nullptr, (uint32_t)slabs);
     };
-    const bool lines = n % 128 == 0;
+    const bool past = rows * n * (act == ACT_NONE ? 2 : 4) > INPUTS_PAST;
+    auto choose = [&](auto act_) {
+      constexpr int ACT = decltype(act_)::value;
+      if (n % 128 == 0)
+        past ? launch(epilogue_backward_kernel<ACT, true, true>) : launch(epilogue_backward_kernel<ACT, true, false>);
+      else
+        past ? launch(epilogue_backward_kernel<ACT, false, true>) : launch(epilogue_backward_kernel<ACT, false, false>);
+    };
     switch (act) {
-      case ACT_RELU:
-        lines ? launch(epilogue_backward_kernel<ACT_RELU, true>) : launch(epilogue_backward_kernel<ACT_RELU, false>);
-        break;
-      case ACT_GELU:
-        lines ? launch(epilogue_backward_kernel<ACT_GELU, true>) : launch(epilogue_backward_kernel<ACT_GELU, false>);
-        break;
-      case ACT_GELU_TANH:
-        lines ? launch(epilogue_backward_kernel<ACT_GELU_TANH, true>)
-              : launch(epilogue_backward_kernel<ACT_GELU_TANH, false>);
-        break;
-      case ACT_SILU:
-        lines ? launch(epilogue_backward_kernel<ACT_SILU, true>) : launch(epilogue_backward_kernel<ACT_SILU, false>);
-        break;
-      default:
-        lines ? launch(epilogue_backward_kernel<ACT_NONE, true>) : launch(epilogue_backward_kernel<ACT_NONE, false>);
+      case ACT_RELU: choose(std::integral_constant<int, ACT_RELU>()); break;
+      case ACT_GELU: choose(std::integral_constant<int, ACT_GELU>()); break;
+      case ACT_GELU_TANH: choose(std::integral_constant<int, ACT_GELU_TANH>()); break;
+      case ACT_SILU: choose(std::integral_constant<int, ACT_SILU>()); break;
+      default: choose(std::integral_constant<int, ACT_NONE>());
     }
   }
   if (dbias) launch_column_sum(workspace, rows > 0 ? (unsigned)slabs : 0, n, n, dbias, nullptr, accumulate, stream);

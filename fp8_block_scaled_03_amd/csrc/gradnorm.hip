@@ -14,6 +14,7 @@
 // each add up the partial sums, in the same order, so two launches do the whole.
 #include "common.hpp"
 #include "launch_layer.hpp"
+#include "quant_g128.hpp"
 
 namespace fp8bs {
 
@@ -39,10 +40,7 @@ constexpr int64_t NORM_PAST = int64_t(512) << 20, CLIP_PAST = int64_t(192) << 20
 typedef uint4 piece_t;
 template <bool PAST>
 __device__ __forceinline__ piece_t load_piece(const piece_t* p) {
-  typedef unsigned v4u __attribute__((ext_vector_type(4)));
-  if constexpr (!PAST) return *p;
-  const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
-  return make_uint4(v[0], v[1], v[2], v[3]);
+  return load_once<PAST>(reinterpret_cast<const uint16_t*>(p));
 }
 __device__ __forceinline__ void store_piece(uint8_t* p, piece_t v) {  // (it is read in another step of the program)
   typedef unsigned v4u __attribute__((ext_vector_type(4)));

@@ -70,7 +70,7 @@ struct LayerNorm {
   float eps;
 };
 
-template <int NL, int WPR, bool LINES>
+template <int NL, int WPR, bool LINES, bool PAST>
 __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNorm p, uint32_t sets) {
   constexpr int WAVES = WPR == 8 ? 8 : 4, RPW = WAVES / WPR;  // waves and rows of a workgroup
   __shared__ float sums[2][WAVES][2];
@@ -92,14 +92,14 @@ __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNo
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int col = (WPR * i + wk) * 512 + lane * 8;
-      hv[i] = col < d ? *reinterpret_cast<const uint4*>(p.x + at + col) : make_uint4(0, 0, 0, 0);
+      hv[i] = col < d ? load_once<PAST>(p.x + at + col) : make_uint4(0, 0, 0, 0);
     }
     if (p.res != nullptr) {
       uint4 rv[NL];
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int col = (WPR * i + wk) * 512 + lane * 8;
-        rv[i] = col < d ? *reinterpret_cast<const uint4*>(p.res + at + col) : make_uint4(0, 0, 0, 0);
+        rv[i] = col < d ? load_once<PAST>(p.res + at + col) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
@@ -183,7 +183,7 @@ struct LayerNormBackward {
   int64_t rows, d;
 };
 
-template <int NL, int WPR, bool STREAM>
+template <int NL, int WPR, bool STREAM, bool PAST>
 __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(LayerNormBackward p, uint32_t sets) {
   constexpr int RPW = LNB_WAVES / WPR;  // rows of a workgroup
   __shared__ float sums[2][LNB_WAVES][2];
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
     const uint16_t *const a = p.dy + from * p.d, *const b = p.h + from * p.d;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      dy[i] = *reinterpret_cast<const uint4*>(a + at_col[i]);
-      h[i] = *reinterpret_cast<const uint4*>(b + at_col[i]);
+      dy[i] = load_once<PAST>(a + at_col[i]);
+      h[i] = load_once<PAST>(b + at_col[i]);
     }
     mean = p.mean[from];
     rstd = p.rstd[from];
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
     if constexpr (STREAM) {
       const uint16_t* const a = p.dres + row_of(id) * p.d;
 #pragma unroll
-      for (int i = 0; i < NL; ++i) rv[i] = *reinterpret_cast<const uint4*>(a + at_col[i]);
+      for (int i = 0; i < NL; ++i) rv[i] = load_once<PAST>(a + at_col[i]);
     }
   };
   // One set of rows; the next set's loads are in flight meanwhile.
@@ -342,10 +342,14 @@ static void launch_ln(const LayerNorm& p, hipStream_t stream) {
   constexpr int THREADS = WPR == 8 ? 512 : 256, RPW = THREADS / 64 / WPR;
   const int64_t sets = (p.rows + RPW - 1) / RPW;
   const dim3 grid((unsigned)(sets < 2048 ? sets : 2048));
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(THREADS), 0, stream, p, (uint32_t)sets);
+  };
+  const bool past = p.rows * p.d * (p.res ? 4 : 2) > INPUTS_PAST;
   if (p.d % 128 == 0)
-    hipLaunchKernelGGL((layernorm_kernel<NL, WPR, true>), grid, dim3(THREADS), 0, stream, p, (uint32_t)sets);
+    past ? launch(layernorm_kernel<NL, WPR, true, true>) : launch(layernorm_kernel<NL, WPR, true, false>);
   else
-    hipLaunchKernelGGL((layernorm_kernel<NL, WPR, false>), grid, dim3(THREADS), 0, stream, p, (uint32_t)sets);
+    past ? launch(layernorm_kernel<NL, WPR, false, true>) : launch(layernorm_kernel<NL, WPR, false, false>);
 }
 
 hipError_t launch_layernorm(const void* x, const void* residual, const void* gamma, const void* beta, float eps,
@@ -381,10 +385,16 @@ constexpr int ln_backward_lds() { return WPR < LNB_WAVES ? 2 * NL * 8 * 64 * WPR
 template <int NL, int WPR>
 static void launch_ln_backward(const LayerNormBackward& p, unsigned grid, uint32_t sets, hipStream_t stream) {
   constexpr int LDS = ln_backward_lds<NL, WPR>(), THREADS = 64 * LNB_WAVES;
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(THREADS), LDS, stream, p, sets);
+  };
+  const bool past = p.rows * p.d * (p.dres ? 6 : 4) > INPUTS_PAST;
   if (p.dres)
-    hipLaunchKernelGGL((layernorm_backward_kernel<NL, WPR, true>), dim3(grid), dim3(THREADS), LDS, stream, p, sets);
+    past ? launch(layernorm_backward_kernel<NL, WPR, true, true>)
+         : launch(layernorm_backward_kernel<NL, WPR, true, false>);
   else
-    hipLaunchKernelGGL((layernorm_backward_kernel<NL, WPR, false>), dim3(grid), dim3(THREADS), LDS, stream, p, sets);
+    past ? launch(layernorm_backward_kernel<NL, WPR, false, true>)
+         : launch(layernorm_backward_kernel<NL, WPR, false, false>);
 }
 
 hipError_t set_layernorm_attributes() {
@@ -392,8 +402,11 @@ hipError_t set_layernorm_attributes() {
   auto allow = [&](const void* kernel, int lds) {
     if (e == hipSuccess) e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   };
-  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, true>, ln_backward_lds<LNB_NL, 8>());
-  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, false>, ln_backward_lds<LNB_NL, 8>());
+  constexpr int LDS = ln_backward_lds<LNB_NL, 8>();
+  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, true, true>, LDS);
+  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, true, false>, LDS);
+  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, false, true>, LDS);
+  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, false, false>, LDS);
   return e;
 }
 

@@ -88,7 +88,7 @@ template <int ACT>
 __device__ __forceinline__ float slope(float z) {
   // far values behave as at these bounds, bit for bit, and overflow nothing; a NaN stays
   auto within = [](float v, float bound) __attribute__((always_inline)) {
-    return v != v ? v : fminf(fmaxf(v, -bound), bound);
+    return __builtin_elementwise_minimum(__builtin_elementwise_maximum(v, -bound), bound);
   };
   if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
   if constexpr (ACT == ACT_SILU) {
@@ -110,7 +110,7 @@ __device__ __forceinline__ float slope(float z) {
   if constexpr (ACT == ACT_GELU) {
     constexpr float L_HI = 0.7213475108146667f, L_LO = 9.629815167500055e-09f;  // log2(e) / 2
     constexpr float ROUND = 0x1.8p23f;
-    const float t = __builtin_fabsf(within(z, 32.0f));
+    const float t = __builtin_elementwise_minimum(__builtin_fabsf(z), 32.0f);
     const float t2 = t * t;                                 // exact: t has eight bits
     const float m = __builtin_fmaf(t2, L_HI, ROUND), n = m - ROUND;
     const float rest = __builtin_fmaf(-t2, L_LO, __builtin_fmaf(-t2, L_HI, n));

@@ -27,6 +27,8 @@
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
 
+#include <type_traits>
+
 namespace fp8bs {
 
 constexpr int LN_NL = 4, LN_MAX_WPR = 8;
@@ -187,7 +189,7 @@ template <int NL, int WPR, bool STREAM, bool PAST>
 __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(LayerNormBackward p, uint32_t sets) {
   constexpr int RPW = LNB_WAVES / WPR;  // rows of a workgroup
   __shared__ float sums[2][LNB_WAVES][2];
-  extern __shared__ __attribute__((aligned(16))) float joined[];  // [2][NL][8][64 WPR] if RPW > 1
+  extern __shared__ __attribute__((aligned(16))) float joined[];  // [RPW][2][512 NL WPR] if RPW > 1
   const int lane = threadIdx.x & 63, w = wave_id_uniform(), wk = w & (WPR - 1), sub = w / WPR;
   const int d = (int)p.d;
   const float inv_d = 1.0f / (float)d;
@@ -293,44 +295,32 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
     load(id + 2 * step, dy0, h0, mean0, rstd0);
     work(id + step, dy1, h1, mean1, rstd1, 1);
   }
-  if constexpr (RPW > 1) {  // the workgroup's rows, in order
-    for (int k = 1; k < RPW; ++k) {
-      __syncthreads();
-      float* const mine = joined + wk * 64 + lane;
-      if (sub == k) {
+  // The workgroup's rows in order: every wave leaves its sums in LDS, 16 x 8 KB in all.
+  float* const out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
+  constexpr int COLS = 512 * NL * WPR;
+  float* const to = RPW > 1 ? joined + sub * 2 * COLS : out;
+  const int64_t second = RPW > 1 ? COLS : p.d;
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
+  for (int i = 0; i < NL; ++i) {
+    const int col = (WPR * i + wk) * 512 + lane * 8;
+    if (col < d) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            mine[(i * 8 + j) * 64 * WPR] = dg[i][j];
-            mine[(NL * 8 + i * 8 + j) * 64 * WPR] = db[i][j];
-          }
-      }
-      __syncthreads();
-      if (sub == 0) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            dg[i][j] += mine[(i * 8 + j) * 64 * WPR];
-            db[i][j] += mine[(NL * 8 + i * 8 + j) * 64 * WPR];
-          }
+      for (int j = 0; j < 8; j += 4) {
+        *reinterpret_cast<float4*>(to + col + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+        *reinterpret_cast<float4*>(to + second + col + j) =
+            make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
       }
     }
   }
-  if (sub == 0) {
-    float* const out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
+  if constexpr (RPW > 1) {
+    __syncthreads();
+    for (int e = threadIdx.x * 4; e < 2 * COLS; e += 64 * LNB_WAVES * 4) {
+      const int half = e >= COLS ? 1 : 0, col = e - half * COLS;
+      if (col >= d) continue;
+      v4f sum = *reinterpret_cast<const v4f*>(joined + e);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int col = (WPR * i + wk) * 512 + lane * 8;
-      if (col < d) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          *reinterpret_cast<float4*>(out + col + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
-          *reinterpret_cast<float4*>(out + d + col + j) =
-              make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
-        }
-      }
+      for (int k = 1; k < RPW; ++k) sum = sum + *reinterpret_cast<const v4f*>(joined + k * 2 * COLS + e);
+      *reinterpret_cast<v4f*>(out + half * p.d + col) = sum;
     }
   }
 }
@@ -380,7 +370,7 @@ static int64_t ln_backward_grid(int64_t rows, int64_t d) {
 int64_t layernorm_backward_workspace(int64_t rows, int64_t d) { return ln_backward_grid(rows, d) * 2 * d * 4; }
 
 template <int NL, int WPR>
-constexpr int ln_backward_lds() { return WPR < LNB_WAVES ? 2 * NL * 8 * 64 * WPR * 4 : 0; }
+constexpr int ln_backward_lds() { return WPR < LNB_WAVES ? LNB_WAVES * 2 * 512 * NL * 4 : 0; }
 
 template <int NL, int WPR>
 static void launch_ln_backward(const LayerNormBackward& p, unsigned grid, uint32_t sets, hipStream_t stream) {
@@ -402,11 +392,19 @@ hipError_t set_layernorm_attributes() {
   auto allow = [&](const void* kernel, int lds) {
     if (e == hipSuccess) e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   };
-  constexpr int LDS = ln_backward_lds<LNB_NL, 8>();
-  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, true, true>, LDS);
-  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, true, false>, LDS);
-  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, false, true>, LDS);
-  allow((const void*)layernorm_backward_kernel<LNB_NL, 8, false, false>, LDS);
+  auto allow_all = [&](auto nl, auto wpr) {
+    constexpr int NL = decltype(nl)::value, WPR = decltype(wpr)::value, LDS = ln_backward_lds<NL, WPR>();
+    allow((const void*)layernorm_backward_kernel<NL, WPR, true, true>, LDS);
+    allow((const void*)layernorm_backward_kernel<NL, WPR, true, false>, LDS);
+    allow((const void*)layernorm_backward_kernel<NL, WPR, false, true>, LDS);
+    allow((const void*)layernorm_backward_kernel<NL, WPR, false, false>, LDS);
+  };
+  using std::integral_constant;
+  allow_all(integral_constant<int, 1>(), integral_constant<int, 1>());
+  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 1>());
+  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 2>());
+  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 4>());
+  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 8>());
   return e;
 }
 

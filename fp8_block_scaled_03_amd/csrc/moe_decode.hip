@@ -183,13 +183,13 @@ __device__ __forceinline__ void products(const uint8_t* const (&rows)[RT], const
 __device__ __forceinline__ Live slots_of(const Moe& m, int y, uint16_t* list) {
   const int lane = threadIdx.x & 63;
   const bool by_slot = m.slots < m.experts;
-  const int e = by_slot ? m.ids[y] : y;
-  Live r = {e, 0, 0, 0};
-  if (e < 0 || e >= m.experts) return r;
   int id[MOE_SLOTS / 64];
 #pragma unroll
   for (int i = 0; i < MOE_SLOTS / 64; ++i)
     if (i * 64 < m.slots) id[i] = m.ids[i * 64 + lane < m.slots ? i * 64 + lane : m.slots - 1];
+  const int e = by_slot ? m.ids[y] : y;
+  Live r = {e, 0, 0, 0};
+  if (e < 0 || e >= m.experts) return r;
   int first = -1;
 #pragma unroll
   for (int i = 0; i < MOE_SLOTS / 64; ++i) {

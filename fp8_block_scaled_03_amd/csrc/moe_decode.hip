@@ -33,6 +33,8 @@
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
 
+#include <type_traits>
+
 namespace fp8bs {
 
 constexpr int MOE_SLOTS = 512;     // most choices of a call
@@ -237,7 +239,7 @@ __device__ __forceinline__ void leave(Part<RT>& part, int w, const v4f (&acc)[RT
 
 // RT / 2 tiles of 16 gates and their ups, NT column tiles of 16 slots at a time; D K-blocks are
 // loaded at a time, WAVES of them share a SIMD.
-template <int RT, int NT, int D, int WAVES>
+template <int RT, int MOST, int WAVES>
 __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
   constexpr int G = RT / 2, ROWS = 16 * G;  // row tiles, and rows, of gates
   __shared__ uint16_t lists[MOE_WAVES][MOE_SLOTS];
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
     rows[r] = uniform_ptr(m.w1 + ((int64_t)v.expert * 2 * I + row) * H);
     scales[r] = m.s1[((int64_t)v.expert * nb + (row >> 7)) * KB + share.mine];
   }
-  for (int c0 = 0; c0 < v.count; c0 += 16 * NT) {
+  auto pass = [&](int c0, auto nt) __attribute__((always_inline)) {
+    constexpr int NT = decltype(nt)::value;
     uint32_t col[NT];
     v4f acc[RT][NT];
 #pragma unroll
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    products<RT, NT, D>(rows, scales, (const uint8_t*)m.x, col, share.kb0, share.kb1, H, acc);
+    products<RT, NT, (NT == 1 ? 2 : 1)>(rows, scales, (const uint8_t*)m.x, col, share.kb0, share.kb1, H, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (c0 + 16 * t >= v.count) break;
@@ -302,12 +305,21 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
         *reinterpret_cast<uint32_t*>(to + (int64_t)m.slots * I) = rest[0] | (rest[1] << 16);
       }
     }
+  };
+  for (int c0 = 0; c0 < v.count;) {
+    if (MOST == 1 || v.count - c0 <= 16) {
+      pass(c0, std::integral_constant<int, 1>());
+      c0 += 16;
+    } else {
+      pass(c0, std::integral_constant<int, MOST>());
+      c0 += 16 * MOST;
+    }
   }
 }
 
 // RT tiles of 16 columns of out, NT column tiles of 8 slots at a time: MFMA columns 0-7 are the slots' rounded y, columns 8-15 the
 // rests, whose sums join in the end.
-template <int RT, int NT, int D, int WAVES>
+template <int RT, int MOST, int WAVES>
 __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) {
   __shared__ __attribute__((aligned(16))) Part<RT> part;
   const int lane = threadIdx.x & 63, w = wave_id_uniform(), lo = lane & 15;
@@ -324,7 +336,8 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) 
     scales[r] = m.s2[((int64_t)v.expert * nb + (row >> 7)) * KB + share.mine];
   }
   const uint16_t* const list = m.list + v.start;
-  for (int c0 = 0; c0 < v.count; c0 += 8 * NT) {
+  auto pass = [&](int c0, auto nt) __attribute__((always_inline)) {
+    constexpr int NT = decltype(nt)::value;
     uint32_t col[NT];
     v4f acc[RT][NT];
 #pragma unroll
@@ -335,7 +348,7 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) 
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[r][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    products<RT, NT, D>(rows, scales, (const uint8_t*)m.y, col, share.kb0, share.kb1, I, acc);
+    products<RT, NT, (NT == 1 ? 2 : 1)>(rows, scales, (const uint8_t*)m.y, col, share.kb0, share.kb1, I, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (c0 + 8 * t >= v.count) break;
@@ -354,9 +367,17 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) 
         *reinterpret_cast<v4f*>(m.z + (int64_t)list[c] * m.hidden + n0 + 16 * r + 4 * q) = sum;
       }
     }
+  };
+  for (int c0 = 0; c0 < v.count;) {
+    if (MOST == 1 || v.count - c0 <= 8) {
+      pass(c0, std::integral_constant<int, 1>());
+      c0 += 8;
+    } else {
+      pass(c0, std::integral_constant<int, MOST>());
+      c0 += 8 * MOST;
+    }
   }
 }
-
 
 // Four columns of a token to a thread.
 __global__ void __launch_bounds__(256) moe_join_kernel(Moe m) {
@@ -426,14 +447,14 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   // 16, 8, 64 194, 186, -; 32, 8, 64 296, 270, -; 61, 8, 64 406, 340, 378; 61, 1, 64 111, 124, -; 61, 2, 8 92, 95, 87;
   // 61, 4, 8 138, 130, 104)
   if (m.slots < 2 * m.candidates) {
-    up(moe_up_kernel<2, 1, 2, 4>, 16);
-    down(moe_down_kernel<2, 1, 2, 4>, 32);
+    up(moe_up_kernel<2, 1, 4>, 16);
+    down(moe_down_kernel<2, 1, 4>, 32);
   } else if (m.slots < 12 * m.candidates) {
-    up(moe_up_kernel<4, 2, 1, 3>, 32);
-    down(moe_down_kernel<4, 2, 1, 3>, 64);
+    up(moe_up_kernel<4, 2, 3>, 32);
+    down(moe_down_kernel<4, 2, 3>, 64);
   } else {
-    up(moe_up_kernel<4, 4, 1, 2>, 32);
-    down(moe_down_kernel<4, 4, 1, 2>, 64);
+    up(moe_up_kernel<4, 4, 2>, 32);
+    down(moe_down_kernel<4, 4, 2>, 64);
   }
   hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((hidden / 4 + 255) / 256), (unsigned)tokens), dim3(256), 0, stream,
                      m);

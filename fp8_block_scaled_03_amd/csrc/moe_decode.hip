@@ -20,12 +20,15 @@
 //   join: every token adds its slots' sums, choices in order.
 // In the first two the waves share K (always a quarter each) and are joined in order in LDS.
 //
-// What bounds it is the weights' stream, and beside it what every workgroup reads of x
-// and y through its L2: that costs as much a byte (61 tokens, 64 experts of 4096 x 2048, top 8,
-// 16 gates to a workgroup: up 250 us, 190 without x; 16 columns: down 210 us, 88 without y).  So
-// with two slots and more to an expert a wave has 64 weight rows to a K-block of
-// values; fewer slots read little, and smaller tiles give more workgroups.  Waves that share rows of
-// y instead of K did not help (down 190): their reads do not meet in the L1.
+// What bounds it is the weights' stream (5.7 TB/s up to 32 tokens), and beside it what every
+// workgroup reads of x and y through its L2, which costs as much a byte, as if the lines that a
+// CU has asked for were the limit: 61 tokens, 64 experts of 4096 x 2048, top 8, 16 gates to a
+// workgroup: up 250 us, 190 without x, 200 with an x that the L1 holds; 16 columns: down 210,
+// 88, 120; as it is now 190 and 160, 138 and 97.  So with 1.5 slots and more to an expert a wave
+// has 64 weight rows to a K-block of values; fewer slots read little, and smaller tiles
+// give more workgroups.  Waves that share rows of y instead of K did not help (down 190): their
+// reads do not meet in the L1; nor did y by eight K of all slots, two lines to a load
+// (141; one token 16.7, not 14.7).
 //
 // No order depends on the other tokens: results are batch invariant.
 #include "activation.hpp"
@@ -237,8 +240,9 @@ __device__ __forceinline__ void leave(Part<RT>& part, int w, const v4f (&acc)[RT
   __syncthreads();
 }
 
-// RT / 2 tiles of 16 gates and their ups, NT column tiles of 16 slots at a time; D K-blocks are
-// loaded at a time, WAVES of them share a SIMD.
+// RT / 2 tiles of 16 gates and their ups; a pass has one column tile of 16 slots, or MOST of them;
+// WAVES share a SIMD.  Two K-blocks are loaded at a time, with several column tiles one
+// (more would cost waves).
 template <int RT, int MOST, int WAVES>
 __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
   constexpr int G = RT / 2, ROWS = 16 * G;  // row tiles, and rows, of gates
@@ -317,8 +321,9 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_up_kernel(Moe m) {
   }
 }
 
-// RT tiles of 16 columns of out, NT column tiles of 8 slots at a time: MFMA columns 0-7 are the slots' rounded y, columns 8-15 the
-// rests, whose sums join in the end.
+// RT tiles of 16 columns of out; a pass has one column tile of 8 slots, or MOST of them: MFMA
+// columns 0-7 are the slots' rounded y, columns 8-15 the rests, whose sums join in
+// the end.
 template <int RT, int MOST, int WAVES>
 __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) {
   __shared__ __attribute__((aligned(16))) Part<RT> part;
@@ -436,17 +441,14 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   m.y = (uint16_t*)take(4 * (int64_t)m.slots * inner);
   m.z = (float*)take(4 * (int64_t)m.slots * hidden);
   const dim3 threads(64 * MOE_WAVES);
-  auto up = [&](auto kernel, int rows) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((inner + rows - 1) / rows), (unsigned)m.candidates), threads, 0, stream, m);
-  };
-  auto down = [&](auto kernel, int rows) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((hidden + rows - 1) / rows), (unsigned)m.candidates), threads, 0, stream, m);
-  };
+  auto tiles = [&](int64_t n, int rows) { return dim3((unsigned)((n + rows - 1) / rows), (unsigned)m.candidates); };
+  auto up = [&](auto kernel, int rows) { hipLaunchKernelGGL(kernel, tiles(inner, rows), threads, 0, stream, m); };
+  auto down = [&](auto kernel, int rows) { hipLaunchKernelGGL(kernel, tiles(hidden, rows), threads, 0, stream, m); };
   // By the slots of an expert, on average if every one is taken (us a call, small, middle and large
-  // tiles, by tokens, top and experts of 4096 x 2048: 1, 8, 64 46.6, 52, -; 4, 8, 64 102, 117, -; 8, 8, 64 133, 149, -;
-  // 16, 8, 64 194, 186, -; 32, 8, 64 296, 270, -; 61, 8, 64 406, 340, 378; 61, 1, 64 111, 124, -; 61, 2, 8 92, 95, 87;
-  // 61, 4, 8 138, 130, 104)
-  if (m.slots < 2 * m.candidates) {
+  // tiles; 64 experts of 4096 x 2048, top 8, by tokens: 1 48.1, 48.3, 51.6; 2 65, 73, 79; 4 102, 107, 113; 8 132, 134,
+  // 140; 12 159, 156, 162; 16 181, 170, 182; 32 284, 251, 269; 61 442, 328, 329; 8 experts, top 2: 32 66, 58, 64; 61
+  // 104, 86, 78; top 4: 61 168, 129, 105)
+  if (2 * m.slots < 3 * m.candidates) {
     up(moe_up_kernel<2, 1, 4>, 16);
     down(moe_down_kernel<2, 1, 4>, 32);
   } else if (m.slots < 12 * m.candidates) {
@@ -456,8 +458,8 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
     up(moe_up_kernel<4, 4, 2>, 32);
     down(moe_down_kernel<4, 4, 2>, 64);
   }
-  hipLaunchKernelGGL(moe_join_kernel, dim3((unsigned)((hidden / 4 + 255) / 256), (unsigned)tokens), dim3(256), 0, stream,
-                     m);
+  const dim3 join((unsigned)((hidden / 4 + 255) / 256), (unsigned)tokens);
+  hipLaunchKernelGGL(moe_join_kernel, join, dim3(256), 0, stream, m);
   return hipGetLastError();
 }
 

@@ -60,7 +60,8 @@ def check(out, pre, ops, bias, act, res, rows, cols):
 
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (3, 272, 144), (17, 16, 528), (64, 80, 272), (130, 272, 400)])
-@pytest.mark.parametrize("with_bias,with_res,with_pre", [(True, True, True), (False, False, False), (True, False, True)])
+@pytest.mark.parametrize("with_bias,with_res,with_pre",
+                         [(True, True, True), (False, False, False), (True, False, True)])
 def test_within_the_bound(M, N, K, act, with_bias, with_res, with_pre):
     say(f"epilogue {M}x{N}x{K} {act} {with_bias} {with_res}")
     ops = operands(M * 7 + N + K, M, N, K)

@@ -155,7 +155,7 @@ def test_refusals():
     q1, s1, q2, s2 = w
     for bad in ((x[:2], ids, weights, *w), (x, ids[:, :1], weights, *w), (x, ids, weights[:2], *w),
                 (x, ids, weights, q1[:, :62], s1, q2, s2), (x, ids, weights, q1, s1[:, :0], q2, s2),
-                (x, ids, weights, q1, s1, q2[:1], s2), (x, ids, weights, q1, s1, q2, s2.t() if s2.dim() == 2 else s2[:1])):
+                (x, ids, weights, q1, s1, q2[:1], s2), (x, ids, weights, q1, s1, q2, s2[:1])):
         with pytest.raises(ValueError):
             fp8bs.moe_decode_b128(*bad)
     with pytest.raises(TypeError):

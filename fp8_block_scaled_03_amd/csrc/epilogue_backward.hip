@@ -16,6 +16,7 @@
 #include "column_sum.hpp"
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
+#include "stream.hpp"
 
 #include <type_traits>
 
@@ -61,8 +62,8 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* 
     const Scale sc = scale_of(row16_max(amax8(v)));
     const uint2 codes = __all(sc.r != 0.0f || !ok) ? codes8<true>(v, sc) : codes8<false>(v, sc);
     if (ok) {
-      if (dz != nullptr) *reinterpret_cast<uint4*>(dz + row * n + col) = bf16_round8(v);
-      put_codes8<LINES>(q + row * n + col, codes);
+      if (dz != nullptr) store_once<PAST>(dz + row * n + col, bf16_round8(v));
+      put_codes8<LINES && !PAST>(q + row * n + col, codes);
       if (piece == 0) scales[row * nb + cb] = sc.s;
     }
   }

@@ -14,7 +14,7 @@
 // each add up the partial sums, in the same order, so two launches do the whole.
 #include "common.hpp"
 #include "launch_layer.hpp"
-#include "quant_g128.hpp"
+#include "stream.hpp"
 
 namespace fp8bs {
 
@@ -43,8 +43,7 @@ __device__ __forceinline__ piece_t load_piece(const piece_t* p) {
   return load_once<PAST>(reinterpret_cast<const uint16_t*>(p));
 }
 __device__ __forceinline__ void store_piece(uint8_t* p, piece_t v) {  // (it is read in another step of the program)
-  typedef unsigned v4u __attribute__((ext_vector_type(4)));
-  __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p));
+  store_once<true>(reinterpret_cast<uint16_t*>(p), v);
 }
 struct __attribute__((packed, aligned(2))) loose_piece_t {
   uint32_t v[4];

@@ -26,6 +26,7 @@
 #include "column_sum.hpp"
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
+#include "stream.hpp"
 
 #include <type_traits>
 
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNo
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] += b[j];  // rounds to bf16 as the exact sum does
         hv[i] = bf16_round8(a);
-        if (p.h != nullptr && row_ok && col < d) *reinterpret_cast<uint4*>(p.h + at + col) = hv[i];
+        if (p.h != nullptr && row_ok && col < d) store_once<PAST>(p.h + at + col, hv[i]);
       }
     }
     float s = 0.0f, unused = 0.0f;
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
         if constexpr (STREAM) dy[j] = __builtin_fmaf(v, rstd, r[j]);
         else dy[j] = v * rstd;
       }
-      if (row_ok && col < d) *reinterpret_cast<uint4*>(out + col) = bf16_round8(dy);
+      if (row_ok && col < d) store_once<PAST>(out + col, bf16_round8(dy));
     }
   };
   uint4 dy0[NL], h0[NL], dy1[NL], h1[NL];

@@ -111,21 +111,6 @@ __device__ __forceinline__ uint4 bf16_round8(const float (&v)[8]) {
                     bf16_round_pair(v[6], v[7]));
 }
 
-// 16 bytes of an input that is read once; PAST: past the caches.  Inputs that together are beyond
-// what the 256 MB of Infinity Cache keep come faster so: 8192 x 8192 layer norm 121 us through
-// the caches, 101 past them, its gradient 111 and 99, an epilogue's gradient
-// (8192 x 16384, gelu) 201 and 189; smaller ones may still be there from the kernel
-// that wrote them (gradients of 2048 x 4096 20.9 and 22.6, 2048 x 8192 27.8 and 34.4).
-constexpr int64_t INPUTS_PAST = int64_t(192) << 20;  // bytes of a call's inputs
-
-template <bool PAST>
-__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
-  typedef unsigned v4u __attribute__((ext_vector_type(4)));
-  if constexpr (!PAST) return *reinterpret_cast<const uint4*>(p);
-  const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
 // Eight codes of a lane.  LINES: the rows of codes are multiples of 128, so each line
 // has one writer and is written past the caches; else neighbouring regions share
 // lines, and their writes meet in the L2 of the XCD that has the run of both.

@@ -167,6 +167,8 @@ def test_outputs_over_gradients_are_refused():
             fp8bs.clip_grad_norm(grads, 1.0, out=out)
     assert (g == 1).all()
     assert abs(float(fp8bs.grad_norm([g, g])) - np.sqrt(200.0)) < 1e-5  # a norm may count a tensor twice
+    one = torch.full((3, 5), 2.0, device=DEV)  # a tensor by itself
+    check_norm(fp8bs.clip_grad_norm(one, 1.0), [torch.full((3, 5), 2.0)])
     with pytest.raises(ValueError):
         fp8bs.clip_grad_norm([torch.ones(4, 6, device=DEV).t()], 1.0)
     with pytest.raises(ValueError):

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNo
     }
     row_sums<WPR>(dev, sq, w, sums[1]);
     const float delta = dev * inv_d;
-    const float var = fmaxf(__builtin_fmaf(-delta, delta, sq * inv_d), 0.0f);
+    const float var = __builtin_elementwise_maximum(__builtin_fmaf(-delta, delta, sq * inv_d), 0.0f);  // a NaN stays
     const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
     if (p.mean != nullptr && row_ok && lane == 0 && wk == 0) {
       p.mean[row] = m + delta;

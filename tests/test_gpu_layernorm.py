@@ -289,3 +289,23 @@ def test_graph_and_second_stream():
         there = step()
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(there, want))
+
+
+@pytest.mark.parametrize("rows,d", [(5, 64), (5, 1040), (3, 2064), (5, 8192), (3, 16384)])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_a_row_that_is_not_finite(rows, d, bad):
+    """Its own results are NaN, as the formula has them, and no other row's change."""
+    say(f"layernorm {rows}x{d} {bad}")
+    x, gamma, beta, dy = normal(1, rows, d), normal(2, d), normal(3, d), normal(4, rows, d)
+    good = fp8bs.layernorm_quantize_tg128(x, gamma, beta, EPS, want_y=True, want_stats=True)
+    good_dx = fp8bs.layernorm_backward(dy, x, gamma, *good[3:])[0]
+    x[1, d // 2] = float(bad)
+    got = fp8bs.layernorm_quantize_tg128(x, gamma, beta, EPS, want_y=True, want_stats=True)
+    y, rstd = got[2], got[4]
+    assert torch.isnan(y[1]).all() and torch.isnan(rstd[1])
+    assert torch.equal(got[0][1:2], fp8bs.quantize_tg128(y[1:2].contiguous())[0])
+    keep = [r for r in range(rows) if r != 1]
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, good))
+    dx, dgamma, dbeta = fp8bs.layernorm_backward(dy, x, gamma, *got[3:])
+    assert torch.isnan(dx[1]).all() and torch.equal(dx[keep], good_dx[keep])
+    assert torch.isnan(dgamma).all() and torch.isfinite(dbeta).all()

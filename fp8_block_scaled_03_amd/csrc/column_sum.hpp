@@ -17,7 +17,7 @@ static __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __
                                                                  float* __restrict__ second, bool accumulate) {
   __shared__ float sums[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t c = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + lane;
   float s = 0.0f;
   if (c < n) {
     const float* const p = partial + c;
@@ -36,8 +36,10 @@ static __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __
 
 static inline void launch_column_sum(const float* partial, unsigned parts, int64_t n, int64_t split, float* first,
                                      float* second, bool accumulate, hipStream_t stream) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, stream, partial, (int)parts, n,
-                     split, first, second, accumulate);
+  const int64_t blocks = (n + 63) / 64;
+  const unsigned x = (unsigned)(blocks < 65536 ? blocks : 65536);  // (a grid side holds fewer than 2^32 threads)
+  hipLaunchKernelGGL(column_sum_kernel, dim3(x, (unsigned)((blocks + x - 1) / x)), dim3(1024), 0, stream, partial,
+                     (int)parts, n, split, first, second, accumulate);
 }
 
 }  // namespace fp8bs

@@ -91,6 +91,16 @@ def test_epilogue_backward(rows, n, act):
     assert ((dbias.double() - want).abs() <= (2.0 ** -8 + (rows / 4 / slabs + slabs + 8) * U) * size).all()
 
 
+@pytest.mark.parametrize("rows,n", [(3, 64 * 65536 + 80), (1, (1 << 28) + 2064)])
+def test_sums_over_many_columns(rows, n):
+    say(f"epilogue_backward {rows}x{n}")
+    dout = rows_of(n // 16, 16, 1).view(1, n).repeat(rows, 1)
+    old = torch.ones(n, device=DEV)
+    dbias = fp8bs.epilogue_backward_quantize_tg128(dout, None, dbias=old, accumulate=True)[3]
+    want = dout[0].float() * rows  # exact: at most three times eight bits; the addition of 1 rounds
+    assert torch.equal(dbias, want + 1.0)
+
+
 @pytest.mark.parametrize("M,N", [(66001, 65552)])
 def test_product_with_epilogue_past_32_bits(M, N):
     K = 16

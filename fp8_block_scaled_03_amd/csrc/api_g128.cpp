@@ -101,6 +101,7 @@ fp8bs_status fp8bs_gemm_tg128_nt_epilogue(const void* a, const float* sa, const 
   fp8bs_status st = check_gemm(a, sa, bt, sbt, c_bf16, M, N, K);
   if (st != FP8BS_OK || M == 0 || N == 0) return st;
   if (!aligned(bias_bf16, 16) || !aligned(residual_bf16, 16) || !aligned(pre_bf16, 16)) return FP8BS_EALIGN;
+  if (pre_bf16 != nullptr && (pre_bf16 == c_bf16 || pre_bf16 == residual_bf16)) return FP8BS_EINVAL;
   st = ensure_attributes();
   if (st != FP8BS_OK) return st;
   const fp8bs::Epilogue e = {(const uint16_t*)bias_bf16, (const uint16_t*)residual_bf16, (uint16_t*)pre_bf16,

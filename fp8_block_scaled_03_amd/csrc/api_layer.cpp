@@ -86,15 +86,17 @@ fp8bs_status check_grads(const void* const* grads, void* const* outs, bool clips
   return FP8BS_OK;
 }
 
-// Does a tensor that is written overlap another one?  (outs[i] == grads[i] is one tensor.)
+// Does a tensor that is written overlap another one?  (outs[i] == grads[i] is one tensor.)  The
+// norm is one more, read or written while tensors are.
 bool overlapping(const void* const* grads, void* const* outs, const int64_t* counts, const int32_t* types,
-                 int32_t n) {
+                 int32_t n, const float* norm, bool norm_written) {
   struct Span {
     uintptr_t begin, end;
     bool written;
   };
   std::vector<Span> spans;
-  spans.reserve(2 * (size_t)n);
+  spans.reserve(2 * (size_t)n + 1);
+  spans.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, norm_written});
   for (int32_t i = 0; i < n; ++i) {
     if (counts[i] == 0) continue;
     const uintptr_t bytes = (uintptr_t)counts[i] * (types[i] == FP8BS_F32 ? 4 : 2);
@@ -113,13 +115,13 @@ bool overlapping(const void* const* grads, void* const* outs, const int64_t* cou
 }
 
 fp8bs_status check_clip(const void* const* grads, void* const* outs, const int64_t* counts, const int32_t* types,
-                        int32_t n, double max_norm, double eps, const float* norm) {
+                        int32_t n, double max_norm, double eps, const float* norm, bool norm_written) {
   const fp8bs_status st = check_grads(grads, outs, true, counts, types, n);
   if (st != FP8BS_OK) return st;
   if (!(max_norm >= 0) || !(eps >= 0) || std::isinf(max_norm) || std::isinf(eps) || !norm) return FP8BS_EINVAL;
   if (!aligned(norm, 4)) return FP8BS_EALIGN;
   try {
-    if (overlapping(grads, outs, counts, types, n)) return FP8BS_EINVAL;
+    if (overlapping(grads, outs, counts, types, n, norm, norm_written)) return FP8BS_EINVAL;
   } catch (...) {  // no host memory
     return FP8BS_EHIP;
   }
@@ -222,7 +224,7 @@ fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, c
     if (!aligned(p, 16)) return FP8BS_EALIGN;
   for (const void* p : {(const void*)ids_dev, (const void*)weights, (const void*)s1, (const void*)s2})
     if (!aligned(p, 4)) return FP8BS_EALIGN;
-  st = check_workspace(workspace, workspace_bytes, 
+  st = check_workspace(workspace, workspace_bytes,
                        fp8bs_moe_decode_b128_workspace(tokens, top, experts, hidden, inner));
   if (st != FP8BS_OK) return st;
   return from_launch(fp8bs::launch_moe_decode(x_bf16, ids_dev, weights, w1, s1, w2, s2, residual_bf16, out_bf16,
@@ -246,7 +248,7 @@ fp8bs_status fp8bs_grad_norm(const void* const* grads, const int64_t* counts, co
 fp8bs_status fp8bs_clip_grads(const void* const* grads, void* const* outs, const int64_t* counts,
                               const int32_t* types, int32_t n, const float* norm, double max_norm, double eps,
                               void* stream) {
-  const fp8bs_status st = check_clip(grads, outs, counts, types, n, max_norm, eps, norm);
+  const fp8bs_status st = check_clip(grads, outs, counts, types, n, max_norm, eps, norm, false);
   if (st != FP8BS_OK) return st;
   return from_launch(fp8bs::launch_clip_grads({grads, outs, counts, types, n}, max_norm, eps,
                                               const_cast<float*>(norm), nullptr, (hipStream_t)stream));
@@ -255,7 +257,7 @@ fp8bs_status fp8bs_clip_grads(const void* const* grads, void* const* outs, const
 fp8bs_status fp8bs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts,
                                   const int32_t* types, int32_t n, double max_norm, double eps, float* norm,
                                   void* workspace, int64_t workspace_bytes, void* stream) {
-  fp8bs_status st = check_clip(grads, outs, counts, types, n, max_norm, eps, norm);
+  fp8bs_status st = check_clip(grads, outs, counts, types, n, max_norm, eps, norm, true);
   if (st == FP8BS_OK) st = check_workspace(workspace, workspace_bytes, fp8bs_grad_norm_workspace(n));
   if (st != FP8BS_OK) return st;
   return from_launch(fp8bs::launch_clip_grads({grads, outs, counts, types, n}, max_norm, eps, norm,

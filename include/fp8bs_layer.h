@@ -88,6 +88,7 @@ fp8bs_status fp8bs_layernorm_backward(const void* dy_bf16, const void* h_bf16, c
  *   bias [N] bf16 or NULL, activation one of FP8BS_ACT_* (else FP8BS_EINVAL)
  *   residual [M, N] bf16 or NULL; may be c itself (in place)
  *   c [M, N] bf16 out; pre [M, N] bf16 out or NULL, apart from the other arguments
+ *      (c or residual itself: FP8BS_EINVAL)
  *   The activation is fp32 arithmetic, off by at most 2^-15 of its result, whose
  *   magnitudes below 2^-118 may come out as 0; an exact zero is stored as +0.
  *   Results are batch invariant as fp8bs_gemm_tg128_nt's.
@@ -167,7 +168,7 @@ fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, c
  *   lost; an infinity gives an infinite norm, a NaN a NaN.
  *   grads  n device pointers, in a host array that is read before the call returns
  *          (so are the next two); each aligned to its type, NULL where the count is 0
- *   counts n numbers of values, >= 0 and at most 2^40
+ *   counts n numbers of values, >= 0 (else FP8BS_EINVAL) and at most 2^36 (else FP8BS_ESHAPE)
  *   types  n types, FP8BS_F32 or FP8BS_BF16 (else FP8BS_EINVAL)
  *   n      0 .. FP8BS_MAX_TENSORS (else FP8BS_EINVAL); without values the norm is 0
  *   norm   one fp32 on the device, out
@@ -183,7 +184,7 @@ fp8bs_status fp8bs_grad_norm(const void* const* grads, const int64_t* counts, co
  *   one that several processes have joined).
  *   outs   n device pointers of g's types and counts.  outs[i] is grads[i] (in
  *          place; a factor of 1 then writes nothing) or overlaps no tensor of the call;
- *          tensors that are written overlap no other one (else FP8BS_EINVAL)
+ *          tensors that are written overlap no other one, and norm none (else FP8BS_EINVAL)
  *   norm   one fp32 on the device.  An infinite norm makes the factor 0, a NaN makes
  *          it NaN, as the formula has it.
  *   max_norm, eps  finite, >= 0 (else FP8BS_EINVAL)
@@ -194,7 +195,8 @@ fp8bs_status fp8bs_clip_grads(const void* const* grads, void* const* outs, const
 
 /*
  * fp8bs_clip_grad_norm - both: the norm, out as by fp8bs_grad_norm, and the clipping
- *   with that norm before it is rounded to fp32.  workspace as for fp8bs_grad_norm.
+ *   with that norm before it is rounded to fp32.  norm overlaps no tensor of the call (else
+ *   FP8BS_EINVAL); workspace as for fp8bs_grad_norm.
  */
 fp8bs_status fp8bs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* counts,
                                   const int32_t* types, int32_t n, double max_norm, double eps, float* norm,

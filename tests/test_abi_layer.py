@@ -105,6 +105,9 @@ def test_epilogue_refusals():
     for i in (1, 3):
         assert with_(**{f"_{i}": A4 + 2}) == EALIGN
 
+    for same in (A16 + 256, A16 + 512):  # z stored over the result or over the residual
+        assert with_(_6=A16 + 256, _7=A16 + 512, _8=same) == EINVAL
+
 
 def test_epilogue_backward_refusals():
     lib = binding.load_library()
@@ -200,6 +203,15 @@ def test_clip_refusals():
     assert _clip([A16], [A16 + 4], [4], [0]) == EINVAL
     assert _clip([A16, far], [far, far + 64], [4, 4], [0, 0]) == EINVAL
     assert _clip([A16, A16 + 16], [far, far + 8], [4, 4], [0, 0]) == EINVAL
+
+
+def test_norm_inside_a_gradient_is_refused():
+    for norm in (A16, A16 + 12):
+        assert _clip([A16], [A16], [4], [0], norm=norm) == EINVAL
+        assert _clip([A16 + 64], [A16], [4], [0], norm=norm) == EINVAL
+    p, c, t = _arrays([A16], [4], [0])
+    o = (ctypes.c_void_p * 1)(A16 + 64)
+    assert binding.clip_grad_norm_raw(p, o, c, t, 1, 1.0, 0.0, A16 + 4, A16, 1 << 20) == EINVAL  # written, and read
 
 
 def test_gradient_lists_are_checked_without_gpu():

@@ -147,6 +147,11 @@ __device__ __forceinline__ void store_wave_rows(uint16_t* c, int64_t N, const v4
 // sub-tile.  The residual is read, and results are written, as C is without an
 // epilogue (16 bytes a lane, whole lines where there are); the exchanges between
 // lanes that lead there are their own inverse.
+//
+// Nothing overlaps it but the next tile's first loads, so it costs its instructions and its
+// traffic: 8192 x 16384 x 4096 455 us, gelu 485 (21 issue slots a value), silu 469, then pre
+// 25 (268 MB more) or a residual 50; 1017 x 2064 x 1552 12.1, with bias, gelu and pre
+// 15.3.  All residual rows asked for before the bias (small tiles) gained nothing.
 struct NoEpilogue {};
 
 enum ActivationCode { CODE_CLAMP, CODE_GATED, CODE_GELU };  // what the loops over a tile are compiled for

@@ -15,7 +15,10 @@
 // Row mapping: WPR waves hold a row, lane l of wave k the columns
 // 512 (WPR i + k) + 8 l .. +7, i < NL <= 4: 16 lanes hold a group of 128.  Sums run
 // over a lane's columns in order, over lanes by a butterfly, over waves in order: a
-// row's results depend on that row and on d only.
+// row's results depend on that row and on d only, so the mapping goes by d.  Forward a row
+// has up to eight waves before a lane has a second piece: few rows are latency (us with
+// twice to four times the pieces, and so: 8 x 8192 6.5 and 4.9, 8 x 2048 5.7 and 3.8, 512 x 4096 7.4
+// and 5.6; but 32768 x 1024 40.2 and 41.3).  Sixteen waves are slower (8192 x 8192 95, not 83).
 //
 // dgamma and dbeta: a workgroup walks every gridDim.x-th set of rows and keeps
 // its columns' sums in registers, joins its rows' sums in LDS and writes them once
@@ -34,11 +37,26 @@ namespace fp8bs {
 
 constexpr int LN_NL = 4, LN_MAX_WPR = 8;
 
-// Sum over the lanes of a wave, in every lane.
+// Sum over the lanes of a wave, in every lane: turns within 16 lanes, then the two exchanges
+// of rows of 16 and of halves (through LDS, as __shfl_xor goes, 8 x 8192 takes 0.4 us more).
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  auto turned = [](float x, auto by) __attribute__((always_inline)) {
+    constexpr int ROW_ROR = 0x120 + decltype(by)::value;
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ROW_ROR, 0xF, 0xF,
+                                                                     true));
+  };
+  v = turned(v, std::integral_constant<int, 8>());
+  v = turned(v, std::integral_constant<int, 4>());
+  v = turned(v, std::integral_constant<int, 2>());
+  v = turned(v, std::integral_constant<int, 1>());
+  auto both = [](auto pair) __attribute__((always_inline)) {
+    const uint32_t a = pair[0], b = pair[1];
+    return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+  };
+  uint32_t x = __builtin_bit_cast(uint32_t, v);
+  v = both(__builtin_amdgcn_permlane16_swap(x, x, false, false));
+  x = __builtin_bit_cast(uint32_t, v);
+  return both(__builtin_amdgcn_permlane32_swap(x, x, false, false));
 }
 
 // Two sums over a row's WPR waves, of which this is wave wk of the workgroup's wave
@@ -350,10 +368,10 @@ hipError_t launch_layernorm(const void* x, const void* residual, const void* gam
                        (uint16_t*)h,       (uint16_t*)y,              (uint8_t*)q,            scales,
                        mean,               rstd,                      rows,                   d, eps};
   if (d <= 512) launch_ln<1, 1>(p, stream);
-  else if (d <= 1024) launch_ln<2, 1>(p, stream);
-  else if (d <= 2048) launch_ln<4, 1>(p, stream);
-  else if (d <= 4096) launch_ln<4, 2>(p, stream);
-  else if (d <= 8192) launch_ln<4, 4>(p, stream);
+  else if (d <= 1024) launch_ln<1, 2>(p, stream);
+  else if (d <= 2048) launch_ln<1, 4>(p, stream);
+  else if (d <= 4096) launch_ln<1, 8>(p, stream);
+  else if (d <= 8192) launch_ln<2, 8>(p, stream);
   else launch_ln<4, 8>(p, stream);
   return hipGetLastError();
 }

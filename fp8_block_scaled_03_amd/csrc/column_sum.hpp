@@ -15,14 +15,20 @@ static __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __
                                                                  int64_t n, int64_t split,
                                                                  float* __restrict__ first,
                                                                  float* __restrict__ second, bool accumulate) {
+  constexpr int AHEAD = 8;  // loads in flight, without conditions (255 parts: the last seven one by one 1.5 us more)
   __shared__ float sums[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t c = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 64 + lane;
   float s = 0.0f;
   if (c < n) {
     const float* const p = partial + c;
-#pragma unroll 8
-    for (int k = w; k < parts; k += 16) s += p[k * n];
+    for (int k0 = w; k0 < parts; k0 += 16 * AHEAD) {
+      float v[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) v[i] = p[(k0 + 16 * i < parts ? k0 + 16 * i : k0) * n];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) s += k0 + 16 * i < parts ? v[i] : 0.0f;
+    }
   }
   sums[w][lane] = s;
   __syncthreads();

@@ -376,14 +376,20 @@ hipError_t launch_layernorm(const void* x, const void* residual, const void* gam
   return hipGetLastError();
 }
 
-// Sets of rows (what a workgroup takes at once) and workgroups of the backward pass.
+// Sets of rows (what a workgroup takes at once: up to eight waves hold a row before a lane has a
+// second piece) and workgroups of the backward pass.  A workgroup takes four rows at
+// least, as long as that leaves 128 of them, since its partial sums are as much traffic as
+// two to three rows (us with one set each, and so: 500 x 4096 11.4 and 9.7, 500 x 8192 15.5 and
+// 14.6, 300 x 12288 19.5 and 17.4).
 static int64_t ln_sets(int64_t rows, int64_t d) {
-  const int wpr = d <= 1024 ? 1 : d <= 2048 ? 2 : d <= 4096 ? 4 : d <= 8192 ? 8 : 16, rpw = LNB_WAVES / wpr;
+  const int wpr = d <= 512 ? 1 : d <= 1024 ? 2 : d <= 2048 ? 4 : d <= 8192 ? 8 : 16, rpw = LNB_WAVES / wpr;
   return (rows + rpw - 1) / rpw;
 }
 static int64_t ln_backward_grid(int64_t rows, int64_t d) {
-  const int64_t sets = ln_sets(rows, d);
-  return sets < 256 ? sets : 256;
+  const int64_t sets = ln_sets(rows, d), fours = (rows + 3) / 4;
+  const int64_t want = fours < 128 ? 128 : fours < 256 ? fours : 256;
+  const int64_t turns = (sets + want - 1) / want;
+  return turns ? (sets + turns - 1) / turns : 0;  // the same number of sets to each but the last
 }
 
 int64_t layernorm_backward_workspace(int64_t rows, int64_t d) { return ln_backward_grid(rows, d) * 2 * d * 4; }
@@ -420,9 +426,9 @@ hipError_t set_layernorm_attributes() {
   };
   using std::integral_constant;
   allow_all(integral_constant<int, 1>(), integral_constant<int, 1>());
-  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 1>());
-  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 2>());
-  allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 4>());
+  allow_all(integral_constant<int, 1>(), integral_constant<int, 2>());
+  allow_all(integral_constant<int, 1>(), integral_constant<int, 4>());
+  allow_all(integral_constant<int, 1>(), integral_constant<int, 8>());
   allow_all(integral_constant<int, LNB_NL>(), integral_constant<int, 8>());
   return e;
 }
@@ -437,9 +443,9 @@ hipError_t launch_layernorm_backward(const void* dy, const void* h, const void* 
   const unsigned grid = (unsigned)ln_backward_grid(rows, d);
   if (grid > 0) {
     if (d <= 512) launch_ln_backward<1, 1>(p, grid, sets, stream);
-    else if (d <= 1024) launch_ln_backward<LNB_NL, 1>(p, grid, sets, stream);
-    else if (d <= 2048) launch_ln_backward<LNB_NL, 2>(p, grid, sets, stream);
-    else if (d <= 4096) launch_ln_backward<LNB_NL, 4>(p, grid, sets, stream);
+    else if (d <= 1024) launch_ln_backward<1, 2>(p, grid, sets, stream);
+    else if (d <= 2048) launch_ln_backward<1, 4>(p, grid, sets, stream);
+    else if (d <= 4096) launch_ln_backward<1, 8>(p, grid, sets, stream);
     else if (d <= 8192) launch_ln_backward<LNB_NL, 8>(p, grid, sets, stream);
     else launch_ln_backward<LNB_NL, 16>(p, grid, sets, stream);
   }

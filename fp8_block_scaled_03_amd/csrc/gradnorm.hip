@@ -5,7 +5,7 @@
 // Squares and sums are 64-bit: a bf16 or fp32 square neither overflows nor
 // vanishes there, and the sum of 2^30 values is right to fp32's last bit.
 //
-// A tensor is cut into chunks of CHUNK bytes from the 16-byte boundary at or before
+// A tensor is cut into chunks of 8 or 32 KB from the 16-byte boundary at or before
 // its first value, so that every 16-byte piece but a tensor's first and last is whole
 // and aligned.  A launch takes up to TABLE tensors, whose addresses and first
 // chunks are kernel arguments (nothing is copied to the device, so a captured graph
@@ -19,8 +19,14 @@
 namespace fp8bs {
 
 constexpr int TABLE = 96;
-constexpr int64_t CHUNK = 32768;
 constexpr int GRAD_GRID = 1024;
+// Pieces of 16 bytes that a thread has of a chunk.  While 8 KB a workgroup are enough for all, more
+// workgroups share the latency; above, larger chunks have more loads in flight (us in a graph, norm and
+// clipping, 32 KB and 8 KB: 61 x 4096 values 9.1 and 6.3, 61 x 20000 9.7 and 7.9; 61 x 50000 11.2 and 11.5,
+// 403 M 820 and 954).
+constexpr int FEW = 2, MANY = 8;
+constexpr int64_t chunk_bytes(int pieces) { return int64_t(256) * 16 * pieces; }
+constexpr int64_t SMALL_LIST = GRAD_GRID * chunk_bytes(FEW);  // bytes of all gradients
 constexpr int64_t JOIN_MAX = 4096;  // partial sums that every workgroup of the clipping kernel adds up by itself
 
 struct GradTable {
@@ -82,9 +88,10 @@ __device__ __forceinline__ void add_squares(piece_t v, bool bf16, double (&acc)[
   }
 }
 
-template <bool PAST>
+template <bool PAST, int P>
 __global__ void __launch_bounds__(256) grad_sumsq_kernel(GradTable t, uint32_t chunks, double* __restrict__ partial) {
   __shared__ double lds[4];
+  constexpr int64_t CHUNK = chunk_bytes(P);
   double acc[2] = {0.0, 0.0};
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int k = tensor_of(t, c);
@@ -95,14 +102,14 @@ __global__ void __launch_bounds__(256) grad_sumsq_kernel(GradTable t, uint32_t c
     const int64_t at = (int64_t)(c - t.first[k]) * CHUNK;
     const uint8_t* const q = p - lead + at;
     if (at >= lead && at + CHUNK <= end) {
-      piece_t v[8];
+      piece_t v[P];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = load_piece<PAST>(reinterpret_cast<const piece_t*>(q) + i * 256 + threadIdx.x);
+      for (int i = 0; i < P; ++i) v[i] = load_piece<PAST>(reinterpret_cast<const piece_t*>(q) + i * 256 + threadIdx.x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) add_squares(v[i], bf16, acc);
+      for (int i = 0; i < P; ++i) add_squares(v[i], bf16, acc);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < P; ++i) {
         const int off = (i * 256 + threadIdx.x) * 16;
         if (at + off >= lead && at + off + 16 <= end) {
           add_squares(*reinterpret_cast<const piece_t*>(q + off), bf16, acc);
@@ -155,11 +162,12 @@ __device__ __forceinline__ piece_t scaled(piece_t v, bool bf16, float f) {
 }
 
 // n partial sums, or (partial null) the norm at norm_in.
-template <bool PAST>
+template <bool PAST, int P>
 __global__ void __launch_bounds__(256) clip_kernel(GradTable t, uint32_t chunks, const double* __restrict__ partial,
                                                    int n, const float* __restrict__ norm_in, double max_norm,
                                                    double eps, float* __restrict__ norm_out) {
   __shared__ double lds[4];
+  constexpr int64_t CHUNK = chunk_bytes(P);
   const double norm = partial ? __builtin_sqrt(join(partial, n, lds)) : (double)*norm_in;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double wanted = max_norm / (norm + eps);
@@ -178,18 +186,18 @@ __global__ void __launch_bounds__(256) clip_kernel(GradTable t, uint32_t chunks,
     uint8_t* const o = d - lead + at;
     const bool even = ((uintptr_t)o & 15) == 0;
     if (at >= lead && at + CHUNK <= end) {
-      piece_t v[8];
+      piece_t v[P];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = load_piece<PAST>(reinterpret_cast<const piece_t*>(q) + j * 256 + threadIdx.x);
+      for (int j = 0; j < P; ++j) v[j] = load_piece<PAST>(reinterpret_cast<const piece_t*>(q) + j * 256 + threadIdx.x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < P; ++j) {
         const piece_t r = scaled(v[j], bf16, f);
         const int64_t off = (j * 256 + threadIdx.x) * 16;
         if (even) store_piece(o + off, r);
         else *reinterpret_cast<loose_piece_t*>(o + off) = loose_piece_t{{r.x, r.y, r.z, r.w}};
       }
     } else {
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < P; ++j) {
         const int off = (j * 256 + threadIdx.x) * 16;
         const int step = bf16 ? 2 : 4;
         if (even && at + off >= lead && at + off + 16 <= end) {
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(256) clip_kernel(GradTable t, uint32_t chunks,
 // The workspace: the joined total, one unused, then GRAD_GRID partial sums for each launch.
 int64_t grad_norm_workspace(int n) { return 8 * (2 + (int64_t)((n + TABLE - 1) / TABLE) * GRAD_GRID); }
 
-static uint32_t fill_table(const Grads& g, int first, GradTable& t) {
+static uint32_t fill_table(const Grads& g, int first, int64_t chunk, GradTable& t) {
   uint32_t chunks = 0;
   for (int i = 0; i < TABLE; ++i) {
     const int k = first + i;
@@ -223,7 +231,7 @@ static uint32_t fill_table(const Grads& g, int first, GradTable& t) {
     t.n[i] = count;
     t.bf16[i] = k < g.n && g.types[k] == 1;
     t.first[i] = chunks;
-    if (count > 0) chunks += (uint32_t)((((uintptr_t)t.src[i] & 15) + count * (t.bf16[i] ? 2 : 4) + CHUNK - 1) / CHUNK);
+    if (count > 0) chunks += (uint32_t)((((uintptr_t)t.src[i] & 15) + count * (t.bf16[i] ? 2 : 4) + chunk - 1) / chunk);
   }
   t.first[TABLE] = chunks;
   return chunks;
@@ -239,11 +247,14 @@ static int64_t grad_bytes(const Grads& g) {
 
 // Partial sums of all tensors at workspace + 2; their number.
 static int64_t launch_sumsq(const Grads& g, double* workspace, hipStream_t stream) {
-  const auto kernel = grad_bytes(g) > NORM_PAST ? grad_sumsq_kernel<true> : grad_sumsq_kernel<false>;
+  const int64_t bytes = grad_bytes(g);
+  const bool few = bytes <= SMALL_LIST;
+  const auto kernel = few ? grad_sumsq_kernel<false, FEW>
+                          : bytes > NORM_PAST ? grad_sumsq_kernel<true, MANY> : grad_sumsq_kernel<false, MANY>;
   int64_t used = 0;
   for (int first = 0; first < g.n; first += TABLE) {
     GradTable t;
-    const uint32_t chunks = fill_table(g, first, t);
+    const uint32_t chunks = fill_table(g, first, chunk_bytes(few ? FEW : MANY), t);
     if (chunks == 0) continue;
     const unsigned grid = grad_grid(chunks);
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, t, chunks, workspace + 2 + used);
@@ -274,10 +285,13 @@ hipError_t launch_clip_grads(const Grads& g, double max_norm, double eps, float*
       norm_out = nullptr;
     }
   }
-  const auto kernel = grad_bytes(g) > CLIP_PAST ? clip_kernel<true> : clip_kernel<false>;
+  const int64_t bytes = grad_bytes(g);
+  const bool few = bytes <= SMALL_LIST;
+  const auto kernel =
+      few ? clip_kernel<false, FEW> : bytes > CLIP_PAST ? clip_kernel<true, MANY> : clip_kernel<false, MANY>;
   for (int first = (g.n - 1) / TABLE * TABLE; first >= 0 && g.n > 0; first -= TABLE) {
     GradTable t;
-    const uint32_t chunks = fill_table(g, first, t);
+    const uint32_t chunks = fill_table(g, first, chunk_bytes(few ? FEW : MANY), t);
     if (chunks == 0) continue;
     hipLaunchKernelGGL(kernel, dim3(grad_grid(chunks)), dim3(256), 0, stream, t, chunks, partial, (int)used,
                        (const float*)norm, max_norm, eps, norm_out);

@@ -14,9 +14,9 @@
 // comparing all ids, one ballot for 64 of them.  MFMA columns are a candidate's slots,
 // 16 at a time; rows are 16 rows of the weight.
 //
-//   up: a workgroup of four waves takes 16 or 32 gates and the ups that belong to them; y goes to the
+//   up: a workgroup of four waves takes 16, 32 or 64 gates and the ups that belong to them; y goes to the
 //     workspace.  The first workgroup of a candidate also leaves its expert and slots there.
-//   down: a workgroup takes 32 or 64 columns of out for one candidate; its slots' sums go to the workspace.
+//   down: a workgroup takes 32, 64 or 128 columns of out for one candidate; its slots' sums go to the workspace.
 //   join: every token adds its slots' sums, choices in order.
 // In the first two the waves share K (always a quarter each) and are joined in order in LDS.
 //
@@ -24,9 +24,9 @@
 // workgroup reads of x and y through its L2, which costs as much a byte, as if the lines that a
 // CU has asked for were the limit: 61 tokens, 64 experts of 4096 x 2048, top 8, 16 gates to a
 // workgroup: up 250 us, 190 without x, 200 with an x that the L1 holds; 16 columns: down 210,
-// 88, 120; as it is now 190 and 160, 138 and 97.  So with 1.5 slots and more to an expert a wave
-// has 64 weight rows to a K-block of values; fewer slots read little, and smaller tiles
-// give more workgroups.  Waves that share rows of y instead of K did not help (down 190): their
+// 88, 120; with 64 weight rows to a K-block of values 190 and 160, 138 and 97; with 128 173 and
+// 128.  So many slots of an expert take large tiles; few read little, and smaller tiles give
+// more workgroups.  Waves that share rows of y instead of K did not help (down 190): their
 // reads do not meet in the L1; nor did y by eight K of all slots, two lines to a load
 // (141; one token 16.7, not 14.7).
 //
@@ -444,20 +444,27 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   auto tiles = [&](int64_t n, int rows) { return dim3((unsigned)((n + rows - 1) / rows), (unsigned)m.candidates); };
   auto up = [&](auto kernel, int rows) { hipLaunchKernelGGL(kernel, tiles(inner, rows), threads, 0, stream, m); };
   auto down = [&](auto kernel, int rows) { hipLaunchKernelGGL(kernel, tiles(hidden, rows), threads, 0, stream, m); };
-  // By the slots of an expert, on average if every one is taken (us a call, small, middle and large
-  // tiles; 64 experts of 4096 x 2048, top 8, by tokens: 1 48.1, 48.3, 51.6; 2 65, 73, 79; 4 102, 107, 113; 8 132, 134,
-  // 140; 12 159, 156, 162; 16 181, 170, 182; 32 284, 251, 269; 61 442, 328, 329; 8 experts, top 2: 32 66, 58, 64; 61
-  // 104, 86, 78; top 4: 61 168, 129, 105)
-  if (2 * m.slots < 3 * m.candidates) {
-    up(moe_up_kernel<2, 1, 4>, 16);
-    down(moe_down_kernel<2, 1, 4>, 32);
-  } else if (m.slots < 12 * m.candidates) {
-    up(moe_up_kernel<4, 2, 3>, 32);
-    down(moe_down_kernel<4, 2, 3>, 64);
-  } else {
-    up(moe_up_kernel<4, 4, 2>, 32);
-    down(moe_down_kernel<4, 4, 2>, 64);
-  }
+  // By the slots of an expert, on average if every one is taken (us a call, tiles of 32, 64 and 64
+  // weight rows, the last with twice the slots a pass; 64 experts of 4096 x 2048, top 8, by tokens: 1 48.1, 48.3, 51.6;
+  // 2 65, 73, 79; 4 102, 107, 113; 8 132, 134, 140; 12 159, 156, 162; 16 181, 170, 182; 32 284, 251, 269; 61 442, 328,
+  // 329; 8 experts, top 2: 32 66, 58, 64; 61 104, 86, 78; top 4: 61 168, 129, 105).
+  // 128 weight rows halve what is read of x and y once more, but take registers for two waves a SIMD
+  // (us, 64 rows and 128: 64 experts, top 8, by tokens: 16 234, 245; 32 262, 261; 48 284, 277; 61 318, 296; 32 experts:
+  // 40 165, 155; 61 230, 206; 16 experts: 32 122, 111; 61 173, 189 (the weights come twice); 8 experts of 4096 x 14336, top
+  // 2, 61 358, 314), and fewer than two workgroups to a CU are slower (8 experts of 4096 x 2048, top 2: 24 48,
+  // 52; top 4: 61 92, 108).
+  const bool few = 2 * m.slots < 3 * m.candidates, many = m.slots >= 12 * m.candidates;
+  auto large = [&](int64_t tiles) {
+    return m.slots >= 5 * m.candidates && m.slots < 20 * m.candidates && tiles * m.candidates >= 512;
+  };
+  if (few) up(moe_up_kernel<2, 1, 4>, 16);
+  else if (large(inner / 64)) up(moe_up_kernel<8, 2, 2>, 64);
+  else if (many) up(moe_up_kernel<4, 4, 2>, 32);
+  else up(moe_up_kernel<4, 2, 3>, 32);
+  if (few) down(moe_down_kernel<2, 1, 4>, 32);
+  else if (large(hidden / 128)) down(moe_down_kernel<8, 2, 2>, 128);
+  else if (many) down(moe_down_kernel<4, 4, 2>, 64);
+  else down(moe_down_kernel<4, 2, 3>, 64);
   const dim3 join((unsigned)((hidden / 4 + 255) / 256), (unsigned)tokens);
   hipLaunchKernelGGL(moe_join_kernel, join, dim3(256), 0, stream, m);
   return hipGetLastError();

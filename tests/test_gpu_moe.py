@@ -61,7 +61,8 @@ def check(out, x, ids, weights, weights_of, residual=None):
 
 CASES = [(1, 1, 1, 16, 16), (1, 2, 4, 48, 80), (3, 2, 4, 144, 272), (5, 1, 7, 1040, 528), (17, 2, 3, 272, 144),
          (1, 8, 64, 512, 640), (33, 4, 8, 128, 256), (64, 8, 16, 256, 128), (61, 8, 12, 400, 1168), (2, 6, 300, 64, 48),
-         (64, 2, 2, 128, 2576), (100, 5, 9, 64, 64), (512, 1, 3, 32, 16), (1, 512, 5, 64, 32), (256, 2, 1024, 16, 16)]
+         (64, 2, 2, 128, 2576), (100, 5, 9, 64, 64), (512, 1, 3, 32, 16), (1, 512, 5, 64, 32), (256, 2, 1024, 16, 16),
+         (25, 2, 8, 80, 4112), (61, 2, 8, 8272, 48), (40, 3, 8, 144, 4176)]
 
 
 @pytest.mark.parametrize("T,k,E,H,inner", CASES)
@@ -123,6 +124,19 @@ def test_tokens_do_not_depend_on_the_batch(E, k):
     order = torch.randperm(T).to(DEV)
     mixed = fp8bs.moe_decode_b128(x[order], ids[order], weights[order], *w, residual=res[order])
     assert torch.equal(mixed.view(torch.int16), full[order].view(torch.int16))
+
+
+@pytest.mark.parametrize("T,k,E,H,inner", [(25, 2, 8, 80, 4112), (61, 2, 8, 8272, 48)])
+def test_a_token_alone_where_tiles_are_large(T, k, E, H, inner):
+    say(f"moe invariance {T} {H} {inner}")
+    w = layer(31, E, H, inner)
+    x = normal(32, T, H)
+    ids, weights = choices(33, T, k, E)
+    out = fp8bs.moe_decode_b128(x, ids, weights, *w)
+    for t in (0, 7, T - 1):
+        at = slice(t, t + 1)
+        one = fp8bs.moe_decode_b128(x[at], ids[at], weights[at], *w)
+        assert torch.equal(one.view(torch.int16), out[at].view(torch.int16)), t
 
 
 def test_not_finite_reaches_its_token_only():

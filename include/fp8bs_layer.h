@@ -42,7 +42,8 @@ extern "C" {
  *   no defined result.  d % 16 == 0, d <= 16384, rows <= 2^30 (else FP8BS_ESHAPE);
  *   rows == 0 or d == 0: no-op.  Matrices, gamma and beta are 16-byte aligned, scales
  *   and statistics 4-byte (else FP8BS_EALIGN).  A row's results depend on that row
- *   only.  Outputs other than h overlap no input.
+ *   only.  The squares are fp32 ones: deviations from the mean of 2^62 and more are beyond
+ *   their range.  Outputs other than h overlap no input, and none another one.
  */
 fp8bs_status fp8bs_layernorm_quantize_tg128(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
                                             const void* beta_bf16, float eps, int64_t rows, int64_t d, void* h_bf16,
@@ -90,7 +91,8 @@ fp8bs_status fp8bs_layernorm_backward(const void* dy_bf16, const void* h_bf16, c
  *   c [M, N] bf16 out; pre [M, N] bf16 out or NULL, apart from the other arguments
  *      (c or residual itself: FP8BS_EINVAL)
  *   The activation is fp32 arithmetic, off by at most 2^-15 of its result, whose
- *   magnitudes below 2^-118 may come out as 0; an exact zero is stored as +0.
+ *   magnitudes below 2^-118 may come out as 0; an exact zero is stored as +0.  At z = -inf
+ *   gelu is 0, its limit; gelu_tanh and silu are NaN, as their formulas have it.
  *   Results are batch invariant as fp8bs_gemm_tg128_nt's.
  */
 fp8bs_status fp8bs_gemm_tg128_nt_epilogue(const void* a, const float* sa, const void* bt, const float* sbt,
@@ -104,7 +106,7 @@ fp8bs_status fp8bs_gemm_tg128_nt_epilogue(const void* a, const float* sa, const 
  *     dz     = dout * act'(pre)  (fp32), rounded to bf16 (for the weight gradient)
  *     q, scales = the row quantizer's rule of fp8bs_g128.h on the fp32 dz
  *     dbias  = sum over the rows of the fp32 dz
- *   relu's derivative at 0 is 0.
+ *   relu's derivative at 0 is 0, a derivative at an infinite z its limit.
  *   dout [rows, n] bf16, pre [rows, n] bf16 (the forward call's; with FP8BS_ACT_NONE
  *   it is not read and may be NULL), dz [rows, n] bf16 out or NULL, q [rows, n] E4M3
  *   out, scales [rows, ceil128(n)] fp32 out
@@ -113,6 +115,7 @@ fp8bs_status fp8bs_gemm_tg128_nt_epilogue(const void* a, const float* sa, const 
  *   workspace of fp8bs_epilogue_backward_workspace(rows, n) bytes (else
  *   FP8BS_EINVAL); not used without dbias.
  *   n % 16 == 0, rows and n at most 2^30 (else FP8BS_ESHAPE); n == 0: no-op.
+ *   Outputs overlap no input, and none another one.
  */
 int64_t fp8bs_epilogue_backward_workspace(int64_t rows, int64_t n);
 fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const void* pre_bf16, int32_t activation,
@@ -141,7 +144,7 @@ fp8bs_status fp8bs_epilogue_backward_quantize_tg128(const void* dout_bf16, const
  *   s1 [experts, ceil128(2 inner), ceil128(hidden)] fp32
  *   w2 [experts, hidden, inner] E4M3, s2 [experts, ceil128(hidden), ceil128(inner)] fp32
  *   residual [tokens, hidden] bf16 or NULL; may be out itself (in place)
- *   out [tokens, hidden] bf16 out
+ *   out [tokens, hidden] bf16 out, apart from the other arguments
  *   1 <= top and 1 <= experts <= FP8BS_MAX_GROUPS (else FP8BS_EINVAL);
  *   tokens * top <= FP8BS_MAX_MOE_CHOICES, hidden and inner multiples of 16, hidden <=
  *   32768, 16 <= inner <= 32768 (else FP8BS_ESHAPE); tokens == 0 or hidden == 0: no-op.
@@ -179,8 +182,8 @@ fp8bs_status fp8bs_grad_norm(const void* const* grads, const int64_t* counts, co
                              float* norm, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * fp8bs_clip_grads - out = g * min(1, max_norm / (norm + eps)), each product
- *   rounded once to g's type, from a norm that is on the device (fp8bs_grad_norm's, or
+ * fp8bs_clip_grads - out = g * min(1, max_norm / (norm + eps)), the factor rounded to
+ *   fp32, each product to fp32 and from there to g's type, from a norm that is on the device (fp8bs_grad_norm's, or
  *   one that several processes have joined).
  *   outs   n device pointers of g's types and counts.  outs[i] is grads[i] (in
  *          place; a factor of 1 then writes nothing) or overlaps no tensor of the call;

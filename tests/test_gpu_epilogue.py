@@ -156,6 +156,24 @@ def test_not_finite_stays_in_its_column():
         assert torch.isfinite(out[:, keep].float()).all() and torch.isnan(pre[:, 100]).all()
 
 
+def test_minus_infinity():
+    """relu and gelu have their limit 0, the products z sigma(z) a NaN; what stands beside is left alone."""
+    say("-inf")
+    ops = dev(operands(9, 21, 272, 144))
+    bias = normal(7, 272)
+    bias[33] = float("-inf")
+    for act in ACTS:
+        out, pre = fp8bs.gemm_tg128_nt_epilogue(*ops, bias=bias, activation=act, want_pre=True)
+        assert (pre[:, 33] == float("-inf")).all(), act
+        if act == "none":
+            assert (out[:, 33] == float("-inf")).all()
+        elif act in ("relu", "gelu"):
+            assert (out[:, 33].view(torch.int16) == 0).all(), act
+        else:
+            assert torch.isnan(out[:, 33]).all(), act
+        assert torch.isfinite(out[:, [n for n in range(272) if n != 33]].float()).all(), act
+
+
 def test_refusals_and_empty():
     say("refusals")
     a, sa, bt, sbt = dev(operands(7, 5, 32, 64))

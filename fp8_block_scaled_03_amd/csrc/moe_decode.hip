@@ -18,7 +18,8 @@
 //     workspace.  The first workgroup of a candidate also leaves its expert and slots there.
 //   down: a workgroup takes 32, 64 or 128 columns of out for one candidate; its slots' sums go to the workspace.
 //   join: every token adds its slots' sums, choices in order.
-// In the first two the waves share K (always a quarter each) and are joined in order in LDS.
+// In the first two the waves share K (always a quarter each) and are joined in order in LDS.  For one
+// token of few choices a workgroup has all of them for its columns, down and join in one.
 //
 // What bounds it is the weights' stream (5.7 TB/s up to 32 tokens), and beside it what every
 // workgroup reads of x and y through its L2, which costs as much a byte, as if the lines that a
@@ -384,6 +385,73 @@ __global__ void __launch_bounds__(64 * MOE_WAVES, WAVES) moe_down_kernel(Moe m) 
   }
 }
 
+// Four columns of a token's sum, the residual added.
+__device__ __forceinline__ void store_token(const Moe& m, int t, int col, v4f acc) {
+  const int64_t at = (int64_t)t * m.hidden + col;
+  if (m.residual != nullptr) {
+    const uint2 r = *reinterpret_cast<const uint2*>(m.residual + at);
+    acc = acc + v4f{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
+  }
+  *reinterpret_cast<uint2*>(m.out + at) =
+      make_uint2(bf16_round_pair(acc[0] + 0.0f, acc[1] + 0.0f), bf16_round_pair(acc[2] + 0.0f, acc[3] + 0.0f));
+}
+
+// Down and join for one token of at most S choices, 16 RT columns of out: four waves to a choice, each
+// a quarter of K (MFMA columns 0-7 the slot's rounded y, 8-15 its rests).  The same sums in the
+// same order as in the two kernels that it stands for: quarters, then choices.
+template <int S, int RT>
+__global__ void __launch_bounds__(64 * S * MOE_WAVES) moe_token_kernel(Moe m) {
+  constexpr int QUADS = 4 * RT;  // of columns
+  __shared__ __attribute__((aligned(16))) float part[S][MOE_WAVES][2][QUADS][4];  // y and its rests apart
+  __shared__ __attribute__((aligned(16))) float sums[S][QUADS][4];
+  const int lane = threadIdx.x & 63, w = wave_id_uniform(), g = lane >> 4, lo = lane & 15;
+  const int n0 = blockIdx.x * 16 * RT, s = w / MOE_WAVES, quarter = w % MOE_WAVES;
+  const int I = m.inner, KB = (I + 127) >> 7, nb = (m.hidden + 127) >> 7;
+  const int mine = lane < m.top ? lane : m.top - 1;  // lane c has choice c
+  const int id = lane < m.top ? m.ids[mine] : -1;
+  const float weight = m.weights[mine];
+  const int e = __builtin_amdgcn_readlane(id, s);
+  if (e >= 0 && e < m.experts) {
+    const Share share(quarter, KB);
+    const uint32_t col[1] = {(uint32_t)((lo >> 3) * m.slots + s) * (uint32_t)I * 2};
+    const uint8_t* rows[RT];
+    float scales[RT];
+    v4f acc[RT][1];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {  // behind hidden: the first tile again
+      const int row = n0 + (n0 + 16 * r < m.hidden ? 16 * r : 0);
+      rows[r] = uniform_ptr(m.w2 + ((int64_t)e * m.hidden + row) * I);
+      scales[r] = m.s2[((int64_t)e * nb + (row >> 7)) * KB + share.mine];
+      acc[r][0] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    products<RT, 1, 2>(rows, scales, (const uint8_t*)m.y, col, share.kb0, share.kb1, I, acc);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      if ((lo & 7) == 0) *reinterpret_cast<v4f*>(part[s][quarter][lo >> 3][4 * r + g]) = acc[r][0];
+  }
+  __syncthreads();
+  if (w > 0) return;
+  if (lane < QUADS * S) {  // (of a choice that is skipped the sums mean nothing, and are not used)
+    const int c = lane / QUADS, q = lane % QUADS;
+    v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < MOE_WAVES; ++k) {
+      const v4f one = *reinterpret_cast<const v4f*>(part[c][k][0][q]) + *reinterpret_cast<const v4f*>(part[c][k][1][q]);
+      sum = k == 0 ? one : sum + one;
+    }
+    *reinterpret_cast<v4f*>(sums[c][q]) = sum;
+  }
+  __builtin_amdgcn_wave_barrier();  // the lanes' sums are there for every lane
+  v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int c = 0; c < S; ++c) {
+    const int of = __builtin_amdgcn_readlane(id, c);
+    const float by = lane_value(weight, c);
+    if (of >= 0 && of < m.experts) promote(acc, *reinterpret_cast<const v4f*>(sums[c][lane % QUADS]), by);
+  }
+  if (lane < QUADS && n0 + 4 * lane < m.hidden) store_token(m, 0, n0 + 4 * lane, acc);
+}
+
 // Four columns of a token to a thread.
 __global__ void __launch_bounds__(256) moe_join_kernel(Moe m) {
   const int quads = m.hidden / 4, q = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
@@ -405,13 +473,7 @@ __global__ void __launch_bounds__(256) moe_join_kernel(Moe m) {
     for (int j = 0; j < J; ++j)
       if (j0 + j < m.top && id[j] >= 0 && id[j] < m.experts) promote(acc, z[j], w[j]);
   }
-  const int64_t at = (int64_t)t * m.hidden + 4 * q;
-  if (m.residual != nullptr) {
-    const uint2 r = *reinterpret_cast<const uint2*>(m.residual + at);
-    acc = acc + v4f{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
-  }
-  *reinterpret_cast<uint2*>(m.out + at) =
-      make_uint2(bf16_round_pair(acc[0] + 0.0f, acc[1] + 0.0f), bf16_round_pair(acc[2] + 0.0f, acc[3] + 0.0f));
+  store_token(m, t, 4 * q, acc);
 }
 
 static int moe_candidates(int slots, int experts) { return slots < experts ? slots : experts; }
@@ -461,6 +523,23 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   else if (large(inner / 64)) up(moe_up_kernel<8, 2, 2>, 64);
   else if (many) up(moe_up_kernel<4, 4, 2>, 32);
   else up(moe_up_kernel<4, 2, 3>, 32);
+  // One token with few choices: down and join in one, 32 columns from hidden 5120 on (us in a graph, three
+  // kernels and two: 8 experts of 4096 x 14336, top 2, 74.4 and 63.9; of 4096 x 2048, top 1 19.6 and 16.5, top 2 21.7
+  // and 18.6; of 512 x 256, top 2 9.3 and 7.5; 64 of 4096 x 2048, top 4 26.9 and 25.2; 8 of 8192 x 2048, top 2 31.2
+  // and 28.7, with 16 columns 29.8; 16 of 7168 x 2048, top 4 37.0 and 34.8, 38.3).  More choices, or three and
+  // four of few columns, gain nothing or lose: a workgroup reads y for fewer columns, and workgroups
+  // are few (64 of 4096 x 2048, top 8 42.2 and 41.6, two tokens 70 and 73; 2048 x 4096, top 8 43 and 52; 8 of
+  // 1024 x 4096, top 4 22 and 24).
+  if (few && tokens == 1 && (top <= 2 || (top <= 4 && hidden >= 4096))) {
+    auto token = [&](auto kernel, int choices, int columns) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((hidden + columns - 1) / columns)), dim3(64 * MOE_WAVES * choices), 0,
+                         stream, m);
+    };
+    const bool wide = hidden >= 5120;
+    if (top <= 2) wide ? token(moe_token_kernel<2, 2>, 2, 32) : token(moe_token_kernel<2, 1>, 2, 16);
+    else wide ? token(moe_token_kernel<4, 2>, 4, 32) : token(moe_token_kernel<4, 1>, 4, 16);
+    return hipGetLastError();
+  }
   if (few) down(moe_down_kernel<2, 1, 4>, 32);
   else if (large(hidden / 128)) down(moe_down_kernel<8, 2, 2>, 128);
   else if (many) down(moe_down_kernel<4, 4, 2>, 64);

@@ -211,3 +211,42 @@ def test_graph_follows_the_choices_and_second_stream():
         there = fp8bs.moe_decode_b128(x, ids, weights, *w)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(there.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("k,E,H,inner", [(1, 8, 144, 272), (1, 1, 5152, 16), (2, 8, 5136, 528), (2, 3, 48, 4112),
+                                         (3, 64, 4112, 144), (3, 5, 8208, 16), (4, 16, 4096, 1040), (4, 9, 5136, 80),
+                                         (4, 9, 4080, 80), (5, 9, 4112, 272)])
+def test_one_token_of_few_choices(k, E, H, inner):
+    """A token alone (its choices' sums joined in the second kernel, where there are few): in its bound, and the bits
+    that it has in a batch; skipped and repeated choices, weights that are not used, the residual in place."""
+    say(f"moe one token {k} {E} {H} {inner}")
+    w = layer(51, E, H, inner)
+    x, res = normal(52, 2, H), normal(53, 2, H)
+    ids, weights = choices(54, 2, k, E)
+    for kind in ("all", "skipped", "repeated", "none"):
+        if kind == "skipped":
+            ids[0, k - 1] = -1 if k < 3 else E
+            weights[0, k - 1] = float("nan")  # not used
+        elif kind == "repeated":
+            ids[0] = E - 1
+            weights[0] = torch.arange(1, k + 1, device=DEV) * 0.25
+        elif kind == "none":
+            ids[0] = torch.tensor([-1, E, 2 ** 31 - 1, -2 ** 31, -7][:k])
+        for residual in (None, res):
+            one = residual[:1].clone() if residual is not None else None
+            both = fp8bs.moe_decode_b128(x, ids, weights, *w, residual=residual)
+            out = fp8bs.moe_decode_b128(x[:1], ids[:1], weights[:1], *w, residual=one, out=one)
+            assert torch.equal(out.view(torch.int16), both[:1].view(torch.int16)), kind
+            used = torch.where((ids[:1] >= 0) & (ids[:1] < E), weights[:1], torch.zeros_like(weights[:1]))
+            check(out, x[:1], ids[:1], used, w, None if residual is None else residual[:1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fp8bs.moe_decode_b128(x[:1], ids[:1], weights[:1], *w)
+    for seed in (55, 56, 57):
+        new, given = choices(seed, 2, k, E)
+        ids.copy_(new)
+        weights.copy_(given)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = fp8bs.moe_decode_b128(x, ids, weights, *w)[:1]
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), seed

@@ -154,6 +154,19 @@ __device__ __forceinline__ void store_wave_rows(uint16_t* c, int64_t N, const v4
 // 15.3.  All residual rows asked for before the bias (small tiles) gained nothing.
 struct NoEpilogue {};
 
+// The result's pointer.  With an epilogue the residual may be the result itself, so that no
+// promise of an only access can be given; without one nothing else is there.
+template <typename E>
+struct ResultPointer {
+  typedef uint16_t* type;
+};
+template <>
+struct ResultPointer<NoEpilogue> {
+  typedef uint16_t* __restrict__ type;
+};
+template <typename E>
+using result_t = typename ResultPointer<E>::type;
+
 enum ActivationCode { CODE_CLAMP, CODE_GATED, CODE_GELU };  // what the loops over a tile are compiled for
 
 // What does not depend on the element: none and relu are max(z, low) with low = -inf and 0
@@ -312,7 +325,7 @@ __device__ __forceinline__ void epilogue_wave(const Epilogue& e, uint16_t* c, in
 template <int MI, int NJ, int WM, int WN, int S, bool GROUPED, typename E>
 __global__ void __launch_bounds__(64 * WM * WN) gemm_g128_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
-    const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
+    const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, result_t<E> c, int64_t M,
     int64_t N, int64_t K, uint32_t tiles_n, E epilogue) {
   constexpr int BM = 16 * MI * WM, BN = 16 * NJ * WN, WAVES = WM * WN;
   constexpr int STAGE = (BM + BN) * GK;
@@ -587,7 +600,7 @@ constexpr int X_LDS = X_S + 2 * X_SBUF;
 template <bool GROUPED, typename E>
 __global__ void __launch_bounds__(XTHREADS) gemm_g128_big_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ bt,
-    const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, uint16_t* __restrict__ c, int64_t M,
+    const float* __restrict__ sbt, const int32_t* __restrict__ offsets, int G, result_t<E> c, int64_t M,
     int64_t N, int64_t K, uint32_t tiles_n, uint32_t tiles, E epilogue) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   typedef __attribute__((address_space(3))) unsigned char lds_u8;
@@ -961,8 +974,8 @@ __global__ void __launch_bounds__(256) gemm_g128_rows_kernel(const uint8_t* __re
                                                              const float* __restrict__ sa,
                                                              const uint8_t* __restrict__ bt,
                                                              const float* __restrict__ sbt,
-                                                             uint16_t* __restrict__ c, int64_t M, int64_t N,
-                                                             int64_t K, E epilogue) {
+                                                             result_t<E> c, int64_t M, int64_t N, int64_t K,
+                                                             E epilogue) {
   __shared__ __attribute__((aligned(16))) float part[2][RKC][256];
   __shared__ float sprod[2][RKC][16];
   const int lane = threadIdx.x & 63;

@@ -30,7 +30,6 @@ hipError_t launch_layernorm_backward(const void* dy, const void* h, const void* 
                                      float* dgamma, float* dbeta, bool accumulate, float* workspace,
                                      hipStream_t stream);
 hipError_t set_layernorm_attributes();
-int moe_max_slots();
 int64_t moe_decode_workspace(int tokens, int top, int experts, int64_t hidden, int64_t inner);
 hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* weights, const void* w1,
                              const float* s1, const void* w2, const float* s2, const void* residual, void* out,

@@ -34,6 +34,7 @@
 // No order depends on the other tokens: results are batch invariant.
 #include "activation.hpp"
 #include "common.hpp"
+#include "fp8bs_layer.h"
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
 
@@ -41,7 +42,8 @@
 
 namespace fp8bs {
 
-constexpr int MOE_SLOTS = 512;     // most choices of a call
+constexpr int MOE_SLOTS = FP8BS_MAX_MOE_CHOICES;  // what a call may have, so what lists and lanes hold
+static_assert(MOE_SLOTS % 64 == 0 && MOE_SLOTS <= 65536, "whole waves of ids, slots of 16 bits");
 constexpr int MOE_WAVES = 4;       // of a workgroup; they share K
 
 // What a candidate stands for, as the first kernel leaves it for the second.
@@ -477,7 +479,6 @@ __global__ void __launch_bounds__(256) moe_join_kernel(Moe m) {
 }
 
 static int moe_candidates(int slots, int experts) { return slots < experts ? slots : experts; }
-int moe_max_slots() { return MOE_SLOTS; }
 
 int64_t moe_decode_workspace(int tokens, int top, int experts, int64_t hidden, int64_t inner) {
   const int64_t slots = (int64_t)tokens * top, candidates = moe_candidates((int)slots, experts);

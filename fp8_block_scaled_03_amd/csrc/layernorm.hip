@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
   const int lane = threadIdx.x & 63, w = wave_id_uniform(), wk = w & (WPR - 1), sub = w / WPR;
   const int d = (int)p.d;
   const float inv_d = 1.0f / (float)d;
-  int at_col[NL];  // columns past d read column 0 (gamma is 0 there, their sums are not stored)
+  int at_col[NL];  // columns past d read column 0 (which may be infinite: they are left out of the row's sums)
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
     const int col = (WPR * i + wk) * 512 + lane * 8;
@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       if (!row_ok) break;
+      const float before1 = s1, before2 = s2;
       float dy[8], h[8], g[8];
       unpack8(dyv[i], dy);
       unpack8(hv[i], h);
@@ -275,6 +276,9 @@ __global__ void __launch_bounds__(64 * LNB_WAVES) layernorm_backward_kernel(Laye
         db[i][j] += dy[j];
         dg[i][j] = __builtin_fmaf(dy[j], xh, dg[i][j]);
       }
+      const bool in = (WPR * i + wk) * 512 + lane * 8 < d;
+      s1 = in ? s1 : before1;
+      s2 = in ? s2 : before2;
     }
     row_sums<WPR>(s1, s2, w, sums[turn]);
     const float c1 = s1 * inv_d, c2 = s2 * inv_d;

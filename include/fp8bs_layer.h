@@ -42,8 +42,10 @@ extern "C" {
  *   no defined result.  d % 16 == 0, d <= 16384, rows <= 2^30 (else FP8BS_ESHAPE);
  *   rows == 0 or d == 0: no-op.  Matrices, gamma and beta are 16-byte aligned, scales
  *   and statistics 4-byte (else FP8BS_EALIGN).  A row's results depend on that row
- *   only.  The squares are fp32 ones: deviations from the mean of 2^62 and more are beyond
- *   their range.  Outputs other than h overlap no input, and none another one.
+ *   only.  The sums are fp32 ones: a row whose values, or whose squared deviations from
+ *   the mean, add up to 2^128 or more is beyond their range (deviations of 2^57 throughout a
+ *   row of 16384, of 2^62 throughout one of 16), and with an eps next to 0 deviations below
+ *   2^-63 lose digits.  Outputs other than h overlap no input, and none another one.
  */
 fp8bs_status fp8bs_layernorm_quantize_tg128(const void* x_bf16, const void* residual_bf16, const void* gamma_bf16,
                                             const void* beta_bf16, float eps, int64_t rows, int64_t d, void* h_bf16,

@@ -232,7 +232,9 @@ fp8bs_status fp8bs_moe_decode_b128(const void* x_bf16, const int32_t* ids_dev, c
                                               (hipStream_t)stream));
 }
 
-int64_t fp8bs_grad_norm_workspace(int32_t n) { return fp8bs::grad_norm_workspace(n > 0 ? n : 0); }
+int64_t fp8bs_grad_norm_workspace(int32_t n) {
+  return n < 0 || n > FP8BS_MAX_TENSORS ? 0 : fp8bs::grad_norm_workspace(n);
+}
 
 fp8bs_status fp8bs_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* types, int32_t n,
                              float* norm, void* workspace, int64_t workspace_bytes, void* stream) {

@@ -8,8 +8,9 @@
 // With t = |z| and phi(t) = exp(-t^2 / 2) / sqrt(2 pi):
 //   Phi(-t) = exp(-t^2 / 2) Q(t),  Q(t) = exp(t^2 / 2) erfc(t / sqrt 2) / 2,
 // and Q, which falls from 1/2 to 0.4 / t, is a polynomial of degree 8 in
-// u = 1 / (1 + 0.264 t) (fitted here to the least relative error on [0, 14.5]: 0.3 x 2^-24
-// in exact arithmetic, 4.4 x 2^-24 with fp32's roundings): far values keep their digits.
+// u = 1 / (1 + 0.264 t) (fitted here to the least relative error on [0, 14.5]: 0.75 x 2^-24
+// in exact arithmetic with the coefficients as fp32 holds them, at most 9.5 x 2^-24 with fp32's
+// roundings and a reciprocal that is off by its last bit): far values keep their digits.
 //   gelu' = Phi(z) + z phi(z) = S for z < 0 and 1 - S else,
 //   S = exp(-t^2 / 2) (Q(t) - t / sqrt(2 pi)).
 #pragma once

@@ -10,8 +10,8 @@
 // launch adds the slabs' sums in order.  Slabs depend on the sizes only.  The next
 // set's loads are in flight while one is worked on.
 //
-// Bound by HBM traffic (7 bytes a value, 5 without z), for gelu nearly as much by the
-// VALU: about 45 issue slots a value.
+// Bound by HBM traffic (7 bytes a value, 5 without z; 8192 x 16384, gelu, 168 us, 5.6 TB/s), for
+// gelu nearly as much by the VALU: about 45 issue slots a value.  Few rows are latency (the slabs below).
 #include "activation.hpp"
 #include "column_sum.hpp"
 #include "launch_layer.hpp"
@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(256) epilogue_backward_kernel(const uint16_t* 
 }
 
 // At least eight sets of four rows to a slab, so that the partial sums are few beside
-// the rows, and at most 8192 waves in all, which fill the chip.
+// the rows, and at most 8192 waves in all, which fill the chip.  With few rows the sets are walked one
+// after another by few waves (in a graph, gelu: 8 x 8192 6.0 us, 256 x 4096 12.3, 1017 x 2064 13.5, of
+// which two launches are 4.8).
 static int64_t epilogue_slabs(int64_t rows, int64_t n) {
   const int64_t sets = (rows + 3) / 4, nb = (n + 127) / 128;
   const int64_t most = nb < 8192 ? 8192 / nb : 1, want = (sets + 7) / 8;

@@ -149,9 +149,10 @@ __device__ __forceinline__ void store_wave_rows(uint16_t* c, int64_t N, const v4
 // lanes that lead there are their own inverse.
 //
 // Nothing overlaps it but the next tile's first loads, so it costs its instructions and its
-// traffic: 8192 x 16384 x 4096 455 us, gelu 485 (21 issue slots a value), silu 469, then pre
-// 25 (268 MB more) or a residual 50; 1017 x 2064 x 1552 12.1, with bias, gelu and pre
-// 15.3.  All residual rows asked for before the bias (small tiles) gained nothing.
+// traffic.  In one run: 8192 x 16384 x 4096 454 us, with bias 465, silu 484, gelu 503 (21 issue
+// slots a value), gelu and pre 540 (268 MB more), bias and residual 530; 1017 x 2064 x 1552
+// 12.9, with bias 14.0, gelu and pre 16.3, silu and residual 15.6; 8 x 8192 x 8192 13.9, with
+// bias and residual 14.7.  All residual rows asked for before the bias (small tiles) gained nothing.
 struct NoEpilogue {};
 
 // The result's pointer.  With an epilogue the residual may be the result itself, so that no

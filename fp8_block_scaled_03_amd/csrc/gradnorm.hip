@@ -22,8 +22,8 @@ constexpr int TABLE = 96;
 constexpr int GRAD_GRID = 1024;
 // Pieces of 16 bytes that a thread has of a chunk.  While 8 KB a workgroup are enough for all, more
 // workgroups share the latency; above, larger chunks have more loads in flight (us in a graph, norm and
-// clipping, 32 KB and 8 KB: 61 x 4096 values 9.1 and 6.3, 61 x 20000 9.7 and 7.9; 61 x 50000 11.2 and 11.5,
-// 403 M 820 and 954).
+// clipping into other tensors, one list again and again, 32 KB and 8 KB: 61 x 4096 values 9.2 and 6.4, 61 x 20000
+// 9.7 and 7.9, 61 x 50000 11.4 and 11.5, 403 M 842 and 969; in place 61 x 20000 11.4 and 10.2).
 constexpr int FEW = 2, MANY = 8;
 constexpr int64_t chunk_bytes(int pieces) { return int64_t(256) * 16 * pieces; }
 constexpr int64_t SMALL_LIST = GRAD_GRID * chunk_bytes(FEW);  // bytes of all gradients

@@ -21,15 +21,16 @@
 // In the first two the waves share K (always a quarter each) and are joined in order in LDS.  For one
 // token of few choices a workgroup has all of them for its columns, down and join in one.
 //
-// What bounds it is the weights' stream (5.7 TB/s up to 32 tokens), and beside it what every
-// workgroup reads of x and y through its L2, which costs as much a byte, as if the lines that a
-// CU has asked for were the limit: 61 tokens, 64 experts of 4096 x 2048, top 8, 16 gates to a
-// workgroup: up 250 us, 190 without x, 200 with an x that the L1 holds; 16 columns: down 210,
-// 88, 120; with 64 weight rows to a K-block of values 190 and 160, 138 and 97; with 128 173 and
-// 128.  So many slots of an expert take large tiles; few read little, and smaller tiles give
-// more workgroups.  Waves that share rows of y instead of K did not help (down 190): their
-// reads do not meet in the L1; nor did y by eight K of all slots, two lines to a load
-// (141; one token 16.7, not 14.7).
+// What bounds it is the weights' stream (6.0 to 6.2 TB/s from 8 tokens to 32 with 64 experts of
+// 4096 x 2048, top 8: 174 and 262 us), and beside it what every workgroup reads of x and y through its
+// L2, which costs as much a byte, as if the lines that a CU has asked for were the limit.  The
+// two products alone, 61 tokens, trial copies: 16 gates to a workgroup: up 250 us, 190 without x,
+// 200 with an x that the L1 holds; 16 columns: down 210, 88, 120; with 64 weight rows to a
+// K-block of values 190 and 160, 138 and 97; with 128 173 and 128.  So many slots of an expert
+// take large tiles; few read little, and smaller tiles give more workgroups.  Waves that share
+// rows of y instead of K did not help (down 190): their reads do not meet in the L1; nor did y by
+// eight K of all slots, two lines to a load (141; one token 16.7, not 14.7).  From about 15 slots
+// of an expert on the products of quantized activations take less time (the header has figures).
 //
 // No order depends on the other tokens: results are batch invariant.
 #include "activation.hpp"
@@ -507,15 +508,19 @@ hipError_t launch_moe_decode(const void* x, const int32_t* ids, const float* wei
   auto tiles = [&](int64_t n, int rows) { return dim3((unsigned)((n + rows - 1) / rows), (unsigned)m.candidates); };
   auto up = [&](auto kernel, int rows) { hipLaunchKernelGGL(kernel, tiles(inner, rows), threads, 0, stream, m); };
   auto down = [&](auto kernel, int rows) { hipLaunchKernelGGL(kernel, tiles(hidden, rows), threads, 0, stream, m); };
-  // By the slots of an expert, on average if every one is taken (us a call, tiles of 32, 64 and 64
-  // weight rows, the last with twice the slots a pass; 64 experts of 4096 x 2048, top 8, by tokens: 1 48.1, 48.3, 51.6;
-  // 2 65, 73, 79; 4 102, 107, 113; 8 132, 134, 140; 12 159, 156, 162; 16 181, 170, 182; 32 284, 251, 269; 61 442, 328,
-  // 329; 8 experts, top 2: 32 66, 58, 64; 61 104, 86, 78; top 4: 61 168, 129, 105).
-  // 128 weight rows halve what is read of x and y once more, but take registers for two waves a SIMD
-  // (us, 64 rows and 128: 64 experts, top 8, by tokens: 16 234, 245; 32 262, 261; 48 284, 277; 61 318, 296; 32 experts:
-  // 40 165, 155; 61 230, 206; 16 experts: 32 122, 111; 61 173, 189 (the weights come twice); 8 experts of 4096 x 14336, top
-  // 2, 61 358, 314), and fewer than two workgroups to a CU are slower (8 experts of 4096 x 2048, top 2: 24 48,
-  // 52; top 4: 61 92, 108).
+  // By the slots of an expert, on average if every one is taken.  One run, us a call in a graph, three sets of
+  // weights and choices in turn, every expert as likely; tiles of 32 weight rows (down: 32 columns), of 64 with up to
+  // two column tiles a pass, of 64 with up to four, and of 128; by tokens:
+  //   64 experts of 4096 x 2048, top 8: 1 43, 47, 48, 50; 4 115, 124, 129, 127; 8 175, 182, 189, 186; 12 202, 207,
+  //     216, 219; 16 225, 222, 233, 231; 32 284, 263, 279, 262; 48 335, 284, 306, 277; 61 405, 318, 338, 297
+  //   32, top 8: 16 148, 141, 151, 143; 40 230, 167, 188, 160; 61 351, 229, 230, 203
+  //   16, top 8: 8 81, 79, 85, 80; 16 106, 90, 98, 83; 32 181, 120, 126, 113; 61 317, 204, 172, 182 (with 128 the
+  //     weights come twice)
+  //   8, top 2: 16 48, 48, 50, 51; 32 61, 50, 56, 53; 61 86, 64, 68, 70; 128 168, 105, 92, 109
+  //   8, top 4: 61 160, 106, 92, 107; 128 299, 177, 141, 172
+  //   8 of 4096 x 14336, top 2: 16 264, 233, 245, 233; 61 544, 347, 357, 323; 128 1051, 631, 533, 538
+  // 128 weight rows halve what is read of x and y, but take registers for two waves a SIMD, and with fewer than
+  // two workgroups to a CU (8 experts of 4096 x 2048) they are slower.
   const bool few = 2 * m.slots < 3 * m.candidates, many = m.slots >= 12 * m.candidates;
   auto large = [&](int64_t tiles) {
     return m.slots >= 5 * m.candidates && m.slots < 20 * m.candidates && tiles * m.candidates >= 512;

@@ -4,9 +4,12 @@
 //   y = (h - mu) rstd gamma + beta;  codes and scales of the fp32 y, 128 columns each
 //
 // A row stays in registers between the sums (packed bf16), so x and the residual are
-// read once.  mu is taken in two steps: m = sum h / d as fp32 gives it, then
-// delta = sum (h - m) / d, so that a row far from zero (|mu| >> sigma) keeps its
-// digits: the deviation is (h - m) - delta, var = sum (h - m)^2 / d - delta^2.
+// read once.  mu is summed in 64 bits over the lanes (a lane's 8 to 32 values of eight bits in 32 bits,
+// which lose next to nothing) and held as m, mu rounded to fp32, and the rest delta, so that a row
+// far from zero (|mu| >> sigma) keeps its digits: the deviation is (h - m) - delta, var =
+// sum (h - m)^2 / d - delta^2.  (delta as the fp32 sum of h - m is no better than m alone: the differences
+// of a binade are all rounded by the same bits of m, and the mean was off by 0.3 to 0.5 x 2^-24
+// sigma on ordinary rows.)
 //
 //   backward, with xh = (h - mean) rstd and g = dy gamma:
 //   dx = rstd (g - sum g / d - xh sum (g xh) / d) [+ the residual stream's gradient]
@@ -25,7 +28,8 @@
 // to the workspace; a second launch adds the workgroups' sums in order.  The
 // grid depends on the sizes only, so results are the same bits every time.
 //
-// Bound by HBM traffic: forward 7 bytes a value (9 with y), backward 6 (8).
+// Bound by HBM traffic: forward 7 bytes a value (9 with y; 8192 x 8192 93 us, 6.5 TB/s), backward
+// 6 (8; 97 us, 5.6 TB/s); few rows by a launch and one chain of loads and sums (8 x 8192 4.3 us in a graph).
 #include "column_sum.hpp"
 #include "launch_layer.hpp"
 #include "quant_g128.hpp"
@@ -59,8 +63,49 @@ __device__ __forceinline__ float wave_sum(float v) {
   return both(__builtin_amdgcn_permlane32_swap(x, x, false, false));
 }
 
-// Two sums over a row's WPR waves, of which this is wave wk of the workgroup's wave
-// w; `lds` is not in use by another sum since the last barrier but one.
+// The same of 64-bit values: 32 bits at a time through the exchanges.
+__device__ __forceinline__ double wave_sum(double v) {
+  typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+  auto turned = [](double x, auto by) __attribute__((always_inline)) {
+    constexpr int ROW_ROR = 0x120 + decltype(by)::value;
+    const v2u w = __builtin_bit_cast(v2u, x);
+    const v2u t = {(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], ROW_ROR, 0xF, 0xF, true),
+                   (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], ROW_ROR, 0xF, 0xF, true)};
+    return x + __builtin_bit_cast(double, t);
+  };
+  v = turned(v, std::integral_constant<int, 8>());
+  v = turned(v, std::integral_constant<int, 4>());
+  v = turned(v, std::integral_constant<int, 2>());
+  v = turned(v, std::integral_constant<int, 1>());
+  auto both = [](auto low, auto high) __attribute__((always_inline)) {
+    const v2u a = {low[0], high[0]}, b = {low[1], high[1]};
+    return __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b);
+  };
+  v2u w = __builtin_bit_cast(v2u, v);
+  v = both(__builtin_amdgcn_permlane16_swap(w[0], w[0], false, false),
+           __builtin_amdgcn_permlane16_swap(w[1], w[1], false, false));
+  w = __builtin_bit_cast(v2u, v);
+  return both(__builtin_amdgcn_permlane32_swap(w[0], w[0], false, false),
+              __builtin_amdgcn_permlane32_swap(w[1], w[1], false, false));
+}
+
+// A sum over a row's WPR waves, of which this is one, wave w of the workgroup; `lds` is not in
+// use by another sum since the last barrier but one.
+template <int WPR, typename T>
+__device__ __forceinline__ T row_sum(T a, int w, T* lds) {
+  a = wave_sum(a);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) lds[w] = a;
+    __syncthreads();
+    const int first = w & ~(WPR - 1);
+    a = lds[first];
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) a += lds[first + k];
+  }
+  return a;
+}
+
+// Two sums.
 template <int WPR>
 __device__ __forceinline__ void row_sums(float& a, float& b, int w, float (*lds)[2]) {
   a = wave_sum(a);
@@ -88,16 +133,18 @@ struct LayerNorm {
   uint8_t* q;
   float *scales, *mean, *rstd;
   int64_t rows, d;
+  double inv_d;
   float eps;
 };
 
 template <int NL, int WPR, bool LINES, bool PAST>
 __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNorm p, uint32_t sets) {
   constexpr int WAVES = WPR == 8 ? 8 : 4, RPW = WAVES / WPR;  // waves and rows of a workgroup
-  __shared__ float sums[2][WAVES][2];
+  __shared__ double totals[WAVES];
+  __shared__ float squares[WAVES];
   const int lane = threadIdx.x & 63, w = wave_id_uniform(), wk = w & (WPR - 1);
   const int d = (int)p.d, nb = (d + 127) >> 7;
-  const float inv_d = 1.0f / (float)d;
+  const float inv_d = (float)p.inv_d;
   uint4 gv[NL], bv[NL];
 #pragma unroll
   for (int i = 0; i < NL; ++i) {
@@ -134,7 +181,7 @@ __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNo
         if (p.h != nullptr && row_ok && col < d) store_once<PAST>(p.h + at + col, hv[i]);
       }
     }
-    float s = 0.0f, unused = 0.0f;
+    float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       float a[8];
@@ -142,9 +189,11 @@ __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNo
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += a[j];
     }
-    row_sums<WPR>(s, unused, w, sums[0]);
-    const float m = s * inv_d;
-    float dev = 0.0f, sq = 0.0f;
+    const double total = row_sum<WPR>((double)s, w, totals);
+    double mu = total * p.inv_d;
+    mu = __builtin_fma(__builtin_fma(-mu, (double)d, total), p.inv_d, mu);  // equal values are their mean; inf: NaN
+    const float m = (float)mu, delta = (float)(mu - (double)m);
+    float sq = 0.0f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const int col = (WPR * i + wk) * 512 + lane * 8;
@@ -153,13 +202,11 @@ __global__ void __launch_bounds__(WPR == 8 ? 512 : 256) layernorm_kernel(LayerNo
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float c = col < d ? a[j] - m : 0.0f;
-        dev += c;
         sq = __builtin_fmaf(c, c, sq);
       }
     }
-    row_sums<WPR>(dev, sq, w, sums[1]);
-    const float delta = dev * inv_d;
-    const float var = __builtin_elementwise_maximum(__builtin_fmaf(-delta, delta, sq * inv_d), 0.0f);  // a NaN stays
+    sq = row_sum<WPR>(sq, w, squares) * inv_d;
+    const float var = __builtin_elementwise_maximum(__builtin_fmaf(-delta, delta, sq), 0.0f);  // a NaN stays
     const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
     if (p.mean != nullptr && row_ok && lane == 0 && wk == 0) {
       p.mean[row] = m + delta;
@@ -370,7 +417,7 @@ hipError_t launch_layernorm(const void* x, const void* residual, const void* gam
                             float* rstd, hipStream_t stream) {
   const LayerNorm p = {(const uint16_t*)x, (const uint16_t*)residual, (const uint16_t*)gamma, (const uint16_t*)beta,
                        (uint16_t*)h,       (uint16_t*)y,              (uint8_t*)q,            scales,
-                       mean,               rstd,                      rows,                   d, eps};
+                       mean,               rstd,                      rows,                   d, 1.0 / (double)d, eps};
   if (d <= 512) launch_ln<1, 1>(p, stream);
   else if (d <= 1024) launch_ln<1, 2>(p, stream);
   else if (d <= 2048) launch_ln<1, 4>(p, stream);

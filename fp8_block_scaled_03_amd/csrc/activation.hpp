@@ -7,10 +7,12 @@
 //
 // With t = |z| and phi(t) = exp(-t^2 / 2) / sqrt(2 pi):
 //   Phi(-t) = exp(-t^2 / 2) Q(t),  Q(t) = exp(t^2 / 2) erfc(t / sqrt 2) / 2,
-// and Q, which falls from 1/2 to 0.4 / t, is a polynomial of degree 8 in
-// u = 1 / (1 + 0.264 t) (fitted here to the least relative error on [0, 14.5]: 0.75 x 2^-24
-// in exact arithmetic with the coefficients as fp32 holds them, at most 9.5 x 2^-24 with fp32's
-// roundings and a reciprocal that is off by its last bit): far values keep their digits.
+// and Q, which falls from 1/2 to 0.4 / t, is for the gradient 1/2 - v r(v), v = a t / (1 + a t),
+// a = 0.28, with a polynomial r of degree 7 (fitted here to the least error on [0, 14.5], which may
+// grow as 0.3 t from t = 3 on, as t phi does, beside which Q stands: 0.15 x 2^-24 with the
+// coefficients as fp32 holds them).  Near t = 0 the 1/2 is exact, so the roundings of the polynomial and of the
+// reciprocal count by the small rest: on normal z of deviation 1.5 the slope is 0.42 x 2^-24 rms off.
+// (As u q(u), u = 1 / (1 + a t), with a polynomial of degree 8 all of Q took them: 0.6 to 0.9 x 2^-24.)
 //   gelu' = Phi(z) + z phi(z) = S for z < 0 and 1 - S else,
 //   S = exp(-t^2 / 2) (Q(t) - t / sqrt(2 pi)).
 #pragma once
@@ -57,17 +59,17 @@ __device__ __forceinline__ Sigmoid sigmoid(float g, float g_lo = 0.0f) {
 
 // Q(t), t >= 0.
 __device__ __forceinline__ float normal_tail_ratio(float t) {
-  const float u = __builtin_amdgcn_rcpf(__builtin_fmaf(t, 0.2639999985694885f, 1.0f));
-  float q = 0.030595216900110245f;
-  q = __builtin_fmaf(q, u, -0.1451054811477661f);
-  q = __builtin_fmaf(q, u, 0.22255466878414154f);
-  q = __builtin_fmaf(q, u, -0.12080366909503937f);
-  q = __builtin_fmaf(q, u, 0.14079324901103973f);
-  q = __builtin_fmaf(q, u, 0.059221748262643814f);
-  q = __builtin_fmaf(q, u, 0.10257281363010406f);
-  q = __builtin_fmaf(q, u, 0.10482796281576157f);
-  q = __builtin_fmaf(q, u, 0.10534346848726273f);
-  return q * u;
+  constexpr float A = 0.2800000011920929f;
+  const float v = t * A * __builtin_amdgcn_rcpf(__builtin_fmaf(t, A, 1.0f));
+  float r = -0.039345093071460724f;
+  r = __builtin_fmaf(r, v, 0.09880146384239197f);
+  r = __builtin_fmaf(r, v, 0.012369181960821152f);
+  r = __builtin_fmaf(r, v, -0.20192770659923553f);
+  r = __builtin_fmaf(r, v, -0.13558310270309448f);
+  r = __builtin_fmaf(r, v, 1.1047779321670532f);
+  r = __builtin_fmaf(r, v, -1.7639546394348145f);
+  r = __builtin_fmaf(r, v, 1.424793004989624f);
+  return __builtin_fmaf(-v, r, 0.5f);
 }
 
 // ---- forward, for results that are rounded to bf16: the exponentials' arguments are

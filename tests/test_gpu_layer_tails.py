@@ -1,7 +1,7 @@
-"""Sums over rows where inputs are beyond the caches: every row is in them, the first and the last rounds' among them.
+"""Sums over rows where inputs are beyond the caches: every row is in them, those of the first and the last turns too.
 
-Some rows (the first, the last, every 997th) are 2^12 times as large as the others, so that any of them would be missed: the
-test says so itself of each.  Sampled columns, against the formula in float64.  U = 2^-24.
+Some rows (the first, the last, every 997th) are 2^12 times as large as the others, so that any of them would be missed:
+the test says so itself of each.  Sampled columns, against the formula in float64.  U = 2^-24.
 
 Tolerance of dbias of an epilogue: a lane adds ceil(sets / slabs) rows of its slab, two exchanges join four rows, a
 wave of the second launch adds ceil(slabs / 16) sums and sixteen are joined; each addition rounds by U of what is
@@ -43,11 +43,11 @@ def rows_of(rows, d, seed, std=1.0):
     return out
 
 
-def enlarged(dy, where, round_rows):
-    """Makes some rows large, in place: those of the first or the last round of all workgroups and a few beside, or
+def enlarged(dy, where, turn_rows):
+    """Makes some rows large, in place: those of all workgroups' first or last turn and a few beside, or
     single ones throughout.  Their numbers."""
     rows = dy.shape[0]
-    n = min(rows, round_rows + 5)
+    n = min(rows, turn_rows + 5)
     at = {"first": np.arange(n), "last": np.arange(rows - n, rows), "spread": np.arange(0, rows, 997)}[where]
     dy[torch.from_numpy(at).to(DEV)] *= 2.0 ** 12
     return at
